@@ -51,7 +51,9 @@ typedef enum {
   FAT_ERR_ALIGNMENT = -3,      /* a tensor is not 16-byte aligned */
   FAT_ERR_LAUNCH = -4,         /* CUDA reported an error while setting up or launching */
   FAT_ERR_DEVICE_TIMEOUT = -5, /* a bounded device wait ran out (see fat_check_device_error) */
-  FAT_ERR_ARCH = -6            /* the current device is not sm_103 */
+  FAT_ERR_ARCH = -6,           /* the current device is not sm_103 */
+  FAT_ERR_INDEX = -7           /* a kernel met a page, slot or length outside the cache or the
+                                  page table (see fat_check_device_error) */
 } fat_status;
 
 typedef enum { FAT_VARIANT_TENSOR = 0, FAT_VARIANT_VEC = 1 } fat_variant;
@@ -291,14 +293,152 @@ int fat_attn_bwd(const void* q, const void* k, const void* v, const float* o, co
 /* Workspace size for fat_attn_bwd (0 for invalid arguments). */
 size_t fat_attn_bwd_workspace_bytes(int B, int H, int N);
 
+/* ------------------------------------------------------------------------
+ * Serving over a paged key-value cache
+ * ------------------------------------------------------------------------
+ * Keys and values of a pool of pages, [num_pages, heads, page_size, d], and a
+ * page table that says which page holds positions [i * page_size,
+ * (i + 1) * page_size) of which sequence.  Query heads come in groups:
+ * q_heads is a multiple of heads, and query head h reads cached head
+ * h / (q_heads / heads).
+ *
+ *  - page_size is a power of two, 16 to 1024; d is 64 or 128.
+ *  - dtype: FAT_DTYPE_BF16, FAT_DTYPE_FP16, or FAT_DTYPE_E4M3 with one scale
+ *    byte e per row (k_scale, v_scale: contiguous [num_pages, heads,
+ *    page_size]): the row's values are code * 2^(e - 127), e = 1..254; e = 255
+ *    marks a row that holds an inf or a NaN, and every element reads as NaN.
+ *  - Strides are in elements, between pages, heads and tokens (the d elements
+ *    of a row are adjacent); each is a multiple of 16 bytes.  Any order of
+ *    the three dimensions is allowed, as are k and v as parts of one tensor.
+ *  - k and v are 16-byte aligned, the scales 16-byte aligned.
+ *
+ * Indexes that live on the device (pages, lengths, slots) cannot be checked
+ * before the launch.  The kernels check them: a page outside [0, num_pages),
+ * a length below 0 or above width * page_size, or a slot beyond the cache is
+ * never used as an address; it sets FAT_ERR_INDEX for fat_check_device_error,
+ * and that sequence's (or token's) results are unspecified.  Table entries
+ * behind a sequence's last page are not read.
+ */
+typedef struct fat_kv_cache {
+  void* k;
+  void* v;
+  unsigned char* k_scale; /* e4m3 only, else ignored */
+  unsigned char* v_scale;
+  long long num_pages;
+  int heads, page_size, d;
+  int dtype; /* fat_dtype */
+  long long k_page_stride, k_head_stride, k_token_stride;
+  long long v_page_stride, v_head_stride, v_token_stride;
+} fat_kv_cache;
+
+typedef struct fat_page_table {
+  const int* pages;    /* page of position i * page_size of sequence b: pages[b * stride + i] */
+  long long stride;    /* >= width */
+  int width;           /* entries of a sequence */
+  int batch;           /* sequences */
+  const int* seq_lens; /* [batch] cached positions of each sequence (0 allowed) */
+} fat_page_table;
+
+/*
+ * Store new tokens: k, v [tokens, heads, d] (bf16 or fp16, strides in
+ * elements, rows 16-byte aligned) go to slots[t] = page * page_size + place
+ * of the cache.  slots[t] < 0 skips the token (padding).  A cache of 16-bit
+ * type takes its own type as it is.  An e4m3 cache takes either: a row's
+ * scale is the least power of two that brings its largest magnitude to at
+ * most 448 (1 for a row of zeros), so dividing by it is exact and each
+ * element is rounded once, to nearest even.  The slots of one call must
+ * differ.  tokens = 0 is allowed.
+ */
+int fat_kv_write(const fat_kv_cache* cache, const void* k, const void* v, int dtype,
+                 long long k_token_stride, long long k_head_stride, long long v_token_stride,
+                 long long v_head_stride, const long long* slots, int tokens,
+                 cudaStream_t stream);
+
+/*
+ * Read sequences back: k, v become contiguous [batch, heads, max_len, d]
+ * tensors of `dtype` (bf16 or fp16; the cache's own type unless it is e4m3),
+ * 16-byte aligned.  Rows from a sequence's length on are zeros; positions from
+ * max_len on are left out.
+ */
+int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k, void* v,
+                int dtype, int max_len, cudaStream_t stream);
+
+/*
+ * Attention of one new query token per sequence over its cached positions:
+ *     z_j = scale * q[b,h] . K_j,  o[b,h] = sum_j softmax_j(z) V_j,
+ *     lse[b,h] = ln sum_j exp(z_j),   j = 0 .. seq_lens[b] - 1.
+ * q: [batch, q_heads, d] of `dtype` (bf16 or fp16, the cache's own type
+ * unless it is e4m3), strides in elements, rows 16-byte aligned; o: contiguous
+ * [batch, q_heads, d] of the same type, rounded once; lse: fp32 [batch,
+ * q_heads].  A sequence of length 0 gives o = 0 and lse = -inf.
+ * workspace: at least fat_attn_decode_workspace_bytes(...) bytes of device
+ * memory, 16-byte aligned, any contents; calls sharing it must not overlap on
+ * the device.
+ */
+int fat_attn_decode_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                          int dtype, long long q_batch_stride, long long q_head_stride,
+                          int q_heads, float scale, void* o, float* lse, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace size for fat_attn_decode_paged (0 for invalid arguments). */
+size_t fat_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int d);
+
+/*
+ * Bounds of the keys of each block (a block is one page): bounds [num_pages,
+ * heads, 2, d], contiguous, 16-byte aligned, of `dtype` (the cache's own
+ * type; bf16 or fp16 for an e4m3 cache), holds the elementwise minimum
+ * (bounds[..., 0, :]) and maximum (bounds[..., 1, :]) of the block's keys.
+ * This call renews the blocks that hold any of the last new_tokens positions
+ * of each sequence (new_tokens >= 1; all blocks if it is at least the
+ * length), over their positions below the length; other blocks keep what
+ * they have.  A NaN key makes its bound NaN.  cache->v is not used.
+ */
+int fat_kv_block_bounds(const fat_kv_cache* cache, const fat_page_table* table, int new_tokens,
+                        void* bounds, int dtype, cudaStream_t stream);
+
+/*
+ * The score of every block of every sequence: scores[b, g, i], fp32
+ * [batch, kv_heads, width], is the largest over the query heads h of group g of
+ *     sum_c max(q[b,h,c], 0) hi_c + min(q[b,h,c], 0) lo_c,
+ * an upper bound of q . k over the block's keys, with lo and hi the bounds of
+ * the page at pages[b, i]; -inf behind the sequence's last block.  q as in
+ * fat_attn_decode_paged, of the bounds' type.
+ */
+int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
+                        long long q_head_stride, int q_heads, const void* bounds,
+                        long long num_pages, int kv_heads, int page_size, int d,
+                        const fat_page_table* table, float* scores, cudaStream_t stream);
+
+/*
+ * Attention of one new query token per sequence over chosen blocks: for each
+ * (sequence, cached head) the num_blocks blocks with the highest scores
+ * (fp32 [batch, kv_heads, width], from fat_kv_block_scores or any other
+ * source), or all if the sequence has no more.  The last last_blocks blocks
+ * (the newest tokens) and then the first first_blocks ones are taken ahead of
+ * all others; NaN counts as the highest score, and of equal ones the lower
+ * index is taken.  blocks: int32 [batch, kv_heads, num_blocks], receives the
+ * chosen block indexes in rising order, then -1.  Everything else as in
+ * fat_attn_decode_paged; workspace: fat_attn_decode_sparse_workspace_bytes.
+ */
+int fat_attn_decode_sparse(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                           int dtype, long long q_batch_stride, long long q_head_stride,
+                           int q_heads, const float* scores, int num_blocks, int first_blocks,
+                           int last_blocks, float scale, void* o, float* lse, int* blocks,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace size for fat_attn_decode_sparse (0 for invalid arguments). */
+size_t fat_attn_decode_sparse_workspace_bytes(int batch, int q_heads, int kv_heads, int d,
+                                              int num_blocks);
+
 /* Human-readable name of a fat_status value (static string). */
 const char* fat_status_string(int status);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns FAT_ERR_DEVICE_TIMEOUT if a kernel of this library
- * stopped on a bounded wait since the last check, FAT_ERR_LAUNCH if the
- * synchronisation itself failed, FAT_OK otherwise.
+ * stopped on a bounded wait since the last check, else FAT_ERR_INDEX if one
+ * met an index outside its tensor, FAT_ERR_LAUNCH if the synchronisation
+ * itself failed, FAT_OK otherwise.
  */
 int fat_check_device_error(cudaStream_t stream);
 

@@ -10,6 +10,10 @@ The operation is the fused attention flow of "FlashAttention-T: Towards Fully
 Tensorized Attention by Exploiting Tensor-Vector Parallelism" (papercache.org
 summary, section A3 / Fig. 2) with its tensorized online softmax (section A2,
 Algorithm 1); ``variant="vec"`` is the vector-softmax ablation arm.
+
+:mod:`.paged` binds the serving operators: a paged key-value cache (bf16, fp16
+or e4m3), its writing and reading, and single-token attention over it, whole or
+over the best-scored blocks.
 """
 from __future__ import annotations
 
@@ -22,9 +26,11 @@ from . import _build
 __all__ = [
     "FatError", "load_library", "attn_fwd", "attn_fwd_vec", "attn_fwd_fp8", "attn_fwd_splitkv",
     "attn_bwd", "attn_fwd_host",
+    "kv_cache_write", "kv_cache_read", "attn_decode_paged", "kv_block_bounds",
+    "kv_block_scores", "attn_decode_sparse", "attn_decode_workspace_bytes",
     "check_device_error", "status_string", "ABI_SYMBOLS", "FAT_OK",
     "FAT_ERR_INVALID_ARG", "FAT_ERR_UNSUPPORTED", "FAT_ERR_ALIGNMENT", "FAT_ERR_LAUNCH",
-    "FAT_ERR_DEVICE_TIMEOUT", "FAT_ERR_ARCH",
+    "FAT_ERR_DEVICE_TIMEOUT", "FAT_ERR_ARCH", "FAT_ERR_INDEX",
 ]
 
 FAT_OK = 0
@@ -34,6 +40,7 @@ FAT_ERR_ALIGNMENT = -3
 FAT_ERR_LAUNCH = -4
 FAT_ERR_DEVICE_TIMEOUT = -5
 FAT_ERR_ARCH = -6
+FAT_ERR_INDEX = -7
 
 VARIANTS = {"tensor": 0, "vec": 1}
 DTYPES = {"bf16": 0, "e4m3": 1, "fp16": 2}
@@ -51,6 +58,9 @@ ABI_SYMBOLS = (
     "fat_attn_fwd_splitkv_noalloc", "fat_attn_fwd_ex",
     "fat_attn_bwd", "fat_attn_bwd_workspace_bytes",
     "fat_attn_fwd_host", "fat_attn_fwd_host_workspace_bytes",
+    "fat_kv_write", "fat_kv_read", "fat_attn_decode_paged", "fat_attn_decode_workspace_bytes",
+    "fat_kv_block_bounds", "fat_kv_block_scores", "fat_attn_decode_sparse",
+    "fat_attn_decode_sparse_workspace_bytes",
     "fat_status_string", "fat_check_device_error",
 )
 
@@ -136,6 +146,7 @@ def load_library(build_if_missing: bool = True):
         lib.fat_status_string.restype = ctypes.c_char_p
         lib.fat_check_device_error.argtypes = [P]
         lib.fat_check_device_error.restype = I
+        paged.declare(lib)
         _lib = lib
         return lib
 
@@ -143,7 +154,7 @@ def load_library(build_if_missing: bool = True):
 def status_string(status: int) -> str:
     names = {0: "FAT_OK", -1: "FAT_ERR_INVALID_ARG", -2: "FAT_ERR_UNSUPPORTED",
              -3: "FAT_ERR_ALIGNMENT", -4: "FAT_ERR_LAUNCH", -5: "FAT_ERR_DEVICE_TIMEOUT",
-             -6: "FAT_ERR_ARCH"}
+             -6: "FAT_ERR_ARCH", -7: "FAT_ERR_INDEX"}
     return names.get(status, "FAT_ERR_UNKNOWN")
 
 
@@ -383,3 +394,10 @@ def raw_call(name: str, *args):
     """Call a C entry point by name with raw arguments (ABI tests)."""
     lib = load_library()
     return getattr(lib, name)(*args)
+
+
+from . import paged  # noqa: E402  (uses the names above)
+from .paged import (  # noqa: E402
+    attn_decode_paged, attn_decode_sparse, attn_decode_workspace_bytes, kv_block_bounds,
+    kv_block_scores, kv_cache_read, kv_cache_write,
+)

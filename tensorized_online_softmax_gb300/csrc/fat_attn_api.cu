@@ -19,7 +19,8 @@ namespace {
 constexpr int kMaxDevices = fat::kMaxDevices;
 
 // Device error word shared by every kernel of the library (their address is
-// passed in the kernel parameters): bit 0 = a bounded wait ran out.
+// passed in the kernel parameters): bit 0 = a bounded wait ran out, bit 1 = an
+// index outside its tensor (fat::kErrIndex).
 __device__ unsigned int g_fat_error_word = 0;
 
 struct DeviceCache {
@@ -100,6 +101,14 @@ int check_device(int* dev_out) {
 
 }  // namespace
 
+namespace fat {
+int host_device(int* dev, unsigned int** error_word) {
+  const int st = check_device(dev);
+  if (st == FAT_OK) *error_word = g_dev[*dev].error_word;
+  return st;
+}
+}  // namespace fat
+
 extern "C" {
 
 const char* fat_status_string(int status) {
@@ -111,6 +120,7 @@ const char* fat_status_string(int status) {
     case FAT_ERR_LAUNCH: return "FAT_ERR_LAUNCH";
     case FAT_ERR_DEVICE_TIMEOUT: return "FAT_ERR_DEVICE_TIMEOUT";
     case FAT_ERR_ARCH: return "FAT_ERR_ARCH";
+    case FAT_ERR_INDEX: return "FAT_ERR_INDEX";
     default: return "FAT_ERR_UNKNOWN";
   }
 }
@@ -440,7 +450,7 @@ int fat_check_device_error(cudaStream_t stream) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_fat_error_word, &zero, sizeof(zero)) != cudaSuccess)
       return FAT_ERR_LAUNCH;
-    return FAT_ERR_DEVICE_TIMEOUT;
+    return (word & ~fat::kErrIndex) ? FAT_ERR_DEVICE_TIMEOUT : FAT_ERR_INDEX;
   }
   return FAT_OK;
 }

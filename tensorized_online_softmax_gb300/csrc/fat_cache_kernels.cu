@@ -1,0 +1,263 @@
+// Writing tokens to the paged cache (quantising them on the way), reading
+// sequences back, and the bounds of the blocks' keys.  All three move each
+// byte once and do next to no arithmetic: they are bound by memory.
+#include "fat_cache.cuh"
+
+namespace fat {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// write
+// ---------------------------------------------------------------------------
+
+// Eight fp32 values of one row's lane -> eight codes and the row's scale byte.
+// kLanes lanes hold the row (a power of two, adjacent).
+//
+// The scale: the largest magnitude is m 2^E, 1 <= m < 2, and 448 = 1.75 2^8,
+// so the least power of two s with amax / s <= 448 is 2^(E - 8), or 2^(E - 7)
+// if m > 1.75.  A row below 2^-118 keeps s = 2^-126 (its byte is 1).
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t& e) {
+  uint32_t top = 0;  // magnitudes compare as integers; an inf or NaN is the largest
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int s = kLanes / 2; s > 0; s >>= 1)
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+  if (top >= 0x7F800000u) {
+    e = 255u;
+    return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  }
+  int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  b = top == 0 ? 127 : max(b, 1);
+  e = static_cast<uint32_t>(b);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // exact
+  uint2 r;
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(h[i])
+        : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
+  r.x = h[0] | (static_cast<uint32_t>(h[1]) << 16);
+  r.y = h[2] | (static_cast<uint32_t>(h[3]) << 16);
+  return r;
+}
+
+// One lane per eight elements of a row; thread -> (token, head, lane), K and V.
+template <int D, bool kE4M3, bool kBf16>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p) {
+  constexpr int kLanes = D / 8;
+  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  const int lane = static_cast<int>(i % kLanes);
+  const long long row = i / kLanes;
+  const bool in = row < static_cast<long long>(p.tokens) * p.c.heads;
+  const int t = in ? static_cast<int>(row / p.c.heads) : 0;
+  const int h = in ? static_cast<int>(row % p.c.heads) : 0;
+  const long long slot = in ? __ldg(p.slots + t) : -1;
+  const long long page = slot >> p.c.page_shift;
+  bool ok = slot >= 0;
+  if (ok && page >= p.c.num_pages) {
+    atomicOr(p.error_word, kErrIndex);
+    ok = false;
+  }
+  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+  if (ok) {
+    kx = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + lane);
+    vx = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + lane);
+  }
+  const long long place = slot & (p.c.page_size - 1);
+  uint8_t* kd = p.c.k + page * p.c.k_page + h * p.c.k_head + place * p.c.k_token;
+  uint8_t* vd = p.c.v + page * p.c.v_page + h * p.c.v_head + place * p.c.v_token;
+  if constexpr (!kE4M3) {
+    if (ok) {
+      reinterpret_cast<uint4*>(kd)[lane] = kx;
+      reinterpret_cast<uint4*>(vd)[lane] = vx;
+    }
+  } else {
+    const uint32_t kw[4] = {kx.x, kx.y, kx.z, kx.w}, vw[4] = {vx.x, vx.y, vx.z, vx.w};
+    float kf[8], vf[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = unpack16<kBf16>(kw[j]), b = unpack16<kBf16>(vw[j]);
+      kf[2 * j] = a.x, kf[2 * j + 1] = a.y;
+      vf[2 * j] = b.x, vf[2 * j + 1] = b.y;
+    }
+    uint32_t ke, ve;
+    const uint2 kc = quantise_row<kLanes>(kf, ke), vc = quantise_row<kLanes>(vf, ve);
+    if (ok) {
+      reinterpret_cast<uint2*>(kd)[lane] = kc;
+      reinterpret_cast<uint2*>(vd)[lane] = vc;
+      if (lane == 0) {
+        const long long at = (page * p.c.heads + h) * p.c.page_size + place;
+        p.c.k_scale[at] = static_cast<uint8_t>(ke);
+        p.c.v_scale[at] = static_cast<uint8_t>(ve);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// read
+// ---------------------------------------------------------------------------
+
+// Eight values of a cached row, as eight 16-bit values of the output type.
+template <bool kE4M3, bool kBf16>
+__device__ __forceinline__ uint4 read_eight(const uint8_t* row, int lane, const uint8_t* scale) {
+  if constexpr (!kE4M3) {
+    return __ldg(reinterpret_cast<const uint4*>(row) + lane);
+  } else {
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+    const float s = scale_value(__ldg(scale));
+    const uint32_t two[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+      // exact in bf16 down to its subnormals; fp16 rounds outside its range
+      r[j] = pack16<kBf16>(f.x * s, f.y * s);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+// Thread -> (position, lane) of one (sequence, head); blockIdx.y walks those.
+template <int D, bool kE4M3, bool kBf16>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
+  constexpr int kLanes = D / 8;
+  const int lane = threadIdx.x % kLanes;
+  const int n = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  if (n >= p.max_len) return;
+  const long long bh_count = static_cast<long long>(p.t.batch) * p.c.heads;
+  for (long long bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
+    const int b = static_cast<int>(bh / p.c.heads), h = static_cast<int>(bh % p.c.heads);
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (n < table_length(p.t, p.c.page_shift, b)) {
+      const long long page = table_page(p.t, p.c.num_pages, b, n >> p.c.page_shift);
+      if (page >= 0) {
+        const int place = n & (p.c.page_size - 1);
+        const long long at = (page * p.c.heads + h) * p.c.page_size + place;
+        k = read_eight<kE4M3, kBf16>(p.c.k + page * p.c.k_page + h * p.c.k_head +
+                                         place * p.c.k_token,
+                                     lane, p.c.k_scale + at);
+        v = read_eight<kE4M3, kBf16>(p.c.v + page * p.c.v_page + h * p.c.v_head +
+                                         place * p.c.v_token,
+                                     lane, p.c.v_scale + at);
+      }
+    }
+    const long long out = (bh * p.max_len + n) * kLanes + lane;
+    reinterpret_cast<uint4*>(p.k)[out] = k;
+    reinterpret_cast<uint4*>(p.v)[out] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bounds
+// ---------------------------------------------------------------------------
+
+// One block of threads per (touched block of a sequence, head); lane -> eight
+// elements, the rows shared out over the row groups and joined in shared
+// memory.
+template <int D, bool kE4M3, bool kBf16>
+__global__ void __launch_bounds__(128) kv_bounds_kernel(const BoundsParams p) {
+  constexpr int kLanes = D / 8, kGroups = 128 / kLanes;
+  __shared__ float lo_s[kGroups][D], hi_s[kGroups][D];
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int h = blockIdx.x;
+  for (int b = blockIdx.z; b < p.t.batch; b += gridDim.z) {
+    const int len = table_length(p.t, p.c.page_shift, b);
+    const int first = max(0, len - p.new_tokens) >> p.c.page_shift;
+    const int blocks = static_cast<int>((static_cast<long long>(len) + p.c.page_size - 1) >> p.c.page_shift);
+    for (int i = first + blockIdx.y; i < blocks; i += gridDim.y) {
+      const long long page = table_page(p.t, p.c.num_pages, b, i);
+      if (page < 0) continue;
+      const int rows = min(p.c.page_size, len - (i << p.c.page_shift));
+      float lo[8], hi[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lo[j] = INFINITY, hi[j] = -INFINITY;
+      for (int r = group; r < rows; r += kGroups) {
+        const uint8_t* row = p.c.k + page * p.c.k_page + h * p.c.k_head + r * p.c.k_token;
+        float x[8];
+        if constexpr (kE4M3) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+          const float s =
+              scale_value(__ldg(p.c.k_scale + (page * p.c.heads + h) * p.c.page_size + r));
+          const uint32_t two[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+            x[2 * j] = f.x * s, x[2 * j + 1] = f.y * s;
+          }
+        } else {
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack16<kBf16>(w[j]);
+            x[2 * j] = f.x, x[2 * j + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lo[j] = min_nan(lo[j], x[j]), hi[j] = max_nan(hi[j], x[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lo_s[group][lane * 8 + j] = lo[j], hi_s[group][lane * 8 + j] = hi[j];
+      __syncthreads();
+      // D / 2 pairs of columns, low then high
+      uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds) + (page * p.c.heads + h) * D;
+      for (int c = threadIdx.x; c < D; c += 128) {
+        const bool high = c >= D / 2;
+        const int col = 2 * (high ? c - D / 2 : c);
+        float a = high ? hi_s[0][col] : lo_s[0][col];
+        float z = high ? hi_s[0][col + 1] : lo_s[0][col + 1];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+          a = high ? max_nan(a, hi_s[g][col]) : min_nan(a, lo_s[g][col]);
+          z = high ? max_nan(z, hi_s[g][col + 1]) : min_nan(z, lo_s[g][col + 1]);
+        }
+        out[c] = pack16<kBf16>(a, z);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? 0 : -4; }
+
+}  // namespace
+
+int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
+  const long long threads = static_cast<long long>(p.tokens) * p.c.heads * (d / 8);
+  const unsigned grid = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+#define FAT_RUN(D, E, B) kv_write_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
+  FAT_PICK(d, e4m3, bf16, FAT_RUN);
+#undef FAT_RUN
+  return launched();
+}
+
+int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
+  const int rows = kThreads / (d / 8);
+  const long long bh = static_cast<long long>(p.t.batch) * p.c.heads;
+  const dim3 grid((p.max_len + rows - 1) / rows, static_cast<unsigned>(bh < 65535 ? bh : 65535));
+#define FAT_RUN(D, E, B) kv_read_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
+  FAT_PICK(d, e4m3, bf16, FAT_RUN);
+#undef FAT_RUN
+  return launched();
+}
+
+int launch_kv_bounds(const BoundsParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
+  // blocks that new_tokens adjacent positions can touch
+  long long most = (static_cast<long long>(p.new_tokens) - 1 + p.c.page_size - 1) / p.c.page_size + 1;
+  if (most > p.t.width) most = p.t.width;
+  const dim3 grid(p.c.heads, static_cast<unsigned>(most < 65535 ? most : 65535),
+                  p.t.batch < 65535 ? p.t.batch : 65535);
+#define FAT_RUN(D, E, B) kv_bounds_kernel<D, E, B><<<grid, 128, 0, stream>>>(p)
+  FAT_PICK(d, e4m3, bf16, FAT_RUN);
+#undef FAT_RUN
+  return launched();
+}
+
+}  // namespace fat

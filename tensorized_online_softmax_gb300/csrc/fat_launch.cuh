@@ -12,6 +12,11 @@
 namespace fat {
 
 constexpr int kMaxDevices = 64;
+constexpr unsigned int kErrIndex = 2;  // the error word's bit for an index out of range
+
+// The current device's number and error word, or the fat_status code that
+// refuses it (fat_attn_api.cu).
+int host_device(int* dev, unsigned int** error_word);
 
 // Returns 0 or the fat_status code FAT_ERR_LAUNCH (-4).
 template <int D, int kX, bool kLTensor, int kDt, bool kZT = false>

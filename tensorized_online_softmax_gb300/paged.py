@@ -1,0 +1,392 @@
+"""Serving over a paged key-value cache: the binding of the ``fat_kv_*`` and
+``fat_attn_decode_*`` entry points of ``include/fat_attn.h``.
+
+The cache is two tensors ``k_cache, v_cache`` of shape ``[num_pages, heads,
+page_size, d]`` (any order of the first three dimensions in memory: pass a
+transposed view), bf16, fp16 or ``torch.float8_e4m3fn``; an e4m3 cache has one
+scale byte per row beside it, ``k_scale, v_scale``: contiguous uint8
+``[num_pages, heads, page_size]``, the row's values being
+``code * 2**(byte - 127)`` and 255 marking a row with an inf or NaN.
+``page_table`` (int32 ``[B, width]``) gives the page of positions
+``[i * page_size, (i + 1) * page_size)`` of each sequence, ``seq_lens`` (int32
+``[B]``) the sequences' lengths.  Both live on the device, so a page or length
+out of range cannot be refused here: the kernels skip it, and
+:func:`check_device_error` then returns ``FAT_ERR_INDEX``.
+
+Every call is asynchronous on ``stream`` (default: torch's current stream of
+the tensors' device), and allocates its outputs and workspace unless they are
+given.  A given workspace must not be shared by calls that overlap.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import DTYPES, FAT_OK, FatError, load_library
+
+_P, _I, _L, _F, _Z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
+                      ctypes.c_size_t)
+
+
+class FatKvCache(ctypes.Structure):
+    """Mirror of ``fat_kv_cache`` in include/fat_attn.h (same field order)."""
+    _fields_ = [
+        ("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P),
+        ("num_pages", _L), ("heads", _I), ("page_size", _I), ("d", _I), ("dtype", _I),
+        ("k_page_stride", _L), ("k_head_stride", _L), ("k_token_stride", _L),
+        ("v_page_stride", _L), ("v_head_stride", _L), ("v_token_stride", _L),
+    ]
+
+
+class FatPageTable(ctypes.Structure):
+    """Mirror of ``fat_page_table`` in include/fat_attn.h (same field order)."""
+    _fields_ = [("pages", _P), ("stride", _L), ("width", _I), ("batch", _I), ("seq_lens", _P)]
+
+
+def declare(lib) -> None:
+    """Argument and result types of the entry points used here."""
+    cache, table = ctypes.POINTER(FatKvCache), ctypes.POINTER(FatPageTable)
+    query = [_P, _I, _L, _L, _I]
+    for name, args, result in (
+            ("fat_kv_write", [cache, _P, _P, _I, _L, _L, _L, _L, _P, _I, _P], _I),
+            ("fat_kv_read", [cache, table, _P, _P, _I, _I, _P], _I),
+            ("fat_attn_decode_paged", [cache, table, *query, _F, _P, _P, _P, _Z, _P], _I),
+            ("fat_attn_decode_workspace_bytes", [_I, _I, _I, _I], _Z),
+            ("fat_kv_block_bounds", [cache, table, _I, _P, _I, _P], _I),
+            ("fat_kv_block_scores", [*query, _P, _L, _I, _I, _I, table, _P, _P], _I),
+            ("fat_attn_decode_sparse",
+             [cache, table, *query, _P, _I, _I, _I, _F, _P, _P, _P, _P, _Z, _P], _I),
+            ("fat_attn_decode_sparse_workspace_bytes", [_I, _I, _I, _I, _I], _Z)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, result
+
+
+_WIDE = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
+_CACHE = {**_WIDE, torch.float8_e4m3fn: DTYPES["e4m3"]}
+_HERE = contextlib.nullcontext()
+
+
+def _strides(t, dims):
+    """Strides of `dims` in elements; a dimension of one entry has none that matters."""
+    return [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
+
+
+def _tensor(name, t, dtypes, dim, device=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, writable=False):
+    """The checked cache as a struct; v_cache None where only the keys are read."""
+    _tensor("k_cache", k_cache, _CACHE, 4)
+    pages, heads, page_size, d = k_cache.shape
+    c = FatKvCache(k=k_cache.data_ptr(), num_pages=pages, heads=heads, page_size=page_size, d=d,
+                   dtype=_CACHE[k_cache.dtype])
+    c.k_page_stride, c.k_head_stride, c.k_token_stride = _strides(k_cache, (0, 1, 2))
+    parts = [("k", k_cache, k_scale)]
+    if v_cache is not None:
+        _tensor("v_cache", v_cache, (k_cache.dtype,), 4, k_cache.device)
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must have the same shape")
+        c.v = v_cache.data_ptr()
+        c.v_page_stride, c.v_head_stride, c.v_token_stride = _strides(v_cache, (0, 1, 2))
+        parts.append(("v", v_cache, v_scale))
+    for name, t, scale in parts:
+        if t.stride(3) != 1:
+            raise ValueError(f"the rows of {name}_cache must be contiguous")
+        if writable and any(t.shape[i] > 1 and t.stride(i) == 0 for i in range(3)):
+            raise ValueError(f"{name}_cache is a broadcast view: its rows share memory")
+        if t.dtype is torch.float8_e4m3fn:
+            if scale is None:
+                raise ValueError(f"an e4m3 cache needs {name}_scale")
+            _tensor(f"{name}_scale", scale, (torch.uint8,), 3, k_cache.device)
+            if scale.shape != (pages, heads, page_size) or not scale.is_contiguous():
+                raise ValueError(f"{name}_scale must be contiguous [num_pages, heads, page_size]")
+            setattr(c, name + "_scale", scale.data_ptr())
+        elif scale is not None:
+            raise ValueError(f"{name}_scale goes with an e4m3 cache only")
+    return c
+
+
+def _table(page_table, seq_lens, device):
+    _tensor("page_table", page_table, (torch.int32,), 2, device)
+    _tensor("seq_lens", seq_lens, (torch.int32,), 1, device)
+    batch, width = page_table.shape
+    if seq_lens.shape[0] != batch or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous [B], page_table [B, width]")
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    return FatPageTable(page_table.data_ptr(), page_table.stride(0) if batch > 1 else width, width,
+                        batch, seq_lens.data_ptr())
+
+
+def _query(q, batch, heads, d, device):
+    """q [B, Hq, d] -> its pointer, type, strides and head count as C arguments."""
+    _tensor("q", q, _WIDE, 3, device)
+    if q.shape[0] != batch or q.shape[2] != d or q.shape[1] < 1 or q.shape[1] % heads:
+        raise ValueError(f"q must be [{batch}, a multiple of {heads}, {d}], "
+                         f"not {list(q.shape)}")
+    if q.stride(2) != 1:
+        raise ValueError("the rows of q must be contiguous")
+    return (q.data_ptr(), _WIDE[q.dtype], *_strides(q, (0, 1)), q.shape[1])
+
+
+def _output(name, t, shape, dtype, device):
+    _tensor(name, t, (dtype,), len(shape), device)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)}")
+    return t
+
+
+def _on(device):
+    """The device as the current one, for the launch."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _stream(stream, device, fresh):
+    """The stream's handle; tensors allocated by this call are kept for a stream that is not the
+    one they were allocated on."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    for t in fresh:
+        t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _done(status, what):
+    if status != FAT_OK:
+        raise FatError(status, what)
+
+
+def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
+                   stream=None) -> None:
+    """Store new tokens in a paged cache, quantising them if it is e4m3.
+
+    ``k, v``: [T, heads, d], bf16 or fp16 (the cache's own type unless it is
+    e4m3); strided views are fine if every row starts on 16 bytes.  ``slots``:
+    int64 [T], ``page * page_size + place`` of each token; a negative slot
+    skips the token.  The slots of one call must differ.  An e4m3 row gets the
+    least power of two as its scale that brings its largest magnitude to at
+    most 448.
+    """
+    lib = load_library()
+    c = _cache(k_cache, v_cache, k_scale, v_scale, writable=True)
+    device = k_cache.device
+    _tensor("k", k, _WIDE, 3, device)
+    _tensor("v", v, (k.dtype,), 3, device)
+    _tensor("slots", slots, (torch.int64,), 1, device)
+    tokens = slots.shape[0]
+    if k.shape != (tokens, c.heads, c.d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{tokens}, {c.heads}, {c.d}]")
+    if c.dtype != DTYPES["e4m3"] and k.dtype != k_cache.dtype:
+        raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} tokens, not {k.dtype}")
+    if tokens == 0:
+        return
+    if k.stride(2) != 1 or v.stride(2) != 1 or not slots.is_contiguous():
+        raise ValueError("the rows of k and v, and slots, must be contiguous")
+    with _on(device):
+        _done(lib.fat_kv_write(c, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype],
+                               *_strides(k, (0, 1)), *_strides(v, (0, 1)), slots.data_ptr(),
+                               tokens, _stream(stream, device, ())), "fat_kv_write")
+
+
+def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype=None,
+                  k_scale=None, v_scale=None, out=None, stream=None):
+    """Read cached sequences back: ``(k, v)``, contiguous [B, heads, max_len, d].
+
+    ``dtype``: bf16 or fp16; the cache's own type (the default) unless it is
+    e4m3 (default bf16).  Rows from a sequence's length on are zeros.
+    """
+    lib = load_library()
+    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    device = k_cache.device
+    t = _table(page_table, seq_lens, device)
+    if dtype is None:
+        dtype = torch.bfloat16 if c.dtype == DTYPES["e4m3"] else k_cache.dtype
+    if dtype not in _WIDE or (c.dtype != DTYPES["e4m3"] and dtype != k_cache.dtype):
+        raise ValueError(f"a {k_cache.dtype} cache is not read as {dtype}")
+    shape = (t.batch, c.heads, int(max_len), c.d)
+    if shape[2] < 1:
+        raise ValueError("max_len must be at least 1")
+    fresh = ()
+    if out is None:
+        fresh = out = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+    k, v = (_output(n, x, shape, dtype, device) for n, x in zip(("k", "v"), out))
+    with _on(device):
+        _done(lib.fat_kv_read(c, t, k.data_ptr(), v.data_ptr(), _WIDE[dtype], shape[2],
+                              _stream(stream, device, fresh)), "fat_kv_read")
+    return k, v
+
+
+def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out):
+    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    device = k_cache.device
+    t = _table(page_table, seq_lens, device)
+    query = _query(q, t.batch, c.heads, c.d, device)
+    if c.dtype != DTYPES["e4m3"] and q.dtype != k_cache.dtype:
+        raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} queries, not {q.dtype}")
+    shape = q.shape
+    fresh = []
+    if out is None:
+        o = torch.empty(shape, dtype=q.dtype, device=device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
+        fresh += [o, lse]
+    else:
+        o = _output("o", out[0], shape, q.dtype, device)
+        lse = _output("lse", out[1], shape[:2], torch.float32, device)
+    return c, t, query, c.d ** -0.5 if scale is None else float(scale), o, lse, fresh
+
+
+def _workspace(workspace, nbytes, device, fresh):
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        fresh.append(workspace)
+        return workspace
+    _tensor("workspace", workspace, (torch.uint8,), 1, device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale: float | None = None, *,
+                      k_scale=None, v_scale=None, workspace=None, out=None, stream=None):
+    """Attention of one new query token per sequence over its cached positions.
+
+    ``q``: [B, q_heads, d], bf16 or fp16 (the cache's own type unless it is
+    e4m3), ``q_heads`` a multiple of the cached heads.  ``scale`` defaults to
+    1/sqrt(d).  Returns ``(o, lse)``: o of q's shape and type, lse fp32
+    [B, q_heads]; a sequence of length 0 gives zeros and -inf.  ``workspace``:
+    a CUDA uint8 tensor of :func:`attn_decode_workspace_bytes` bytes.
+    """
+    lib = load_library()
+    c, t, query, scale, o, lse, fresh = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out)
+    nbytes = lib.fat_attn_decode_workspace_bytes(t.batch, q.shape[1], c.heads, c.d)
+    workspace = _workspace(workspace, nbytes, q.device, fresh)
+    with _on(q.device):
+        _done(lib.fat_attn_decode_paged(c, t, *query, scale, o.data_ptr(), lse.data_ptr(),
+                                        workspace.data_ptr(), workspace.numel(),
+                                        _stream(stream, q.device, fresh)),
+              "fat_attn_decode_paged")
+    return o, lse
+
+
+def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | None = None, *,
+                    k_scale=None, stream=None):
+    """Renew the bounds of the blocks (pages) that hold the newest positions.
+
+    ``bounds``: contiguous [num_pages, heads, 2, d] (the cache's type; bf16 or
+    fp16 for an e4m3 cache), the elementwise minimum and maximum of each
+    block's keys.  The blocks with any of the last ``new_tokens`` positions of
+    a sequence are computed anew (all of them if None); the others keep what
+    they have.  Returns ``bounds``.
+    """
+    lib = load_library()
+    c = _cache(k_cache, None, k_scale, None)
+    device = k_cache.device
+    t = _table(page_table, seq_lens, device)
+    dtypes = _WIDE if c.dtype == DTYPES["e4m3"] else (k_cache.dtype,)
+    _tensor("bounds", bounds, dtypes, 4, device)
+    _output("bounds", bounds, (c.num_pages, c.heads, 2, c.d), bounds.dtype, device)
+    new_tokens = 0x7fffffff if new_tokens is None else int(new_tokens)
+    if not 1 <= new_tokens <= 0x7fffffff:
+        raise ValueError("new_tokens must be at least 1")
+    with _on(device):
+        _done(lib.fat_kv_block_bounds(c, t, new_tokens, bounds.data_ptr(), _WIDE[bounds.dtype],
+                                      _stream(stream, device, ())), "fat_kv_block_bounds")
+    return bounds
+
+
+def kv_block_scores(q, bounds, page_table, seq_lens, page_size: int, *, out=None, stream=None):
+    """Score every block of every sequence for :func:`attn_decode_sparse`.
+
+    ``q``: [B, q_heads, d] of the type of ``bounds`` (see
+    :func:`kv_block_bounds`).  Returns fp32 [B, heads, width]: the largest, over
+    the query heads that share a cached head, of an upper bound on q . k over
+    the block's keys; -inf behind a sequence's last block.
+    """
+    lib = load_library()
+    _tensor("bounds", bounds, _WIDE, 4)
+    device = bounds.device
+    pages, heads, two, d = bounds.shape
+    if two != 2 or not bounds.is_contiguous():
+        raise ValueError("bounds must be contiguous [num_pages, heads, 2, d]")
+    t = _table(page_table, seq_lens, device)
+    query = _query(q, t.batch, heads, d, device)
+    if q.dtype != bounds.dtype:
+        raise ValueError("q and bounds must have the same type")
+    shape = (t.batch, heads, t.width)
+    fresh = ()
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=device)
+        fresh = (out,)
+    scores = _output("out", out, shape, torch.float32, device)
+    with _on(device):
+        _done(lib.fat_kv_block_scores(*query, bounds.data_ptr(), pages, heads, int(page_size), d,
+                                      t, scores.data_ptr(), _stream(stream, device, fresh)),
+              "fat_kv_block_scores")
+    return scores
+
+
+def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_blocks: int,
+                       scale: float | None = None, *, first_blocks: int = 0,
+                       last_blocks: int = 1, k_scale=None, v_scale=None, workspace=None,
+                       out=None, stream=None):
+    """Attention of one new query token per sequence over its best blocks.
+
+    ``scores``: contiguous fp32 [B, heads, width], from :func:`kv_block_scores`
+    or any other source.  Each (sequence, cached head) takes the
+    ``num_blocks`` blocks (pages) with the highest scores, all if it has no
+    more: the last ``last_blocks`` and the first ``first_blocks`` ahead of all
+    others (together at most ``num_blocks``), NaN as the highest score, the
+    lower index of equal ones.  Returns ``(o, lse, blocks)``: o and lse as in
+    :func:`attn_decode_paged`, over the chosen blocks; blocks int32 [B, heads,
+    num_blocks], the choice in rising order, then -1.  ``out``: optional
+    ``(o, lse, blocks)``.
+    """
+    lib = load_library()
+    c, t, query, scale, o, lse, fresh = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out)
+    device = q.device
+    num_blocks = int(num_blocks)
+    if num_blocks < 1 or first_blocks < 0 or last_blocks < 0 or \
+            first_blocks + last_blocks > num_blocks:
+        raise ValueError("num_blocks must be at least 1 and at least first_blocks + last_blocks")
+    _tensor("scores", scores, (torch.float32,), 3, device)
+    _output("scores", scores, (t.batch, c.heads, t.width), torch.float32, device)
+    shape = (t.batch, c.heads, num_blocks)
+    if out is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=device)
+        fresh.append(blocks)
+    else:
+        blocks = _output("blocks", out[2], shape, torch.int32, device)
+    nbytes = lib.fat_attn_decode_sparse_workspace_bytes(t.batch, q.shape[1], c.heads, c.d,
+                                                        num_blocks)
+    workspace = _workspace(workspace, nbytes, device, fresh)
+    with _on(device):
+        _done(lib.fat_attn_decode_sparse(
+            c, t, *query, scores.data_ptr(), num_blocks, int(first_blocks), int(last_blocks),
+            scale, o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream(stream, device, fresh)), "fat_attn_decode_sparse")
+    return o, lse, blocks
+
+
+def attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, d: int,
+                                num_blocks: int | None = None) -> int:
+    """Workspace size of :func:`attn_decode_paged`, or with ``num_blocks`` of
+    :func:`attn_decode_sparse` (0 for invalid arguments)."""
+    lib = load_library()
+    if num_blocks is None:
+        return lib.fat_attn_decode_workspace_bytes(batch, q_heads, kv_heads, d)
+    return lib.fat_attn_decode_sparse_workspace_bytes(batch, q_heads, kv_heads, d, num_blocks)
