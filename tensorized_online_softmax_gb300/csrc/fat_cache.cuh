@@ -169,6 +169,7 @@ struct DecodeParams {
   uint8_t* o;
   float* lse;
   void* workspace;
+  int least_tiles;            // tiles that a thread block takes at least
 };
 // what launch_decode needs, whatever the batch
 size_t decode_workspace_bytes(int d);

@@ -155,6 +155,7 @@ static int decode_common(const fat_kv_cache* cache, const fat_page_table* table,
   if (!(scale > 0.f) || !std::isfinite(scale) || !o || !lse) return FAT_ERR_INVALID_ARG;
   if (!aligned(o, 16) || !aligned(lse, 4)) return FAT_ERR_ALIGNMENT;
   p->batch = table->batch;
+  p->least_tiles = 2;
   p->q = static_cast<const uint8_t*>(q);
   p->group = q_heads / cache->heads;
   p->scale_log2 = scale * kLog2e;

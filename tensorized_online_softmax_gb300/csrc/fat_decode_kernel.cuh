@@ -1,0 +1,688 @@
+// Attention of one query token per sequence over the paged cache.
+//
+// What bounds it: every cached byte is used once, by the few query heads of its
+// group, so the kernel is a stream through HBM; all else has to stay below it.
+//
+// Work: fat_decode_plan.h.  Each of a block's four warps takes 16 positions of
+// every 64-position tile through a ring of its own in shared memory, filled by
+// 16-byte asynchronous copies several tiles ahead (a ring per warp needs no
+// barrier between warps; 16 positions never straddle two pages).  Rows behind
+// the length are filled with zeros, not read.
+//
+// Arithmetic per 16 positions, on m16n8k16 MMAs with the positions as rows, so
+// that a group of up to 8 query heads (kNT = 1; 16: kNT = 2) fills the columns:
+//     S[16, heads] = K Q^T,   z = scale log2(e) S   (-inf behind the length)
+//     p = 2^(z - r),  l += p,   O^T[d, heads] += V^T P^T
+// r is a running reference for each head, raised to the running maximum only
+// when a score exceeds it by more than 8 binades, so the usual tile needs one
+// vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
+// the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and the only
+// rounding that counts is that of the output.
+//
+// e4m3 caches: the codes become fp16 exactly, the keys' scales multiply S, and
+// the values' scales join the weights, w = 2^(z + log2 s - r'), with a running
+// reference r' of its own: fp16 weights keep their precision relative to the
+// largest weighted row whatever the scales are.  q is brought into fp16's range
+// by a power of two for each head.
+//
+// The warps' (r, r', l, O) are joined through shared memory at an item's end;
+// an item that other blocks share leaves a normalised O and its LSE in the
+// workspace for the join kernel, in a fixed order: the result does not depend
+// on timing.
+#pragma once
+
+#include "fat_cache.cuh"
+#include "fat_decode_plan.h"
+#include "sm103_ptx.cuh"
+
+namespace fat {
+
+namespace decode {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRowsPerWarp = kDecodeTile / kWarps;  // 16
+static_assert(kRowsPerWarp == 16, "one MMA tile of positions to a warp");
+constexpr float kRaise = 8.f;  // binades above the reference that are let pass
+
+struct Join {  // what the join kernel needs of the item that starts, unfinished, in a block
+  int entry, item;
+  int last;  // the last block with a part of it; -1: nothing to join
+  int part;  // where the first block keeps its part
+};
+
+// workspace: Join[kDecodeMaxBlocks], then for each block and part the LSEs
+// (log2) of up to 16 rows, then the rows
+constexpr int kMaxRows = 16;
+constexpr size_t kJoinBytes = sizeof(Join) * kDecodeMaxBlocks;
+constexpr size_t kLseBytes = sizeof(float) * kDecodeMaxBlocks * 2 * kMaxRows;
+
+template <int D, int kNT, bool kE4M3>
+struct Layout {
+  static constexpr int kRow = D * (kE4M3 ? 1 : 2);  // bytes
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kStage = 2 * kRowsPerWarp * kRow;  // K and V of 16 positions
+  // about 24 KiB a warp: two blocks of an SM hold 192 KiB in flight
+  static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 6 : 8;
+  static constexpr int kScales = kE4M3 ? 32 : 0;
+  static constexpr int kRing = kStages * (kStage + kScales);  // of one warp
+  static constexpr int kPitch = D + 4;  // floats: spreads the heads over the banks
+  static constexpr int kJoinO = kWarps * 8 * kPitch * 4;
+  static constexpr int kJoinRows = 3 * kWarps * kMaxRows * 4;
+  static constexpr int kSmem = kWarps * kRing + kJoinO + kJoinRows;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (kBf16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two weights rounded down to 16 bits, strictly below the weight itself, so that
+// the remainder is positive: with an infinite value both products have its sign
+// (a remainder of zero or of the other sign would make their sum a NaN).
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_below(float a, float b) {
+  constexpr float kLess = 1.f - 0x1p-10f;  // less than a step of either type away
+  a *= kLess;
+  b *= kLess;
+  uint32_t r;
+  if constexpr (kBf16)
+    r = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  else
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// The byte offset of 16-byte chunk c of row r in a stage: chunks are permuted
+// within a row so that eight rows' worth of one chunk meet no bank twice.
+template <int kChunks>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (kChunks >= 8)
+    return static_cast<uint32_t>(r * kChunks + (c ^ (r & 7))) * 16u;
+  else
+    return static_cast<uint32_t>(r * kChunks + (c ^ ((r >> 1) & 3))) * 16u;
+}
+
+// Inclusive prefix sum over the block's threads.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,
+                                                long long& total) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) x += warp_sums[w];
+    total += warp_sums[w];
+  }
+  return x;
+}
+
+// A walk along the line of tiles, with the current entry's length and page.
+struct Walk {
+  DecodePlace at;
+  int len;
+  __device__ __forceinline__ void enter(const DecodeParams& p) {
+    len = table_length(p.t, p.c.page_shift, at.entry);
+    at.tiles = decode_tiles(len);
+  }
+};
+
+template <int D, int kNT, bool kE4M3, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
+  using L = Layout<D, kNT, kE4M3>;
+  constexpr bool kMmaBf16 = kBf16 && !kE4M3;
+  constexpr int kR = 8 * kNT;  // query heads of a block of rows
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long warp_sums[kWarps];
+  __shared__ DecodePlace start_s;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, t = lane % 4;
+  float* join_o = reinterpret_cast<float*>(smem + kWarps * L::kRing);
+  float* join_r = join_o + kWarps * 8 * L::kPitch;  // [3][warp][kMaxRows]: r, r', l
+
+  grid_dep_launch();
+  grid_dep_wait();
+
+  // ---- the block's share ----
+  const int blocks_of_rows = (p.group + kR - 1) / kR;
+  const int heads_per_entry = p.per_head ? 1 : p.c.heads;
+  const int copies = heads_per_entry * blocks_of_rows;
+  long long begin, share, total;
+  {
+    const int entries = p.t.batch;
+    const int each = (entries + kThreads - 1) / kThreads;
+    const int lo = threadIdx.x * each, hi = min(entries, lo + each);
+    long long mine = 0;
+    for (int e = lo; e < hi; ++e) mine += decode_tiles(table_length(p.t, p.c.page_shift, e));
+    const long long upto = block_scan(mine, warp_sums, total);
+    total *= copies;
+    share = decode_share(total, gridDim.x, p.least_tiles);
+    begin = blockIdx.x * share;
+    long long before = (upto - mine) * copies;
+    if (begin >= before && begin < upto * copies) {
+      for (int e = lo; e < hi; ++e) {
+        const int tiles = decode_tiles(table_length(p.t, p.c.page_shift, e));
+        const long long n = static_cast<long long>(tiles) * copies;
+        if (begin < before + n) {
+          start_s = decode_place(e, begin - before, tiles);
+          break;
+        }
+        before += n;
+      }
+    }
+    __syncthreads();
+  }
+  Join* joins = static_cast<Join*>(p.workspace);
+  if (threadIdx.x == 0) joins[blockIdx.x].last = -1;
+  if (begin >= total) return;
+  const long long end = min(total, begin + share);
+  const int count = static_cast<int>(end - begin);
+
+  // ---- the copies, ahead of the arithmetic ----
+  const uint32_t ring = smem_u32(smem) + warp * L::kRing;
+  Walk load;
+  load.at = start_s;
+  load.enter(p);
+  auto first_row = [&](const Walk& w) { return w.at.tile * kDecodeTile + warp * kRowsPerWarp; };
+  auto page_of = [&](const Walk& w) -> long long {
+    const int row = first_row(w);
+    return row < w.len ? table_page(p.t, p.c.num_pages, w.at.entry, row >> p.c.page_shift) : -1;
+  };
+  long long page = page_of(load);
+  int loaded = 0;
+  auto issue = [&]() {
+    const int row = first_row(load);
+    if (row < load.len) {
+      const int h = (p.per_head ? load.at.entry % p.c.heads : 0) + load.at.item / blocks_of_rows;
+      const uint32_t stage = ring + (loaded % L::kStages) * (L::kStage + L::kScales);
+      const int place = row & (p.c.page_size - 1);
+      const int valid = page < 0 ? 0 : min(kRowsPerWarp, load.len - row);
+      const long long at = max(page, 0ll);
+      const uint8_t* k = p.c.k + at * p.c.k_page + h * p.c.k_head + place * p.c.k_token;
+      const uint8_t* v = p.c.v + at * p.c.v_page + h * p.c.v_head + place * p.c.v_token;
+      constexpr int kPer = kRowsPerWarp * L::kChunks / 32;  // chunks of K to a lane
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = (i * 32 + lane) / L::kChunks, c = (i * 32 + lane) % L::kChunks;
+        const uint32_t bytes = r < valid ? 16u : 0u;
+        const int from = r < valid ? r : 0;
+        copy16(stage + chunk_at<L::kChunks>(r, c), k + from * p.c.k_token + c * 16, bytes);
+        copy16(stage + L::kStage / 2 + chunk_at<L::kChunks>(r, c),
+               v + from * p.c.v_token + c * 16, bytes);
+      }
+      if constexpr (kE4M3) {
+        if (lane < 2) {
+          const uint8_t* s = (lane == 0 ? p.c.k_scale : p.c.v_scale) +
+                             ((at * p.c.heads + h) * p.c.page_size + place);
+          copy16(stage + L::kStage + lane * 16, s, page < 0 ? 0u : 16u);
+        }
+      }
+    }
+    ++loaded;
+    if (loaded < count) {
+      if (decode_advance(load.at, copies)) load.enter(p);
+      page = page_of(load);  // used by the next issue(): its latency is hidden
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < L::kStages - 1; ++i) {
+    if (loaded < count) issue();
+    copy_commit();
+  }
+
+  // ---- the arithmetic ----
+  Walk cur;
+  cur.at = start_s;
+  cur.enter(p);
+  long long first_tile = begin - cur.at.tile;  // of the current item
+  uint32_t qf[D / 16][kNT][2];
+  float factor[kNT][2];            // of the scores, by column
+  float o[D / 16][kNT][4];
+  float ref[kNT][2], ref_v[kNT][2], sum[kNT][2];
+  bool fresh = true;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    if (loaded < count) issue();
+    copy_commit();
+    const int seq = p.per_head ? cur.at.entry / p.c.heads : cur.at.entry;
+    const int head =
+        (p.per_head ? cur.at.entry % p.c.heads : 0) + cur.at.item / blocks_of_rows;
+    const int row0 = (cur.at.item % blocks_of_rows) * kR;  // first query head of the group
+    if (fresh) {
+      fresh = false;
+      const uint8_t* q0 = p.q + seq * p.q_batch + (head * p.group + row0) * p.q_head;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const bool in = row0 + n * 8 + g < p.group;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(q0 + (n * 8 + (in ? g : 0)) * p.q_head);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          // the columns of K that this lane's fragment multiplies: 2t, 2t + 1 and 2t + 8, 2t + 9
+          // of each 16, or for e4m3 (four codes to a word) 4t .. 4t + 3
+          qf[s][n][0] = in ? __ldg(q + s * 8 + (kE4M3 ? 2 * t : t)) : 0u;
+          qf[s][n][1] = in ? __ldg(q + s * 8 + (kE4M3 ? 2 * t + 1 : t + 4)) : 0u;
+        }
+        if constexpr (kE4M3) {
+          float top = 0.f;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 f = unpack16<kBf16>(qf[s][n][j]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // largest magnitude into [1, 2) (a row with an infinity stays as it is)
+          const uint32_t e = top > 0.f && top < INFINITY
+                                 ? min(max(__float_as_uint(top) >> 23, 1u), 253u)
+                                 : 127u;
+          const float down = __uint_as_float((254u - e) << 23);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 f = unpack16<kBf16>(qf[s][n][j]);
+              qf[s][n][j] = pack16<false>(f.x * down, f.y * down);
+            }
+          const float up = __uint_as_float(e << 23) * p.scale_log2;
+          factor[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
+          factor[n][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+        } else {
+          factor[n][0] = factor[n][1] = p.scale_log2;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ref[n][j] = ref_v[n][j] = -INFINITY;
+          sum[n][j] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[c][n][j] = 0.f;
+      }
+    }
+    copy_wait<L::kStages - 1>();
+    __syncwarp();
+    const int row = first_row(cur);
+    if (row < cur.len) {
+      const uint32_t stage = ring + (i % L::kStages) * (L::kStage + L::kScales);
+      const int mat = lane / 8, mr = lane % 8;
+      // S = K Q^T, in two chains
+      float s0[kNT][4], s1[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s0[n][j] = s1[n][j] = 0.f;
+      {
+        const int r = mr + (mat & 1) * 8;
+#pragma unroll
+        for (int s = 0; s < L::kChunks / 2; ++s) {
+          uint32_t a[4];
+          ldsm4(a, stage + chunk_at<L::kChunks>(r, 2 * s + (mat >> 1)));
+          if constexpr (!kE4M3) {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              mma<kMmaBf16>(s & 1 ? s1[n] : s0[n], a, qf[s][n][0], qf[s][n][1]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t f[4] = {e4m3x2_to_f16x2(a[2 * x]), e4m3x2_to_f16x2(a[2 * x + 1]),
+                                     e4m3x2_to_f16x2(a[2 * x] >> 16),
+                                     e4m3x2_to_f16x2(a[2 * x + 1] >> 16)};
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+                mma<false>(x ? s1[n] : s0[n], f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
+            }
+          }
+        }
+      }
+      float ks[2] = {1.f, 1.f}, vs[2] = {0.f, 0.f};
+      const bool in[2] = {row + g < cur.len, row + g + 8 < cur.len};
+      if constexpr (kE4M3) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = stage + L::kStage + g + 8 * j;
+          uint32_t ke, ve;
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ke) : "r"(at) : "memory");
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ve) : "r"(at + 16) : "memory");
+          ks[j] = scale_value(ke);
+          vs[j] = ve == 255u ? __uint_as_float(0x7FFFFFFFu) : static_cast<float>(ve) - 127.f;
+        }
+      }
+      float z[kNT][4], zv[kNT][4];
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rr = j >> 1, cc = j & 1;
+          const float s = s0[n][j] + s1[n][j];
+          z[n][j] = in[rr] ? s * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]) : -INFINITY;
+          raise |= z[n][j] > ref[n][cc] + kRaise;
+          if constexpr (kE4M3) {
+            zv[n][j] = in[rr] ? z[n][j] + vs[rr] : -INFINITY;
+            raise |= zv[n][j] > ref_v[n][cc] + kRaise;
+          }
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float m = fmaxf(z[n][cc], z[n][2 + cc]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            m = fmaxf(m, ref[n][cc]);
+            const float f = m == -INFINITY ? 1.f : ex2_approx(ref[n][cc] - m);
+            ref[n][cc] = m;
+            sum[n][cc] *= f;
+            float fv = f;
+            if constexpr (kE4M3) {
+              float mv = fmaxf(zv[n][cc], zv[n][2 + cc]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, x));
+              mv = fmaxf(mv, ref_v[n][cc]);
+              fv = mv == -INFINITY ? 1.f : ex2_approx(ref_v[n][cc] - mv);
+              ref_v[n][cc] = mv;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][n][cc] *= fv;
+              o[c][n][2 + cc] *= fv;
+            }
+          }
+      }
+      uint32_t hi[kNT][2], lo[kNT][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int cc = j & 1;
+          const float base = ref[n][cc] == -INFINITY ? 0.f : ref[n][cc];
+          const float e = ex2_approx(z[n][j] - base);
+          sum[n][cc] += e;
+          if constexpr (kE4M3)
+            w[j] = ex2_approx(zv[n][j] - (ref_v[n][cc] == -INFINITY ? 0.f : ref_v[n][cc]));
+          else
+            w[j] = e;
+        }
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const uint32_t h = pack_below<kMmaBf16>(w[2 * rr], w[2 * rr + 1]);
+          const float2 back = unpack16<kMmaBf16>(h);
+          hi[n][rr] = transpose8(h);
+          lo[n][rr] = transpose8(pack16<kMmaBf16>(w[2 * rr] - back.x, w[2 * rr + 1] - back.y));
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int c = 0; c < L::kChunks / 2; ++c) {
+        uint32_t a[4];
+        if constexpr (!kE4M3) {
+          const int r = mr + (mat >> 1) * 8;
+          ldsm4_t(a, stage + L::kStage / 2 + chunk_at<L::kChunks>(r, 2 * c + (mat & 1)));
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) mma<kMmaBf16>(o[c][n], a, hi[n][0], hi[n][1]);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) mma<kMmaBf16>(o[c][n], a, lo[n][0], lo[n][1]);
+        } else {
+          const int r = mr + (mat & 1) * 8;
+          ldsm4_t(a, stage + L::kStage / 2 + chunk_at<L::kChunks>(r, 2 * c + (mat >> 1)));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            // a word holds two adjacent columns of d at two adjacent positions: put the positions
+            // of each column together; row i of the MMA tile is column 2 i, row i + 8 is 2 i + 1
+            const uint32_t w0 = __byte_perm(a[2 * x], 0, 0x3120);
+            const uint32_t w1 = __byte_perm(a[2 * x + 1], 0, 0x3120);
+            const uint32_t f[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w0 >> 16),
+                                   e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w1 >> 16)};
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, hi[n][0], hi[n][1]);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, lo[n][0], lo[n][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage may be filled again
+
+    const bool done = cur.at.tile == cur.at.tiles - 1;
+    if (done || i == count - 1) {
+      // ---- join the warps ----
+      const bool whole = done && first_tile >= begin;
+      const int part = decode_part(first_tile, begin);
+      float* ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kJoinBytes) +
+                      (blockIdx.x * 2 + part) * kMaxRows;
+      float* ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kJoinBytes +
+                                             kLseBytes) +
+                    static_cast<size_t>(blockIdx.x * 2 + part) * kMaxRows * D;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          float l = sum[n][cc];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+          const int col = 2 * t + cc;
+          if (g == 0) {
+            float* r = join_r + warp * kMaxRows + n * 8 + col;
+            r[0] = ref[n][cc];
+            r[kWarps * kMaxRows] = kE4M3 ? ref_v[n][cc] : ref[n][cc];
+            r[2 * kWarps * kMaxRows] = l;
+          }
+          float* dst = join_o + (warp * 8 + col) * L::kPitch;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            dst[16 * c + (kE4M3 ? 2 * g : g)] = o[c][n][cc];
+            dst[16 * c + (kE4M3 ? 2 * g + 1 : g + 8)] = o[c][n][2 + cc];
+          }
+        }
+        __syncthreads();
+        const int d = threadIdx.x % D;
+#pragma unroll 1
+        for (int col = threadIdx.x / D; col < 8; col += kThreads / D) {
+          const int qr = row0 + n * 8 + col;  // query head within the group
+          if (qr >= p.group) break;
+          const float* r = join_r + n * 8 + col;
+          float m = -INFINITY, mv = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            m = fmaxf(m, r[w * kMaxRows]);
+            mv = fmaxf(mv, r[(kWarps + w) * kMaxRows]);
+          }
+          const float base = m == -INFINITY ? 0.f : m, base_v = mv == -INFINITY ? 0.f : mv;
+          float l = 0.f, acc = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            l += r[(2 * kWarps + w) * kMaxRows] * ex2_approx(r[w * kMaxRows] - base);
+            acc += join_o[(w * 8 + col) * L::kPitch + d] *
+                   ex2_approx(r[(kWarps + w) * kMaxRows] - base_v);
+          }
+          const float out = l == 0.f ? 0.f : acc / l * exp2f(base_v - base);
+          const float lse = l == 0.f ? -INFINITY : base + log2f(l);
+          if (whole) {
+            const long long at =
+                (static_cast<long long>(seq) * p.c.heads + head) * p.group + qr;
+            reinterpret_cast<uint16_t*>(p.o)[at * D + d] =
+                static_cast<uint16_t>(pack16<kBf16>(out, 0.f));
+            if (d == 0) p.lse[at] = lse * 0.69314718055994531f;
+          } else {
+            ws_o[(n * 8 + col) * D + d] = out;
+            if (d == 0) ws_lse[n * 8 + col] = lse;
+          }
+        }
+        __syncthreads();
+      }
+      if (!done && first_tile >= begin && threadIdx.x == 0) {
+        Join j;
+        j.entry = cur.at.entry;
+        j.item = cur.at.item;
+        j.last = static_cast<int>((first_tile + cur.at.tiles - 1) / share);
+        j.part = part;
+        joins[blockIdx.x] = j;
+      }
+      fresh = true;
+      first_tile = begin + i + 1;
+    }
+    if (i + 1 < count && decode_advance(cur.at, copies)) cur.enter(p);
+  }
+}
+
+// The join of an item's parts: block c handles the item that starts, unfinished,
+// in block c of decode_kernel.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads) join_kernel(const DecodeParams p, int rows_per_block) {
+  grid_dep_wait();
+  const Join j = static_cast<const Join*>(p.workspace)[blockIdx.x];
+  if (j.last < 0) return;
+  const float* ws_lse =
+      reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + kJoinBytes);
+  const float* ws_o = reinterpret_cast<const float*>(
+      static_cast<const uint8_t*>(p.workspace) + kJoinBytes + kLseBytes);
+  const int blocks_of_rows = (p.group + rows_per_block - 1) / rows_per_block;
+  const int seq = p.per_head ? j.entry / p.c.heads : j.entry;
+  const int head = (p.per_head ? j.entry % p.c.heads : 0) + j.item / blocks_of_rows;
+  const int row0 = (j.item % blocks_of_rows) * rows_per_block;
+  const int d = threadIdx.x % D, c0 = blockIdx.x;
+  for (int r = threadIdx.x / D; r < rows_per_block && row0 + r < p.group; r += kThreads / D) {
+    float m = -INFINITY;
+    for (int c = c0; c <= j.last; ++c)
+      m = fmaxf(m, ws_lse[(c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= j.last; ++c) {
+      const int slot = (c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r;
+      const float w = ex2_approx(ws_lse[slot] - base);
+      l += w;
+      acc = fmaf(w, ws_o[static_cast<size_t>(slot) * D + d], acc);
+    }
+    const long long at = (static_cast<long long>(seq) * p.c.heads + head) * p.group + row0 + r;
+    const float out = l == 0.f ? 0.f : acc / l;
+    reinterpret_cast<uint16_t*>(p.o)[at * D + d] =
+        static_cast<uint16_t>(pack16<kBf16>(out, 0.f));
+    if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// ---- host ----
+
+// `early`: the launch may begin while the kernel before it in the stream ends.
+// Only where that one is a kernel of this call: it waits for its own
+// predecessors, and ours waits for it (grid_dep_wait) before it reads anything.
+template <typename... A>
+bool launch_kernel(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem,
+                   cudaStream_t stream, bool early, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+template <int D, int kNT, bool kE4M3, bool kBf16>
+int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
+  using L = Layout<D, kNT, kE4M3>;
+  auto kernel = decode_kernel<D, kNT, kE4M3, kBf16>;
+  static std::once_flag once[kMaxDevices];
+  static int sms[kMaxDevices];
+  std::call_once(once[dev], [&] {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) ==
+            cudaSuccess)
+      sms[dev] = n;
+  });
+  if (sms[dev] < 1) return -4;
+  // two blocks to an SM; fewer if the table cannot hold that many tiles
+  const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
+  const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
+  const long long tiles = (positions + kDecodeTile - 1) / kDecodeTile;
+  long long grid = 2ll * sms[dev];
+  if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
+  const long long most =
+      (tiles * copies * p.t.batch + p.least_tiles - 1) / p.least_tiles;
+  if (grid > most) grid = most;
+  // (per_head: the choice of blocks ran just before)
+  if (!launch_kernel(kernel, static_cast<unsigned>(grid), kThreads, L::kSmem, stream,
+                     p.per_head != 0, p))
+    return -4;
+  if (!launch_kernel(join_kernel<D, kBf16>, static_cast<unsigned>(grid), kThreads, 0, stream,
+                     true, p, 8 * kNT))
+    return -4;
+  return 0;
+}
+
+template <int D>
+int dispatch(const DecodeParams& p, bool e4m3, bool bf16, int dev, cudaStream_t stream) {
+  const bool wide = p.group > 8;
+  if (e4m3) {
+    if (bf16)
+      return wide ? launch<D, 2, true, true>(p, dev, stream)
+                  : launch<D, 1, true, true>(p, dev, stream);
+    return wide ? launch<D, 2, true, false>(p, dev, stream)
+                : launch<D, 1, true, false>(p, dev, stream);
+  }
+  if (bf16)
+    return wide ? launch<D, 2, false, true>(p, dev, stream)
+                : launch<D, 1, false, true>(p, dev, stream);
+  return wide ? launch<D, 2, false, false>(p, dev, stream)
+              : launch<D, 1, false, false>(p, dev, stream);
+}
+
+}  // namespace decode
+
+}  // namespace fat
