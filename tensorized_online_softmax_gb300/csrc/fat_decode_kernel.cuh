@@ -65,10 +65,9 @@ struct Layout {
   static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 6 : 8;
   static constexpr int kScales = kE4M3 ? 32 : 0;
   static constexpr int kRing = kStages * (kStage + kScales);  // of one warp
-  static constexpr int kPitch = D + 4;  // floats: spreads the heads over the banks
-  static constexpr int kJoinO = kWarps * 8 * kPitch * 4;
+  static_assert(8 * D * 4 <= kStage, "a stage holds a warp's O for the join");
   static constexpr int kJoinRows = 3 * kWarps * kMaxRows * 4;
-  static constexpr int kSmem = kWarps * kRing + kJoinO + kJoinRows;
+  static constexpr int kSmem = kWarps * kRing + kJoinRows;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -182,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   __shared__ DecodePlace start_s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
-  float* join_o = reinterpret_cast<float*>(smem + kWarps * L::kRing);
-  float* join_r = join_o + kWarps * 8 * L::kPitch;  // [3][warp][kMaxRows]: r, r', l
+  float* join_r = reinterpret_cast<float*>(smem + kWarps * L::kRing);  // [3][warp][kMaxRows]: r, r', l
 
   grid_dep_launch();
   grid_dep_wait();
@@ -495,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 
     const bool done = cur.at.tile == cur.at.tiles - 1;
     if (done || i == count - 1) {
-      // ---- join the warps ----
+      // ---- join the warps: each leaves O in the stage that it has just used ----
+      const int used = (i % L::kStages) * (L::kStage + L::kScales);
       const bool whole = done && first_tile >= begin;
       const int part = decode_part(first_tile, begin);
       float* ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kJoinBytes) +
@@ -517,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
             r[kWarps * kMaxRows] = kE4M3 ? ref_v[n][cc] : ref[n][cc];
             r[2 * kWarps * kMaxRows] = l;
           }
-          float* dst = join_o + (warp * 8 + col) * L::kPitch;
+          float* dst = reinterpret_cast<float*>(smem + warp * L::kRing + used) + col * D;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            dst[16 * c + (kE4M3 ? 2 * g : g)] = o[c][n][cc];
-            dst[16 * c + (kE4M3 ? 2 * g + 1 : g + 8)] = o[c][n][2 + cc];
+          for (int c = 0; c < D / 16; ++c) {  // (the columns of four t go to different banks)
+            dst[(16 * c + (kE4M3 ? 2 * g : g)) ^ (8 * t)] = o[c][n][cc];
+            dst[(16 * c + (kE4M3 ? 2 * g + 1 : g + 8)) ^ (8 * t)] = o[c][n][2 + cc];
           }
         }
         __syncthreads();
@@ -542,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             l += r[(2 * kWarps + w) * kMaxRows] * ex2_approx(r[w * kMaxRows] - base);
-            acc += join_o[(w * 8 + col) * L::kPitch + d] *
+            const float* src = reinterpret_cast<const float*>(smem + w * L::kRing + used);
+            acc += src[col * D + (d ^ (8 * (col >> 1)))] *
                    ex2_approx(r[(kWarps + w) * kMaxRows] - base_v);
           }
           const float out = l == 0.f ? 0.f : acc / l * exp2f(base_v - base);
