@@ -17,7 +17,8 @@
 // when a score exceeds it by more than 8 binades, so the usual tile needs one
 // vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
 // the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and the only
-// rounding that counts is that of the output.
+// rounding that counts is that of the output (without the remainder the e4m3
+// batch below is 3.4 % faster).
 //
 // e4m3 caches: the codes become fp16 exactly, the keys' scales multiply S, and
 // the values' scales join the weights, w = 2^(z + log2 s - r'), with a running
@@ -56,14 +57,23 @@ constexpr int kMaxRows = 16;
 constexpr size_t kJoinBytes = sizeof(Join) * kDecodeMaxBlocks;
 constexpr size_t kLseBytes = sizeof(float) * kDecodeMaxBlocks * 2 * kMaxRows;
 
+#ifndef FAT_DECODE_BLOCKS
+#define FAT_DECODE_BLOCKS(nt, st) ((nt) == 1 ? 3 : 2)
+#endif
+
 template <int D, int kNT, bool kE4M3>
 struct Layout {
   static constexpr int kRow = D * (kE4M3 ? 1 : 2);  // bytes
   static constexpr int kChunks = kRow / 16;
   static constexpr int kStage = 2 * kRowsPerWarp * kRow;  // K and V of 16 positions
-  // about 24 KiB a warp: two blocks of an SM hold 192 KiB in flight
-  static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 6 : 8;
   static constexpr int kScales = kE4M3 ? 32 : 0;
+  // blocks on an SM (their registers allow no more), and a ring as deep as their share of the
+  // SM's 228 KiB
+  static constexpr int kBlocks = FAT_DECODE_BLOCKS(kNT, kStage);
+  static constexpr int kRoom = (228 * 1024 / kBlocks - 1024 - 1024) / kWarps;
+  static constexpr int kFit = kRoom / (kStage + kScales);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static_assert(kStages >= 2, "one stage is filled while another is used");
   static constexpr int kRing = kStages * (kStage + kScales);  // of one warp
   static_assert(8 * D * 4 <= kStage, "a stage holds a warp's O for the join");
   static constexpr int kJoinRows = 3 * kWarps * kMaxRows * 4;
@@ -73,6 +83,9 @@ struct Layout {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -172,7 +185,7 @@ struct Walk {
 };
 
 template <int D, int kNT, bool kE4M3, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) decode_kernel(const DecodeParams p) {
   using L = Layout<D, kNT, kE4M3>;
   constexpr bool kMmaBf16 = kBf16 && !kE4M3;
   constexpr int kR = 8 * kNT;  // query heads of a block of rows
@@ -244,14 +257,38 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
       const uint8_t* k = p.c.k + at * p.c.k_page + h * p.c.k_head + place * p.c.k_token;
       const uint8_t* v = p.c.v + at * p.c.v_page + h * p.c.v_head + place * p.c.v_token;
       constexpr int kPer = kRowsPerWarp * L::kChunks / 32;  // chunks of K to a lane
+      constexpr int kStep = 32 / L::kChunks;                // rows from one to the next
+      const int r0 = lane / L::kChunks, c = lane % L::kChunks;
+      if (valid == kRowsPerWarp) {
+        const uint8_t* kl = k + r0 * p.c.k_token + c * 16;
+        const uint8_t* vl = v + r0 * p.c.v_token + c * 16;
+        if (p.c.k_token == L::kRow && p.c.v_token == L::kRow) {  // rows follow one another
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = (i * 32 + lane) / L::kChunks, c = (i * 32 + lane) % L::kChunks;
-        const uint32_t bytes = r < valid ? 16u : 0u;
-        const int from = r < valid ? r : 0;
-        copy16(stage + chunk_at<L::kChunks>(r, c), k + from * p.c.k_token + c * 16, bytes);
-        copy16(stage + L::kStage / 2 + chunk_at<L::kChunks>(r, c),
-               v + from * p.c.v_token + c * 16, bytes);
+          for (int i = 0; i < kPer; ++i) {
+            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c);
+            copy16(to, kl + i * 512);
+            copy16(to + L::kStage / 2, vl + i * 512);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c);
+            copy16(to, kl);
+            copy16(to + L::kStage / 2, vl);
+            kl += kStep * p.c.k_token;
+            vl += kStep * p.c.v_token;
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+          const int r = r0 + i * kStep;
+          const uint32_t to = stage + chunk_at<L::kChunks>(r, c);
+          const uint32_t bytes = r < valid ? 16u : 0u;
+          const int from = r < valid ? r : 0;
+          copy16(to, k + from * p.c.k_token + c * 16, bytes);
+          copy16(to + L::kStage / 2, v + from * p.c.v_token + c * 16, bytes);
+        }
       }
       if constexpr (kE4M3) {
         if (lane < 2) {
@@ -281,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   uint32_t qf[D / 16][kNT][2];
   float factor[kNT][2];            // of the scores, by column
   float o[D / 16][kNT][4];
-  float ref[kNT][2], ref_v[kNT][2], sum[kNT][2];
+  // the references r and r' (0 while there is none), what raises them (-inf), and the sums
+  float ref[kNT][2], ref_v[kNT][2], top[kNT][2], top_v[kNT][2], sum[kNT][2];
   bool fresh = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
@@ -306,19 +344,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
           qf[s][n][1] = in ? __ldg(q + s * 8 + (kE4M3 ? 2 * t + 1 : t + 4)) : 0u;
         }
         if constexpr (kE4M3) {
-          float top = 0.f;
+          float most = 0.f;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float2 f = unpack16<kBf16>(qf[s][n][j]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
           // largest magnitude into [1, 2) (a row with an infinity stays as it is)
-          const uint32_t e = top > 0.f && top < INFINITY
-                                 ? min(max(__float_as_uint(top) >> 23, 1u), 253u)
+          const uint32_t e = most > 0.f && most < INFINITY
+                                 ? min(max(__float_as_uint(most) >> 23, 1u), 253u)
                                  : 127u;
           const float down = __uint_as_float((254u - e) << 23);
 #pragma unroll
@@ -336,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          ref[n][j] = ref_v[n][j] = -INFINITY;
-          sum[n][j] = 0.f;
+          ref[n][j] = ref_v[n][j] = sum[n][j] = 0.f;
+          top[n][j] = top_v[n][j] = -INFINITY;
         }
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -381,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
         }
       }
       float ks[2] = {1.f, 1.f}, vs[2] = {0.f, 0.f};
-      const bool in[2] = {row + g < cur.len, row + g + 8 < cur.len};
       if constexpr (kE4M3) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -394,45 +431,54 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
         }
       }
       float z[kNT][4], zv[kNT][4];
-      bool raise = false;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int rr = j >> 1, cc = j & 1;
-          const float s = s0[n][j] + s1[n][j];
-          z[n][j] = in[rr] ? s * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]) : -INFINITY;
-          raise |= z[n][j] > ref[n][cc] + kRaise;
-          if constexpr (kE4M3) {
-            zv[n][j] = in[rr] ? z[n][j] + vs[rr] : -INFINITY;
-            raise |= zv[n][j] > ref_v[n][cc] + kRaise;
-          }
+          z[n][j] = (s0[n][j] + s1[n][j]) * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
+          zv[n][j] = z[n][j] + vs[rr];
+        }
+      if (row + kRowsPerWarp > cur.len) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row + g + 8 * (j >> 1) >= cur.len) z[n][j] = zv[n][j] = -INFINITY;
+      }
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          raise |= z[n][j] > top[n][j & 1];
+          if constexpr (kE4M3) raise |= zv[n][j] > top_v[n][j & 1];
         }
       if (__any_sync(0xffffffffu, raise)) {
+        // r <- the maximum so far; what was summed shrinks by 2^(r_old - r)
+        auto raise_to = [&](float a, float b, float& r, float& limit) {
+          float m = fmaxf(a, b);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          const float old = limit == -INFINITY ? -INFINITY : r;
+          m = fmaxf(m, old);
+          if (m == -INFINITY) return 1.f;
+          r = m;
+          limit = m + kRaise;
+          return ex2_approx(old - m);
+        };
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            float m = fmaxf(z[n][cc], z[n][2 + cc]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            m = fmaxf(m, ref[n][cc]);
-            const float f = m == -INFINITY ? 1.f : ex2_approx(ref[n][cc] - m);
-            ref[n][cc] = m;
+            float f = raise_to(z[n][cc], z[n][2 + cc], ref[n][cc], top[n][cc]);
             sum[n][cc] *= f;
-            float fv = f;
-            if constexpr (kE4M3) {
-              float mv = fmaxf(zv[n][cc], zv[n][2 + cc]);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, x));
-              mv = fmaxf(mv, ref_v[n][cc]);
-              fv = mv == -INFINITY ? 1.f : ex2_approx(ref_v[n][cc] - mv);
-              ref_v[n][cc] = mv;
-            }
+            if constexpr (kE4M3)
+              f = raise_to(zv[n][cc], zv[n][2 + cc], ref_v[n][cc], top_v[n][cc]);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-              o[c][n][cc] *= fv;
-              o[c][n][2 + cc] *= fv;
+              o[c][n][cc] *= f;
+              o[c][n][2 + cc] *= f;
             }
           }
       }
@@ -442,14 +488,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
         float w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int cc = j & 1;
-          const float base = ref[n][cc] == -INFINITY ? 0.f : ref[n][cc];
-          const float e = ex2_approx(z[n][j] - base);
-          sum[n][cc] += e;
-          if constexpr (kE4M3)
-            w[j] = ex2_approx(zv[n][j] - (ref_v[n][cc] == -INFINITY ? 0.f : ref_v[n][cc]));
-          else
-            w[j] = e;
+          const float e = ex2_approx(z[n][j] - ref[n][j & 1]);
+          sum[n][j & 1] += e;
+          w[j] = kE4M3 ? ex2_approx(zv[n][j] - ref_v[n][j & 1]) : e;
         }
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -512,8 +553,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
           const int col = 2 * t + cc;
           if (g == 0) {
             float* r = join_r + warp * kMaxRows + n * 8 + col;
-            r[0] = ref[n][cc];
-            r[kWarps * kMaxRows] = kE4M3 ? ref_v[n][cc] : ref[n][cc];
+            r[0] = top[n][cc] == -INFINITY ? -INFINITY : ref[n][cc];
+            r[kWarps * kMaxRows] = !kE4M3                     ? r[0]
+                                   : top_v[n][cc] == -INFINITY ? -INFINITY
+                                                               : ref_v[n][cc];
             r[2 * kWarps * kMaxRows] = l;
           }
           float* dst = reinterpret_cast<float*>(smem + warp * L::kRing + used) + col * D;
@@ -575,40 +618,65 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   }
 }
 
-// The join of an item's parts: block c handles the item that starts, unfinished,
-// in block c of decode_kernel.
+// The join of an item's parts: block (c, row) handles a row of the item that
+// starts, unfinished, in block c of decode_kernel.  Groups of lanes (four
+// columns each) take the parts in turn: a long sequence alone has a few dozen.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeParams p, int rows_per_block) {
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
+  __shared__ float4 acc_s[kGroups][kLanes];
+  __shared__ float sum_s[kGroups];
   grid_dep_wait();
   const Join j = static_cast<const Join*>(p.workspace)[blockIdx.x];
   if (j.last < 0) return;
-  const float* ws_lse =
-      reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + kJoinBytes);
-  const float* ws_o = reinterpret_cast<const float*>(
-      static_cast<const uint8_t*>(p.workspace) + kJoinBytes + kLseBytes);
+  const int c0 = blockIdx.x, r = blockIdx.y;
   const int blocks_of_rows = (p.group + rows_per_block - 1) / rows_per_block;
   const int seq = p.per_head ? j.entry / p.c.heads : j.entry;
   const int head = (p.per_head ? j.entry % p.c.heads : 0) + j.item / blocks_of_rows;
-  const int row0 = (j.item % blocks_of_rows) * rows_per_block;
-  const int d = threadIdx.x % D, c0 = blockIdx.x;
-  for (int r = threadIdx.x / D; r < rows_per_block && row0 + r < p.group; r += kThreads / D) {
-    float m = -INFINITY;
-    for (int c = c0; c <= j.last; ++c)
-      m = fmaxf(m, ws_lse[(c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc = 0.f;
+  const int qr = (j.item % blocks_of_rows) * rows_per_block + r;
+  if (qr >= p.group) return;
+  const float* ws_lse =
+      reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + kJoinBytes);
+  const float4* ws_o = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(p.workspace) +
+                                                       kJoinBytes + kLseBytes);
+  auto slot = [&](int c) { return (c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r; };
+  float m = -INFINITY;
+  for (int c = c0 + threadIdx.x % 32; c <= j.last; c += 32) m = fmaxf(m, ws_lse[slot(c)]);
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float base = m == -INFINITY ? 0.f : m;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= j.last; ++c) {
-      const int slot = (c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r;
-      const float w = ex2_approx(ws_lse[slot] - base);
-      l += w;
-      acc = fmaf(w, ws_o[static_cast<size_t>(slot) * D + d], acc);
+  for (int c = c0 + group; c <= j.last; c += kGroups) {
+    const int at = slot(c);
+    const float w = ex2_approx(ws_lse[at] - base);
+    const float4 x = ws_o[static_cast<size_t>(at) * kLanes + lane];
+    l += w;
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  acc_s[group][lane] = acc;
+  if (lane == 0) sum_s[group] = l;
+  __syncthreads();
+  if (group == 0) {
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+      const float4 x = acc_s[i][lane];
+      l += sum_s[i];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
     }
-    const long long at = (static_cast<long long>(seq) * p.c.heads + head) * p.group + row0 + r;
-    const float out = l == 0.f ? 0.f : acc / l;
-    reinterpret_cast<uint16_t*>(p.o)[at * D + d] =
-        static_cast<uint16_t>(pack16<kBf16>(out, 0.f));
-    if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+    const long long at = (static_cast<long long>(seq) * p.c.heads + head) * p.group + qr;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<uint2*>(p.o)[at * kLanes + lane] =
+        make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
+    if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -618,10 +686,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeParams p, in
 // Only where that one is a kernel of this call: it waits for its own
 // predecessors, and ours waits for it (grid_dep_wait) before it reads anything.
 template <typename... A>
-bool launch_kernel(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem,
+bool launch_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem,
                    cudaStream_t stream, bool early, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -647,21 +715,22 @@ int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
       sms[dev] = n;
   });
   if (sms[dev] < 1) return -4;
-  // two blocks to an SM; fewer if the table cannot hold that many tiles
+  // as many blocks as are resident; fewer if the table cannot hold that many tiles
   const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
   const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
   const long long tiles = (positions + kDecodeTile - 1) / kDecodeTile;
-  long long grid = 2ll * sms[dev];
+  long long grid = static_cast<long long>(L::kBlocks) * sms[dev];
   if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
   const long long most =
       (tiles * copies * p.t.batch + p.least_tiles - 1) / p.least_tiles;
   if (grid > most) grid = most;
   // (per_head: the choice of blocks ran just before)
-  if (!launch_kernel(kernel, static_cast<unsigned>(grid), kThreads, L::kSmem, stream,
-                     p.per_head != 0, p))
+  const unsigned blocks = static_cast<unsigned>(grid);
+  if (!launch_kernel(kernel, dim3(blocks), kThreads, L::kSmem, stream, p.per_head != 0, p))
     return -4;
-  if (!launch_kernel(join_kernel<D, kBf16>, static_cast<unsigned>(grid), kThreads, 0, stream,
-                     true, p, 8 * kNT))
+  const unsigned rows = static_cast<unsigned>(p.group < 8 * kNT ? p.group : 8 * kNT);
+  if (!launch_kernel(join_kernel<D, kBf16>, dim3(blocks, rows), kThreads, 0, stream, true, p,
+                     8 * kNT))
     return -4;
   return 0;
 }
