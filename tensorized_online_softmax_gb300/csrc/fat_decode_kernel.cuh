@@ -57,8 +57,8 @@ constexpr int kMaxRows = 16;
 constexpr size_t kJoinBytes = sizeof(Join) * kDecodeMaxBlocks;
 constexpr size_t kLseBytes = sizeof(float) * kDecodeMaxBlocks * 2 * kMaxRows;
 
-#ifndef FAT_DECODE_BLOCKS
-#define FAT_DECODE_BLOCKS(nt, st) ((nt) == 1 ? 3 : 2)
+#ifndef FAT_SB
+#define FAT_SB 3
 #endif
 
 template <int D, int kNT, bool kE4M3>
@@ -69,7 +69,7 @@ struct Layout {
   static constexpr int kScales = kE4M3 ? 32 : 0;
   // blocks on an SM (their registers allow no more), and a ring as deep as their share of the
   // SM's 228 KiB
-  static constexpr int kBlocks = FAT_DECODE_BLOCKS(kNT, kStage);
+  static constexpr int kBlocks = kNT > 1 ? 2 : kStage < 8192 ? FAT_SB : 3;
   static constexpr int kRoom = (228 * 1024 / kBlocks - 1024 - 1024) / kWarps;
   static constexpr int kFit = kRoom / (kStage + kScales);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -174,15 +174,25 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   return x;
 }
 
-// A walk along the line of tiles, with the current entry's length and page.
-struct Walk {
-  DecodePlace at;
-  int len;
-  __device__ __forceinline__ void enter(const DecodeParams& p) {
-    len = table_length(p.t, p.c.page_shift, at.entry);
-    at.tiles = decode_tiles(len);
-  }
+// What an item is: its sequence, cached head and first query head of the group.
+struct Item {
+  int seq, head, row0;
 };
+__device__ __forceinline__ Item item_of(const DecodeParams& p, const DecodePlace& at, int rows,
+                                        int blocks_of_rows) {
+  const int h = at.item / blocks_of_rows;
+  Item r;
+  r.row0 = (at.item - h * blocks_of_rows) * rows;
+  r.seq = p.per_head ? at.entry / p.c.heads : at.entry;
+  r.head = p.per_head ? at.entry - r.seq * p.c.heads : h;
+  return r;
+}
+
+__device__ __forceinline__ int enter(const DecodeParams& p, DecodePlace& at) {
+  const int len = table_length(p.t, p.c.page_shift, at.entry);
+  at.tiles = decode_tiles(len);
+  return len;
+}
 
 template <int D, int kNT, bool kE4M3, bool kBf16>
 __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) decode_kernel(const DecodeParams p) {
@@ -236,43 +246,56 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 
   // ---- the copies, ahead of the arithmetic ----
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
-  Walk load;
-  load.at = start_s;
-  load.enter(p);
-  auto first_row = [&](const Walk& w) { return w.at.tile * kDecodeTile + warp * kRowsPerWarp; };
-  auto page_of = [&](const Walk& w) -> long long {
-    const int row = first_row(w);
-    return row < w.len ? table_page(p.t, p.c.num_pages, w.at.entry, row >> p.c.page_shift) : -1;
+  DecodePlace load = start_s;
+  int load_len = enter(p, load);
+  const uint8_t *load_k, *load_v;  // the item's head in page 0
+  const int* load_pages;           // the entry's line of the table
+  int load_head;
+  auto load_item = [&]() {
+    load_head = item_of(p, load, kR, blocks_of_rows).head;
+    load_k = p.c.k + load_head * p.c.k_head;
+    load_v = p.c.v + load_head * p.c.v_head;
+    load_pages = p.t.pages + load.entry * p.t.stride;
   };
-  long long page = page_of(load);
+  load_item();
+  const int warp_row = warp * kRowsPerWarp;
+  auto next_page = [&]() {  // (checked where it is used)
+    const int row = load.tile * kDecodeTile + warp_row;
+    return row < load_len ? __ldg(load_pages + (row >> p.c.page_shift)) : 0;
+  };
+  int page = next_page();
   int loaded = 0;
+  uint32_t stage_in = ring;  // of the next copy
+  const int r0 = lane / L::kChunks, c0 = lane % L::kChunks;  // the lane's first chunk
   auto issue = [&]() {
-    const int row = first_row(load);
-    if (row < load.len) {
-      const int h = (p.per_head ? load.at.entry % p.c.heads : 0) + load.at.item / blocks_of_rows;
-      const uint32_t stage = ring + (loaded % L::kStages) * (L::kStage + L::kScales);
+    const int row = load.tile * kDecodeTile + warp_row;
+    if (row < load_len) {
+      const uint32_t stage = stage_in;
       const int place = row & (p.c.page_size - 1);
-      const int valid = page < 0 ? 0 : min(kRowsPerWarp, load.len - row);
-      const long long at = max(page, 0ll);
-      const uint8_t* k = p.c.k + at * p.c.k_page + h * p.c.k_head + place * p.c.k_token;
-      const uint8_t* v = p.c.v + at * p.c.v_page + h * p.c.v_head + place * p.c.v_token;
+      int valid = min(kRowsPerWarp, load_len - row);
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.num_pages)) {
+        atomicOr(p.t.error_word, kErrIndex);
+        page = valid = 0;  // zeros in place of rows, and no address made of the page
+      }
+      const uint32_t pg = static_cast<uint32_t>(page);
+      const uint8_t* k = load_k + pg * p.c.k_page + place * p.c.k_token;
+      const uint8_t* v = load_v + pg * p.c.v_page + place * p.c.v_token;
       constexpr int kPer = kRowsPerWarp * L::kChunks / 32;  // chunks of K to a lane
       constexpr int kStep = 32 / L::kChunks;                // rows from one to the next
-      const int r0 = lane / L::kChunks, c = lane % L::kChunks;
       if (valid == kRowsPerWarp) {
-        const uint8_t* kl = k + r0 * p.c.k_token + c * 16;
-        const uint8_t* vl = v + r0 * p.c.v_token + c * 16;
+        const uint8_t* kl = k + r0 * p.c.k_token + c0 * 16;
+        const uint8_t* vl = v + r0 * p.c.v_token + c0 * 16;
         if (p.c.k_token == L::kRow && p.c.v_token == L::kRow) {  // rows follow one another
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
-            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c);
+            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c0);
             copy16(to, kl + i * 512);
             copy16(to + L::kStage / 2, vl + i * 512);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
-            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c);
+            const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c0);
             copy16(to, kl);
             copy16(to + L::kStage / 2, vl);
             kl += kStep * p.c.k_token;
@@ -283,25 +306,30 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 #pragma unroll 1
         for (int i = 0; i < kPer; ++i) {
           const int r = r0 + i * kStep;
-          const uint32_t to = stage + chunk_at<L::kChunks>(r, c);
+          const uint32_t to = stage + chunk_at<L::kChunks>(r, c0);
           const uint32_t bytes = r < valid ? 16u : 0u;
           const int from = r < valid ? r : 0;
-          copy16(to, k + from * p.c.k_token + c * 16, bytes);
-          copy16(to + L::kStage / 2, v + from * p.c.v_token + c * 16, bytes);
+          copy16(to, k + from * p.c.k_token + c0 * 16, bytes);
+          copy16(to + L::kStage / 2, v + from * p.c.v_token + c0 * 16, bytes);
         }
       }
       if constexpr (kE4M3) {
         if (lane < 2) {
-          const uint8_t* s = (lane == 0 ? p.c.k_scale : p.c.v_scale) +
-                             ((at * p.c.heads + h) * p.c.page_size + place);
-          copy16(stage + L::kStage + lane * 16, s, page < 0 ? 0u : 16u);
+          const long long at = (static_cast<long long>(pg) * p.c.heads + load_head) * p.c.page_size;
+          copy16(stage + L::kStage + lane * 16,
+                 (lane == 0 ? p.c.k_scale : p.c.v_scale) + at + place, valid ? 16u : 0u);
         }
       }
     }
-    ++loaded;
-    if (loaded < count) {
-      if (decode_advance(load.at, copies)) load.enter(p);
-      page = page_of(load);  // used by the next issue(): its latency is hidden
+    stage_in += L::kStage + L::kScales;
+    if (stage_in == ring + L::kRing) stage_in = ring;
+    if (++loaded < count) {
+      const bool entry = decode_advance(load, copies);
+      if (load.tile == 0) {
+        if (entry) load_len = enter(p, load);
+        load_item();
+      }
+      page = next_page();  // used by the next issue(): its latency is hidden
     }
   };
 #pragma unroll 1
@@ -311,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   }
 
   // ---- the arithmetic ----
-  Walk cur;
-  cur.at = start_s;
-  cur.enter(p);
-  long long first_tile = begin - cur.at.tile;  // of the current item
+  DecodePlace cur = start_s;
+  int cur_len = enter(p, cur);
+  long long first_tile = begin - cur.tile;  // of the current item
+  uint32_t stage_out = ring;
   uint32_t qf[D / 16][kNT][2];
   float factor[kNT][2];            // of the scores, by column
   float o[D / 16][kNT][4];
@@ -325,13 +353,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   for (int i = 0; i < count; ++i) {
     if (loaded < count) issue();
     copy_commit();
-    const int seq = p.per_head ? cur.at.entry / p.c.heads : cur.at.entry;
-    const int head =
-        (p.per_head ? cur.at.entry % p.c.heads : 0) + cur.at.item / blocks_of_rows;
-    const int row0 = (cur.at.item % blocks_of_rows) * kR;  // first query head of the group
     if (fresh) {
       fresh = false;
-      const uint8_t* q0 = p.q + seq * p.q_batch + (head * p.group + row0) * p.q_head;
+      const Item it = item_of(p, cur, kR, blocks_of_rows);
+      const int row0 = it.row0;
+      const uint8_t* q0 = p.q + it.seq * p.q_batch + (it.head * p.group + row0) * p.q_head;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         const bool in = row0 + n * 8 + g < p.group;
@@ -385,9 +411,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
     }
     copy_wait<L::kStages - 1>();
     __syncwarp();
-    const int row = first_row(cur);
-    if (row < cur.len) {
-      const uint32_t stage = ring + (i % L::kStages) * (L::kStage + L::kScales);
+    const int row = cur.tile * kDecodeTile + warp_row;
+    const uint32_t used = stage_out - ring;  // the same in every warp
+    if (row < cur_len) {
+      const uint32_t stage = stage_out;
       const int mat = lane / 8, mr = lane % 8;
       // S = K Q^T, in two chains
       float s0[kNT][4], s1[kNT][4];
@@ -439,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           z[n][j] = (s0[n][j] + s1[n][j]) * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
           zv[n][j] = z[n][j] + vs[rr];
         }
-      if (row + kRowsPerWarp > cur.len) {
+      if (row + kRowsPerWarp > cur_len) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (row + g + 8 * (j >> 1) >= cur.len) z[n][j] = zv[n][j] = -INFINITY;
+            if (row + g + 8 * (j >> 1) >= cur_len) z[n][j] = zv[n][j] = -INFINITY;
       }
       bool raise = false;
 #pragma unroll
@@ -531,11 +558,13 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       }
     }
     __syncwarp();  // the stage may be filled again
+    stage_out += L::kStage + L::kScales;
+    if (stage_out == ring + L::kRing) stage_out = ring;
 
-    const bool done = cur.at.tile == cur.at.tiles - 1;
+    const bool done = cur.tile == cur.tiles - 1;
     if (done || i == count - 1) {
       // ---- join the warps: each leaves O in the stage that it has just used ----
-      const int used = (i % L::kStages) * (L::kStage + L::kScales);
+      const Item it = item_of(p, cur, kR, blocks_of_rows);
       const bool whole = done && first_tile >= begin;
       const int part = decode_part(first_tile, begin);
       float* ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kJoinBytes) +
@@ -570,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
         const int d = threadIdx.x % D;
 #pragma unroll 1
         for (int col = threadIdx.x / D; col < 8; col += kThreads / D) {
-          const int qr = row0 + n * 8 + col;  // query head within the group
+          const int qr = it.row0 + n * 8 + col;  // query head within the group
           if (qr >= p.group) break;
           const float* r = join_r + n * 8 + col;
           float m = -INFINITY, mv = -INFINITY;
@@ -592,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           const float lse = l == 0.f ? -INFINITY : base + log2f(l);
           if (whole) {
             const long long at =
-                (static_cast<long long>(seq) * p.c.heads + head) * p.group + qr;
+                (static_cast<long long>(it.seq) * p.c.heads + it.head) * p.group + qr;
             reinterpret_cast<uint16_t*>(p.o)[at * D + d] =
                 static_cast<uint16_t>(pack16<kBf16>(out, 0.f));
             if (d == 0) p.lse[at] = lse * 0.69314718055994531f;
@@ -605,16 +634,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       }
       if (!done && first_tile >= begin && threadIdx.x == 0) {
         Join j;
-        j.entry = cur.at.entry;
-        j.item = cur.at.item;
-        j.last = static_cast<int>((first_tile + cur.at.tiles - 1) / share);
+        j.entry = cur.entry;
+        j.item = cur.item;
+        j.last = static_cast<int>((first_tile + cur.tiles - 1) / share);
         j.part = part;
         joins[blockIdx.x] = j;
       }
       fresh = true;
       first_tile = begin + i + 1;
     }
-    if (i + 1 < count && decode_advance(cur.at, copies)) cur.enter(p);
+    if (i + 1 < count && decode_advance(cur, copies)) cur_len = enter(p, cur);
   }
 }
 
