@@ -169,6 +169,7 @@ struct DecodeParams {
   uint8_t* o;
   float* lse;
   void* workspace;
+  int direct;                 // each block has one item (set by the launch)
   int least_tiles;            // tiles that a thread block takes at least
 };
 // what launch_decode needs, whatever the batch

@@ -214,7 +214,17 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   const int heads_per_entry = p.per_head ? 1 : p.c.heads;
   const int copies = heads_per_entry * blocks_of_rows;
   long long begin, share, total;
-  {
+  if (p.direct) {
+    const int e = blockIdx.x / copies;
+    if (threadIdx.x == 0) {
+      start_s.entry = e;
+      start_s.item = blockIdx.x - e * copies;
+      start_s.tile = 0;
+    }
+    begin = 0;
+    share = total = decode_tiles(table_length(p.t, p.c.page_shift, e));
+    __syncthreads();
+  } else {
     const int entries = p.t.batch;
     const int each = (entries + kThreads - 1) / kThreads;
     const int lo = threadIdx.x * each, hi = min(entries, lo + each);
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
     __syncthreads();
   }
   Join* joins = static_cast<Join*>(p.workspace);
-  if (threadIdx.x == 0) joins[blockIdx.x].last = -1;
+  if (!p.direct && threadIdx.x == 0) joins[blockIdx.x].last = -1;
   if (begin >= total) return;
   const long long end = min(total, begin + share);
   const int count = static_cast<int>(end - begin);
@@ -744,16 +754,23 @@ int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
       sms[dev] = n;
   });
   if (sms[dev] < 1) return -4;
-  // as many blocks as are resident; fewer if the table cannot hold that many tiles
   const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
   const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
   const long long tiles = (positions + kDecodeTile - 1) / kDecodeTile;
+  if (tiles <= kDirectTiles && static_cast<long long>(copies) * p.t.batch <= 0x7fffffffll) {
+    DecodeParams one = p;
+    one.direct = 1;
+    const unsigned items = static_cast<unsigned>(copies) * static_cast<unsigned>(p.t.batch);
+    return launch_kernel(kernel, dim3(items), kThreads, L::kSmem, stream, p.per_head != 0, one)
+               ? 0
+               : -4;
+  }
+  // as many blocks as are resident; fewer if the table cannot hold that many tiles
   long long grid = static_cast<long long>(L::kBlocks) * sms[dev];
   if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
   const long long most =
       (tiles * copies * p.t.batch + p.least_tiles - 1) / p.least_tiles;
   if (grid > most) grid = most;
-  // (per_head: the choice of blocks ran just before)
   const unsigned blocks = static_cast<unsigned>(grid);
   if (!launch_kernel(kernel, dim3(blocks), kThreads, L::kSmem, stream, p.per_head != 0, p))
     return -4;

@@ -65,15 +65,15 @@ def declare(lib) -> None:
 
 _WIDE = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
 _CACHE = {**_WIDE, torch.float8_e4m3fn: DTYPES["e4m3"]}
+_E4M3 = DTYPES["e4m3"]
 _HERE = contextlib.nullcontext()
 
-
-def _strides(t, dims):
-    """Strides of `dims` in elements; a dimension of one entry has none that matters."""
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
+# The checks below run for every call of a serving loop, where a few microseconds count: each
+# function first asks everything at once, and only finds out what is wrong if something is.
 
 
-def _tensor(name, t, dtypes, dim, device=None):
+def _wrong(name, t, dtypes, dim, device=None):
+    """The ValueError for a tensor that is not what `dtypes`, `dim` and `device` say, if it is not."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -82,62 +82,93 @@ def _tensor(name, t, dtypes, dim, device=None):
         raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _tensor(name, t, dtypes, dim, device=None):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == dim
+            and (device is None or t.device == device)):
+        _wrong(name, t, dtypes, dim, device)
     return t
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, writable=False):
-    """The checked cache as a struct; v_cache None where only the keys are read."""
-    _tensor("k_cache", k_cache, _CACHE, 4)
-    pages, heads, page_size, d = k_cache.shape
-    c = FatKvCache(k=k_cache.data_ptr(), num_pages=pages, heads=heads, page_size=page_size, d=d,
-                   dtype=_CACHE[k_cache.dtype])
-    c.k_page_stride, c.k_head_stride, c.k_token_stride = _strides(k_cache, (0, 1, 2))
-    parts = [("k", k_cache, k_scale)]
-    if v_cache is not None:
-        _tensor("v_cache", v_cache, (k_cache.dtype,), 4, k_cache.device)
-        if v_cache.shape != k_cache.shape:
+def _rows(name, t, shape, writable):
+    """Strides between pages, heads and tokens; those of a dimension of one entry do not matter."""
+    a, b, c, row = t.stride()
+    if row != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if 1 in shape:
+        a, b, c = (x if n > 1 else 0 for x, n in zip((a, b, c), shape))
+    if writable and not (a and b and c) and any(
+            n > 1 and not x for x, n in zip((a, b, c), shape)):
+        raise ValueError(f"{name} is a broadcast view: its rows share memory")
+    return a, b, c
+
+
+def _scale(name, t, shape, device):
+    if t is None:
+        raise ValueError(f"an e4m3 cache needs {name}")
+    _tensor(name, t, (torch.uint8,), 3, device)
+    if t.shape != shape[:3] or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [num_pages, heads, page_size]")
+    return t.data_ptr()
+
+
+def _cache(k, v, k_scale, v_scale, writable=False):
+    """The checked cache as a struct; v None where only the keys are read."""
+    _tensor("k_cache", k, _CACHE, 4)
+    device, kind, shape = k.device, _CACHE[k.dtype], k.shape
+    k_rows = _rows("k_cache", k, shape, writable)
+    at, v_rows = None, (0, 0, 0)
+    if v is not None:
+        _tensor("v_cache", v, (k.dtype,), 4, device)
+        if v.shape != shape:
             raise ValueError("k_cache and v_cache must have the same shape")
-        c.v = v_cache.data_ptr()
-        c.v_page_stride, c.v_head_stride, c.v_token_stride = _strides(v_cache, (0, 1, 2))
-        parts.append(("v", v_cache, v_scale))
-    for name, t, scale in parts:
-        if t.stride(3) != 1:
-            raise ValueError(f"the rows of {name}_cache must be contiguous")
-        if writable and any(t.shape[i] > 1 and t.stride(i) == 0 for i in range(3)):
-            raise ValueError(f"{name}_cache is a broadcast view: its rows share memory")
-        if t.dtype is torch.float8_e4m3fn:
-            if scale is None:
-                raise ValueError(f"an e4m3 cache needs {name}_scale")
-            _tensor(f"{name}_scale", scale, (torch.uint8,), 3, k_cache.device)
-            if scale.shape != (pages, heads, page_size) or not scale.is_contiguous():
-                raise ValueError(f"{name}_scale must be contiguous [num_pages, heads, page_size]")
-            setattr(c, name + "_scale", scale.data_ptr())
-        elif scale is not None:
-            raise ValueError(f"{name}_scale goes with an e4m3 cache only")
-    return c
+        at, v_rows = v.data_ptr(), _rows("v_cache", v, shape, writable)
+    ks = vs = None
+    if kind == _E4M3:
+        ks = _scale("k_scale", k_scale, shape, device)
+        vs = _scale("v_scale", v_scale, shape, device) if v is not None else None
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales go with an e4m3 cache only")
+    return FatKvCache(k.data_ptr(), at, ks, vs, shape[0], shape[1], shape[2], shape[3], kind,
+                      *k_rows, *v_rows)
 
 
 def _table(page_table, seq_lens, device):
     _tensor("page_table", page_table, (torch.int32,), 2, device)
     _tensor("seq_lens", seq_lens, (torch.int32,), 1, device)
     batch, width = page_table.shape
+    stride, step = page_table.stride()
     if seq_lens.shape[0] != batch or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be contiguous [B], page_table [B, width]")
-    if width > 1 and page_table.stride(1) != 1:
+    if width > 1 and step != 1:
         raise ValueError("the rows of page_table must be contiguous")
-    return FatPageTable(page_table.data_ptr(), page_table.stride(0) if batch > 1 else width, width,
-                        batch, seq_lens.data_ptr())
+    return FatPageTable(page_table.data_ptr(), stride if batch > 1 else width, width, batch,
+                        seq_lens.data_ptr())
 
 
 def _query(q, batch, heads, d, device):
     """q [B, Hq, d] -> its pointer, type, strides and head count as C arguments."""
     _tensor("q", q, _WIDE, 3, device)
-    if q.shape[0] != batch or q.shape[2] != d or q.shape[1] < 1 or q.shape[1] % heads:
+    b, h, c = q.shape
+    if b != batch or c != d or h < 1 or h % heads:
         raise ValueError(f"q must be [{batch}, a multiple of {heads}, {d}], "
                          f"not {list(q.shape)}")
-    if q.stride(2) != 1:
+    per_batch, per_head, step = q.stride()
+    if step != 1:
         raise ValueError("the rows of q must be contiguous")
-    return (q.data_ptr(), _WIDE[q.dtype], *_strides(q, (0, 1)), q.shape[1])
+    return (q.data_ptr(), _WIDE[q.dtype], per_batch if b > 1 else 0, per_head if h > 1 else 0, h)
+
+
+def _tokens(name, t, shape, dtypes, device):
+    """k or v [T, heads, d] -> its strides between tokens and heads."""
+    _tensor(name, t, dtypes, 3, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    a, b, row = t.stride()
+    if row != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
 
 def _output(name, t, shape, dtype, device):
@@ -156,7 +187,7 @@ def _stream(stream, device, fresh):
     """The stream's handle; tensors allocated by this call are kept for a stream that is not the
     one they were allocated on."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     for t in fresh:
@@ -183,22 +214,20 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
     lib = load_library()
     c = _cache(k_cache, v_cache, k_scale, v_scale, writable=True)
     device = k_cache.device
-    _tensor("k", k, _WIDE, 3, device)
-    _tensor("v", v, (k.dtype,), 3, device)
     _tensor("slots", slots, (torch.int64,), 1, device)
-    tokens = slots.shape[0]
-    if k.shape != (tokens, c.heads, c.d) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [{tokens}, {c.heads}, {c.d}]")
-    if c.dtype != DTYPES["e4m3"] and k.dtype != k_cache.dtype:
+    shape = torch.Size((slots.shape[0], c.heads, c.d))
+    k_strides = _tokens("k", k, shape, _WIDE, device)
+    v_strides = _tokens("v", v, shape, (k.dtype,), device)
+    if c.dtype != _E4M3 and k.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} tokens, not {k.dtype}")
-    if tokens == 0:
+    if not shape[0]:
         return
-    if k.stride(2) != 1 or v.stride(2) != 1 or not slots.is_contiguous():
-        raise ValueError("the rows of k and v, and slots, must be contiguous")
+    if not slots.is_contiguous():
+        raise ValueError("slots must be contiguous")
     with _on(device):
-        _done(lib.fat_kv_write(c, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype],
-                               *_strides(k, (0, 1)), *_strides(v, (0, 1)), slots.data_ptr(),
-                               tokens, _stream(stream, device, ())), "fat_kv_write")
+        _done(lib.fat_kv_write(c, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype], *k_strides,
+                               *v_strides, slots.data_ptr(), shape[0],
+                               _stream(stream, device, ())), "fat_kv_write")
 
 
 def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype=None,
@@ -213,8 +242,8 @@ def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype
     device = k_cache.device
     t = _table(page_table, seq_lens, device)
     if dtype is None:
-        dtype = torch.bfloat16 if c.dtype == DTYPES["e4m3"] else k_cache.dtype
-    if dtype not in _WIDE or (c.dtype != DTYPES["e4m3"] and dtype != k_cache.dtype):
+        dtype = torch.bfloat16 if c.dtype == _E4M3 else k_cache.dtype
+    if dtype not in _WIDE or (c.dtype != _E4M3 and dtype != k_cache.dtype):
         raise ValueError(f"a {k_cache.dtype} cache is not read as {dtype}")
     shape = (t.batch, c.heads, int(max_len), c.d)
     if shape[2] < 1:
@@ -234,12 +263,12 @@ def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, scale, k_scale,
     device = k_cache.device
     t = _table(page_table, seq_lens, device)
     query = _query(q, t.batch, c.heads, c.d, device)
-    if c.dtype != DTYPES["e4m3"] and q.dtype != k_cache.dtype:
+    if c.dtype != _E4M3 and q.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} queries, not {q.dtype}")
     shape = q.shape
     fresh = []
     if out is None:
-        o = torch.empty(shape, dtype=q.dtype, device=device)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
         fresh += [o, lse]
     else:
@@ -296,7 +325,7 @@ def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | Non
     c = _cache(k_cache, None, k_scale, None)
     device = k_cache.device
     t = _table(page_table, seq_lens, device)
-    dtypes = _WIDE if c.dtype == DTYPES["e4m3"] else (k_cache.dtype,)
+    dtypes = _WIDE if c.dtype == _E4M3 else (k_cache.dtype,)
     _tensor("bounds", bounds, dtypes, 4, device)
     _output("bounds", bounds, (c.num_pages, c.heads, 2, c.d), bounds.dtype, device)
     new_tokens = 0x7fffffff if new_tokens is None else int(new_tokens)
