@@ -223,7 +223,10 @@ int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
   p.heads = kv_heads;
   p.group = q_heads / kv_heads;
   p.scores = scores;
-  return status(fat::launch_kv_scores(p, d, dtype == FAT_DTYPE_BF16, stream));
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return FAT_ERR_LAUNCH;
+  return status(fat::launch_kv_scores(p, d, dtype == FAT_DTYPE_BF16, sms, stream));
 }
 
 static size_t choice_bytes(long long bh, long long list) {
