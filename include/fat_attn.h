@@ -347,7 +347,7 @@ typedef struct fat_page_table {
  * scale is the least power of two that brings its largest magnitude to at
  * most 448 (1 for a row of zeros), so dividing by it is exact and each
  * element is rounded once, to nearest even.  The slots of one call must
- * differ.  tokens = 0 is allowed.
+ * differ.  tokens = 0 is allowed; tokens * heads is below 2^31 - 2^16.
  */
 int fat_kv_write(const fat_kv_cache* cache, const void* k, const void* v, int dtype,
                  long long k_token_stride, long long k_head_stride, long long v_token_stride,

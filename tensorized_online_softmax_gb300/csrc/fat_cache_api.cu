@@ -103,7 +103,7 @@ int fat_kv_write(const fat_kv_cache* cache, const void* k, const void* v, int dt
     return FAT_ERR_INVALID_ARG;
   if (tokens == 0) return FAT_OK;
   if (!k || !v || !slots) return FAT_ERR_INVALID_ARG;
-  if (static_cast<long long>(tokens) * cache->heads > (1ll << 34)) return FAT_ERR_INVALID_ARG;
+  if (static_cast<long long>(tokens) * cache->heads > 0x7fff0000ll) return FAT_ERR_INVALID_ARG;
   if (!stride_ok(k_token_stride, 2, &p.k_token) || !stride_ok(k_head_stride, 2, &p.k_head) ||
       !stride_ok(v_token_stride, 2, &p.v_token) || !stride_ok(v_head_stride, 2, &p.v_head) ||
       !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))

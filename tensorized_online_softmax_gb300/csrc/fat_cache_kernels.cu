@@ -47,54 +47,67 @@ __device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t& e) 
   return r;
 }
 
-// One lane per eight elements of a row; thread -> (token, head, lane), K and V.
+// One lane per eight elements of a row; a thread takes that lane of kWriteRows
+// rows (token, head) of K and V, whose loads are all in flight together.
+constexpr int kWriteRows = 2;
+
 template <int D, bool kE4M3, bool kBf16>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p) {
-  constexpr int kLanes = D / 8;
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const int lane = static_cast<int>(i % kLanes);
-  const long long row = i / kLanes;
-  const bool in = row < static_cast<long long>(p.tokens) * p.c.heads;
-  const int t = in ? static_cast<int>(row / p.c.heads) : 0;
-  const int h = in ? static_cast<int>(row % p.c.heads) : 0;
-  const long long slot = in ? __ldg(p.slots + t) : -1;
-  const long long page = slot >> p.c.page_shift;
-  bool ok = slot >= 0;
-  if (ok && page >= p.c.num_pages) {
-    atomicOr(p.error_word, kErrIndex);
-    ok = false;
-  }
-  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-  if (ok) {
-    kx = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + lane);
-    vx = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + lane);
-  }
-  const long long place = slot & (p.c.page_size - 1);
-  uint8_t* kd = p.c.k + page * p.c.k_page + h * p.c.k_head + place * p.c.k_token;
-  uint8_t* vd = p.c.v + page * p.c.v_page + h * p.c.v_head + place * p.c.v_token;
-  if constexpr (!kE4M3) {
-    if (ok) {
-      reinterpret_cast<uint4*>(kd)[lane] = kx;
-      reinterpret_cast<uint4*>(vd)[lane] = vx;
-    }
-  } else {
-    const uint32_t kw[4] = {kx.x, kx.y, kx.z, kx.w}, vw[4] = {vx.x, vx.y, vx.z, vx.w};
-    float kf[8], vf[8];
+  constexpr int kLanes = D / 8, kBlockRows = kThreads / kLanes;
+  const uint32_t lane = threadIdx.x % kLanes;
+  const uint32_t heads = p.c.heads, rows = static_cast<uint32_t>(p.tokens) * heads;
+  long long slot[kWriteRows];
+  uint32_t head[kWriteRows];
+  uint4 k[kWriteRows], v[kWriteRows];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = unpack16<kBf16>(kw[j]), b = unpack16<kBf16>(vw[j]);
-      kf[2 * j] = a.x, kf[2 * j + 1] = a.y;
-      vf[2 * j] = b.x, vf[2 * j + 1] = b.y;
+  for (int i = 0; i < kWriteRows; ++i) {
+    const uint32_t row = (blockIdx.x * kWriteRows + i) * kBlockRows + threadIdx.x / kLanes;
+    const uint32_t t = row / heads;
+    head[i] = row - t * heads;
+    slot[i] = -1;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      slot[i] = __ldg(p.slots + t);
+      k[i] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + head[i] * p.k_head) + lane);
+      v[i] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + head[i] * p.v_head) + lane);
     }
-    uint32_t ke, ve;
-    const uint2 kc = quantise_row<kLanes>(kf, ke), vc = quantise_row<kLanes>(vf, ve);
-    if (ok) {
-      reinterpret_cast<uint2*>(kd)[lane] = kc;
-      reinterpret_cast<uint2*>(vd)[lane] = vc;
-      if (lane == 0) {
-        const long long at = (page * p.c.heads + h) * p.c.page_size + place;
-        p.c.k_scale[at] = static_cast<uint8_t>(ke);
-        p.c.v_scale[at] = static_cast<uint8_t>(ve);
+  }
+#pragma unroll
+  for (int i = 0; i < kWriteRows; ++i) {
+    const long long page = slot[i] >> p.c.page_shift;
+    bool ok = slot[i] >= 0;
+    if (ok && page >= p.c.num_pages) {
+      atomicOr(p.error_word, kErrIndex);
+      ok = false;
+    }
+    const long long place = slot[i] & (p.c.page_size - 1);
+    uint8_t* kd = p.c.k + page * p.c.k_page + head[i] * p.c.k_head + place * p.c.k_token;
+    uint8_t* vd = p.c.v + page * p.c.v_page + head[i] * p.c.v_head + place * p.c.v_token;
+    if constexpr (!kE4M3) {
+      if (ok) {
+        reinterpret_cast<uint4*>(kd)[lane] = k[i];
+        reinterpret_cast<uint4*>(vd)[lane] = v[i];
+      }
+    } else {
+      const uint32_t kw[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+      const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      float kf[8], vf[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = unpack16<kBf16>(kw[j]), b = unpack16<kBf16>(vw[j]);
+        kf[2 * j] = a.x, kf[2 * j + 1] = a.y;
+        vf[2 * j] = b.x, vf[2 * j + 1] = b.y;
+      }
+      uint32_t ke, ve;
+      const uint2 kc = quantise_row<kLanes>(kf, ke), vc = quantise_row<kLanes>(vf, ve);
+      if (ok) {
+        reinterpret_cast<uint2*>(kd)[lane] = kc;
+        reinterpret_cast<uint2*>(vd)[lane] = vc;
+        if (lane == 0) {
+          const long long at = (page * p.c.heads + head[i]) * p.c.page_size + place;
+          p.c.k_scale[at] = static_cast<uint8_t>(ke);
+          p.c.v_scale[at] = static_cast<uint8_t>(ve);
+        }
       }
     }
   }
@@ -104,53 +117,80 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p)
 // read
 // ---------------------------------------------------------------------------
 
-// Eight values of a cached row, as eight 16-bit values of the output type.
-template <bool kE4M3, bool kBf16>
-__device__ __forceinline__ uint4 read_eight(const uint8_t* row, int lane, const uint8_t* scale) {
-  if constexpr (!kE4M3) {
-    return __ldg(reinterpret_cast<const uint4*>(row) + lane);
-  } else {
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-    const float s = scale_value(__ldg(scale));
-    const uint32_t two[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
-    uint32_t r[4];
+// Eight codes of a row with scale s as 16-bit values.
+template <bool kBf16>
+__device__ __forceinline__ uint4 widen(uint2 c, float s) {
+  const uint32_t two[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
+  uint32_t r[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
-      // exact in bf16 down to its subnormals; fp16 rounds outside its range
-      r[j] = pack16<kBf16>(f.x * s, f.y * s);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+    // exact in bf16 down to its subnormals; fp16 rounds outside its range
+    r[j] = pack16<kBf16>(f.x * s, f.y * s);
   }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Thread -> (position, lane) of one (sequence, head); blockIdx.y walks those.
+// A thread takes one lane (eight elements) of kReadRows positions of one
+// (sequence, head), their loads in flight together: a length, a page and then
+// the row are three loads one after another, which single rows to a thread
+// would wait for many times over.  blockIdx.y walks the sequences and heads.
+constexpr int kReadRows = 4;
+
 template <int D, bool kE4M3, bool kBf16>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 8, kBlockRows = kThreads / kLanes;
   const int lane = threadIdx.x % kLanes;
-  const int n = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  if (n >= p.max_len) return;
+  const int n0 = blockIdx.x * (kReadRows * kBlockRows) + threadIdx.x / kLanes;
   const long long bh_count = static_cast<long long>(p.t.batch) * p.c.heads;
   for (long long bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
-    const int b = static_cast<int>(bh / p.c.heads), h = static_cast<int>(bh % p.c.heads);
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    if (n < table_length(p.t, p.c.page_shift, b)) {
-      const long long page = table_page(p.t, p.c.num_pages, b, n >> p.c.page_shift);
-      if (page >= 0) {
-        const int place = n & (p.c.page_size - 1);
-        const long long at = (page * p.c.heads + h) * p.c.page_size + place;
-        k = read_eight<kE4M3, kBf16>(p.c.k + page * p.c.k_page + h * p.c.k_head +
-                                         place * p.c.k_token,
-                                     lane, p.c.k_scale + at);
-        v = read_eight<kE4M3, kBf16>(p.c.v + page * p.c.v_page + h * p.c.v_head +
-                                         place * p.c.v_token,
-                                     lane, p.c.v_scale + at);
+    const int b = static_cast<int>(bh / p.c.heads);
+    const int h = static_cast<int>(bh - static_cast<long long>(b) * p.c.heads);
+    const int len = min(table_length(p.t, p.c.page_shift, b), p.max_len);
+    const uint8_t* k0 = p.c.k + h * p.c.k_head;
+    const uint8_t* v0 = p.c.v + h * p.c.v_head;
+    long long page[kReadRows];
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      const int n = n0 + i * kBlockRows;
+      page[i] = n < len ? table_page(p.t, p.c.num_pages, b, n >> p.c.page_shift) : -1;
+    }
+    uint4 k[kReadRows], v[kReadRows];
+    uint32_t ks[kReadRows], vs[kReadRows];
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      k[i] = v[i] = make_uint4(0, 0, 0, 0);
+      ks[i] = vs[i] = 0;
+      if (page[i] >= 0) {
+        const int place = (n0 + i * kBlockRows) & (p.c.page_size - 1);
+        const uint8_t* kr = k0 + page[i] * p.c.k_page + place * p.c.k_token;
+        const uint8_t* vr = v0 + page[i] * p.c.v_page + place * p.c.v_token;
+        if constexpr (kE4M3) {
+          const long long at = (page[i] * p.c.heads + h) * p.c.page_size + place;
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(kr) + lane);
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(vr) + lane);
+          k[i].x = a.x, k[i].y = a.y;
+          v[i].x = c.x, v[i].y = c.y;
+          ks[i] = __ldg(p.c.k_scale + at);
+          vs[i] = __ldg(p.c.v_scale + at);
+        } else {
+          k[i] = __ldg(reinterpret_cast<const uint4*>(kr) + lane);
+          v[i] = __ldg(reinterpret_cast<const uint4*>(vr) + lane);
+        }
       }
     }
-    const long long out = (bh * p.max_len + n) * kLanes + lane;
-    reinterpret_cast<uint4*>(p.k)[out] = k;
-    reinterpret_cast<uint4*>(p.v)[out] = v;
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      const int n = n0 + i * kBlockRows;
+      if (n >= p.max_len) break;
+      if constexpr (kE4M3) {
+        k[i] = widen<kBf16>(make_uint2(k[i].x, k[i].y), scale_value(ks[i]));
+        v[i] = widen<kBf16>(make_uint2(v[i].x, v[i].y), scale_value(vs[i]));
+      }
+      const long long out = (bh * p.max_len + n) * kLanes + lane;
+      reinterpret_cast<uint4*>(p.k)[out] = k[i];
+      reinterpret_cast<uint4*>(p.v)[out] = v[i];
+    }
   }
 }
 
@@ -230,8 +270,9 @@ int launched() { return cudaGetLastError() == cudaSuccess ? 0 : -4; }
 }  // namespace
 
 int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
-  const long long threads = static_cast<long long>(p.tokens) * p.c.heads * (d / 8);
-  const unsigned grid = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+  const long long rows = static_cast<long long>(p.tokens) * p.c.heads;
+  const int each = kWriteRows * kThreads / (d / 8);
+  const unsigned grid = static_cast<unsigned>((rows + each - 1) / each);
 #define FAT_RUN(D, E, B) kv_write_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
   FAT_PICK(d, e4m3, bf16, FAT_RUN);
 #undef FAT_RUN
@@ -239,7 +280,7 @@ int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, cudaStrea
 }
 
 int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
-  const int rows = kThreads / (d / 8);
+  const int rows = kReadRows * kThreads / (d / 8);
   const long long bh = static_cast<long long>(p.t.batch) * p.c.heads;
   const dim3 grid((p.max_len + rows - 1) / rows, static_cast<unsigned>(bh < 65535 ? bh : 65535));
 #define FAT_RUN(D, E, B) kv_read_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
