@@ -125,7 +125,8 @@ struct WriteParams {
   int tokens;
   unsigned int* error_word;
 };
-int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream);
+int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, int sms,
+                    cudaStream_t stream);
 
 struct ReadParams {
   CacheView c;
@@ -134,7 +135,8 @@ struct ReadParams {
   uint8_t* v;
   int max_len;
 };
-int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream);
+int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, int sms,
+                   cudaStream_t stream);
 
 struct BoundsParams {
   CacheView c;

@@ -85,6 +85,12 @@ int query_ok(const void* q, int q_dtype, long long batch_stride, long long head_
   return FAT_OK;
 }
 
+// SMs of a device, 0 if CUDA does not say
+int sm_count(int dev) {
+  int n = 0;
+  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+}
+
 int status(int launch) { return launch == 0 ? FAT_OK : FAT_ERR_LAUNCH; }
 
 }  // namespace
@@ -114,7 +120,9 @@ int fat_kv_write(const fat_kv_cache* cache, const void* k, const void* v, int dt
   p.v = static_cast<const uint8_t*>(v);
   p.slots = slots;
   p.tokens = tokens;
-  return status(fat::launch_kv_write(p, cache->d, e4m3, dtype == FAT_DTYPE_BF16, stream));
+  const int sms = sm_count(dev);
+  if (sms < 1) return FAT_ERR_LAUNCH;
+  return status(fat::launch_kv_write(p, cache->d, e4m3, dtype == FAT_DTYPE_BF16, sms, stream));
 }
 
 int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k, void* v,
@@ -132,7 +140,9 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
   p.k = static_cast<uint8_t*>(k);
   p.v = static_cast<uint8_t*>(v);
   p.max_len = max_len;
-  return status(fat::launch_kv_read(p, cache->d, e4m3, dtype == FAT_DTYPE_BF16, stream));
+  const int sms = sm_count(dev);
+  if (sms < 1) return FAT_ERR_LAUNCH;
+  return status(fat::launch_kv_read(p, cache->d, e4m3, dtype == FAT_DTYPE_BF16, sms, stream));
 }
 
 size_t fat_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int d) {
@@ -223,9 +233,8 @@ int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
   p.heads = kv_heads;
   p.group = q_heads / kv_heads;
   p.scores = scores;
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return FAT_ERR_LAUNCH;
+  const int sms = sm_count(dev);
+  if (sms < 1) return FAT_ERR_LAUNCH;
   return status(fat::launch_kv_scores(p, d, dtype == FAT_DTYPE_BF16, sms, stream));
 }
 

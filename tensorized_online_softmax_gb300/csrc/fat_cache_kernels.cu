@@ -49,9 +49,8 @@ __device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t& e) 
 
 // One lane per eight elements of a row; a thread takes that lane of kWriteRows
 // rows (token, head) of K and V, whose loads are all in flight together.
-constexpr int kWriteRows = 2;
-
-template <int D, bool kE4M3, bool kBf16>
+// (Two for large calls; one where that many threads would not fill the GPU.)
+template <int D, bool kE4M3, bool kBf16, int kWriteRows>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p) {
   constexpr int kLanes = D / 8, kBlockRows = kThreads / kLanes;
   const uint32_t lane = threadIdx.x % kLanes;
@@ -68,8 +67,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p)
     k[i] = v[i] = make_uint4(0, 0, 0, 0);
     if (row < rows) {
       slot[i] = __ldg(p.slots + t);
-      k[i] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + head[i] * p.k_head) + lane);
-      v[i] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + head[i] * p.v_head) + lane);
+      k[i] = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_token + head[i] * p.k_head) + lane);
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_token + head[i] * p.v_head) + lane);
     }
   }
 #pragma unroll
@@ -135,9 +134,8 @@ __device__ __forceinline__ uint4 widen(uint2 c, float s) {
 // (sequence, head), their loads in flight together: a length, a page and then
 // the row are three loads one after another, which single rows to a thread
 // would wait for many times over.  blockIdx.y walks the sequences and heads.
-constexpr int kReadRows = 4;
-
-template <int D, bool kE4M3, bool kBf16>
+// (Four for large calls; one where that many threads would not fill the GPU.)
+template <int D, bool kE4M3, bool kBf16, int kReadRows>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
   constexpr int kLanes = D / 8, kBlockRows = kThreads / kLanes;
   const int lane = threadIdx.x % kLanes;
@@ -188,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
         v[i] = widen<kBf16>(make_uint2(v[i].x, v[i].y), scale_value(vs[i]));
       }
       const long long out = (bh * p.max_len + n) * kLanes + lane;
-      reinterpret_cast<uint4*>(p.k)[out] = k[i];
-      reinterpret_cast<uint4*>(p.v)[out] = v[i];
+      __stcs(reinterpret_cast<uint4*>(p.k) + out, k[i]);
+      __stcs(reinterpret_cast<uint4*>(p.v) + out, v[i]);
     }
   }
 }
@@ -269,21 +267,35 @@ int launched() { return cudaGetLastError() == cudaSuccess ? 0 : -4; }
 
 }  // namespace
 
-int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
+// Rows to a thread: `most` if that still gives every SM two blocks, else one.
+static int rows_per_thread(long long rows, int d, int most, int sms) {
+  return rows * (d / 8) >= 2ll * most * kThreads * sms ? most : 1;
+}
+
+int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, int sms,
+                    cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.tokens) * p.c.heads;
-  const int each = kWriteRows * kThreads / (d / 8);
+  const int many = rows_per_thread(rows, d, 2, sms);
+  const int each = many * kThreads / (d / 8);
   const unsigned grid = static_cast<unsigned>((rows + each - 1) / each);
-#define FAT_RUN(D, E, B) kv_write_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
+#define FAT_RUN(D, E, B)                                              \
+  (many == 2 ? kv_write_kernel<D, E, B, 2><<<grid, kThreads, 0, stream>>>(p) \
+             : kv_write_kernel<D, E, B, 1><<<grid, kThreads, 0, stream>>>(p))
   FAT_PICK(d, e4m3, bf16, FAT_RUN);
 #undef FAT_RUN
   return launched();
 }
 
-int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, cudaStream_t stream) {
-  const int rows = kReadRows * kThreads / (d / 8);
+int launch_kv_read(const ReadParams& p, int d, bool e4m3, bool bf16, int sms,
+                   cudaStream_t stream) {
   const long long bh = static_cast<long long>(p.t.batch) * p.c.heads;
-  const dim3 grid((p.max_len + rows - 1) / rows, static_cast<unsigned>(bh < 65535 ? bh : 65535));
-#define FAT_RUN(D, E, B) kv_read_kernel<D, E, B><<<grid, kThreads, 0, stream>>>(p)
+  const int many = rows_per_thread(bh * p.max_len, d, 4, sms);
+  const int rows = many * kThreads / (d / 8);
+  const dim3 grid(p.max_len / rows + (p.max_len % rows != 0),
+                  static_cast<unsigned>(bh < 65535 ? bh : 65535));
+#define FAT_RUN(D, E, B)                                             \
+  (many == 4 ? kv_read_kernel<D, E, B, 4><<<grid, kThreads, 0, stream>>>(p) \
+             : kv_read_kernel<D, E, B, 1><<<grid, kThreads, 0, stream>>>(p))
   FAT_PICK(d, e4m3, bf16, FAT_RUN);
 #undef FAT_RUN
   return launched();
