@@ -659,63 +659,106 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 
 // The join of an item's parts: block (c, row) handles a row of the item that
 // starts, unfinished, in block c of decode_kernel.  Groups of lanes (four
-// columns each) take the parts in turn: a long sequence alone has a few dozen.
+// columns each) take the parts in turn, a batch of loads at a time, with a
+// running maximum: it is a chain of latencies, and each group's first part is
+// loaded together with the note of what is to be joined.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeParams p, int rows_per_block) {
-  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kBatch = 8;
   __shared__ float4 acc_s[kGroups][kLanes];
-  __shared__ float sum_s[kGroups];
-  grid_dep_wait();
-  const Join j = static_cast<const Join*>(p.workspace)[blockIdx.x];
-  if (j.last < 0) return;
+  __shared__ float sum_s[kGroups], top_s[kGroups];
   const int c0 = blockIdx.x, r = blockIdx.y;
-  const int blocks_of_rows = (p.group + rows_per_block - 1) / rows_per_block;
-  const int seq = p.per_head ? j.entry / p.c.heads : j.entry;
-  const int head = (p.per_head ? j.entry % p.c.heads : 0) + j.item / blocks_of_rows;
-  const int qr = (j.item % blocks_of_rows) * rows_per_block + r;
-  if (qr >= p.group) return;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const float* ws_lse =
       reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + kJoinBytes);
   const float4* ws_o = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(p.workspace) +
                                                        kJoinBytes + kLseBytes);
-  auto slot = [&](int c) { return (c * 2 + (c == c0 ? j.part : 0)) * kMaxRows + r; };
-  float m = -INFINITY;
-  for (int c = c0 + threadIdx.x % 32; c <= j.last; c += 32) m = fmaxf(m, ws_lse[slot(c)]);
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float base = m == -INFINITY ? 0.f : m;
-  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-  float l = 0.f;
+  // the group's first part: of block c0 + group (for c0 itself it can be either of the two)
+  const int ahead = min(c0 + group, static_cast<int>(gridDim.x) - 1) * 2 * kMaxRows + r;
+  grid_dep_wait();
+  const Join j = static_cast<const Join*>(p.workspace)[c0];
+  float lse0 = ws_lse[ahead];
+  float4 o0 = ws_o[static_cast<size_t>(ahead) * kLanes + lane];
+  if (group == 0) {
+    const float other = ws_lse[ahead + kMaxRows];
+    const float4 other_o = ws_o[static_cast<size_t>(ahead + kMaxRows) * kLanes + lane];
+    if (j.part) lse0 = other, o0 = other_o;
+  }
+  if (j.last < 0) return;
+  const int blocks_of_rows = (p.group + rows_per_block - 1) / rows_per_block;
+  const int seq = p.per_head ? j.entry / p.c.heads : j.entry;
+  const int h = j.item / blocks_of_rows;
+  const int head = p.per_head ? j.entry - seq * p.c.heads : h;
+  const int qr = (j.item - h * blocks_of_rows) * rows_per_block + r;
+  if (qr >= p.group) return;
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0 + group; c <= j.last; c += kGroups) {
-    const int at = slot(c);
-    const float w = ex2_approx(ws_lse[at] - base);
-    const float4 x = ws_o[static_cast<size_t>(at) * kLanes + lane];
+  auto add = [&](float lse, const float4& x, float base) {
+    const float w = ex2_approx(lse - base);
     l += w;
     acc.x = fmaf(w, x.x, acc.x);
     acc.y = fmaf(w, x.y, acc.y);
     acc.z = fmaf(w, x.z, acc.z);
     acc.w = fmaf(w, x.w, acc.w);
+  };
+  auto raise = [&](float to) {  // what is summed so far, relative to the maximum `to` >= m
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - to);
+    const bool none = m == -INFINITY && l == 0.f;  // (a NaN stays one)
+    m = to;
+    if (none) return;
+    l *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+  };
+  if (c0 + group <= j.last) {
+    m = fmaxf(lse0, m);
+    add(lse0, o0, m == -INFINITY ? 0.f : m);
+  }
+  for (int c = c0 + group + kGroups; c <= j.last; c += kGroups * kBatch) {
+    float lse[kBatch];
+    float4 x[kBatch];
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = min(c + i * kGroups, j.last) * 2 * kMaxRows + r;
+      lse[i] = ws_lse[at];
+      x[i] = ws_o[static_cast<size_t>(at) * kLanes + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
+    raise(top);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (c + i * kGroups <= j.last) add(lse[i], x[i], m == -INFINITY ? 0.f : m);
   }
   acc_s[group][lane] = acc;
-  if (lane == 0) sum_s[group] = l;
+  if (lane == 0) sum_s[group] = l, top_s[group] = m;
   __syncthreads();
   if (group == 0) {
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) top = fmaxf(top, top_s[i]);
+    raise(top);
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) {
+      if (c0 + i > j.last) break;
       const float4 x = acc_s[i][lane];
-      l += sum_s[i];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
+      const float f = ex2_approx(top_s[i] - (top == -INFINITY ? 0.f : top));
+      l = fmaf(sum_s[i], f, l);
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
     }
     const long long at = (static_cast<long long>(seq) * p.c.heads + head) * p.group + qr;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     reinterpret_cast<uint2*>(p.o)[at * kLanes + lane] =
         make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
-    if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+    if (lane == 0)
+      p.lse[at] = l == 0.f ? -INFINITY
+                           : ((top == -INFINITY ? 0.f : top) + log2f(l)) * 0.69314718055994531f;
   }
 }
 
