@@ -157,16 +157,15 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
 //
 // One block of threads per (sequence, cached head), whose warps hold adjacent
 // runs of the scores, as unsigned integers of the same order, in registers.
-// The num_blocks-th largest is found in two steps: a histogram of the leading
+// The num_blocks-th largest is found in two steps for 1025 to 8192 blocks: a histogram of the leading
 // 11 bits (four copies, as scores share leading bits and lanes would queue for
 // one bin) gives the bin that it is in, and a warp finds the other bits among
 // the keys of that bin, two at a time, by counting.  Then every warp writes its
 // chosen ones at its place: all larger ones, and of those equal to the
 // threshold the first.
 //
-// For up to 1024 blocks, and for more than 8192, all keys take part in the
-// counting (over 32768 they are read again in each step).  512 blocks: 1.4 us
-// less than with the histogram; 8192: 3.5 us more.
+// Up to 1024 blocks, and over 8192, all keys take part in the counting, two bits
+// at a time (over 32768 they are read again in each step).
 // ---------------------------------------------------------------------------
 
 // The order of the choice as unsigned integers: the newest blocks, the first
@@ -304,10 +303,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
                 for (int j = 0; j < 3; ++j) c[j] += k >= (value | ((j + 1u) << shift));
               }
               uint32_t digit = 0;
+              bool exact = false;
 #pragma unroll
-              for (int j = 0; j < 3; ++j)
-                digit += __reduce_add_sync(0xffffffffu, c[j]) >= rest;
+              for (int j = 0; j < 3; ++j) {
+                const uint32_t all = __reduce_add_sync(0xffffffffu, c[j]);
+                digit += all >= rest;
+                exact |= all == rest;
+              }
               value |= digit << shift;
+              if (exact) break;
             }
           }
           if (lane == 0) found[0] = value;
@@ -331,13 +335,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         }
         __syncthreads();  // (the other half is free: all have passed the barrier before)
         uint32_t digit = 0;
+        bool exact = false;
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           const uint32_t all =
               __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[odd][j][lane] : 0u);
           digit += all >= static_cast<uint32_t>(take);  // (the counts fall with j)
+          exact |= all == static_cast<uint32_t>(take);
         }
         threshold |= digit << shift;
+        if (exact) break;  // just the wanted number is at or above it (the same in all threads)
       }
     }
     // how many of each kind the warp holds
@@ -365,6 +372,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     int* out = p.blocks + bh * p.num_blocks;
     int* pages = p.pages + bh * p.list;
     const uint32_t below = (1u << lane) - 1u;
+    const int* table = p.t.pages + b * p.t.stride;
+    int page[kKeys ? kKeys : 1];  // loaded together: one latency, not one a round
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int r = 0; r < kKeys; ++r)
+        page[r] = base + r * 32 < blocks ? __ldg(table + base + r * 32) : 0;
+    }
 #pragma unroll
     for (int r = 0; r < (kKeys ? kKeys : rounds); ++r) {
       const uint32_t k = key(r);
@@ -376,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
       if (chosen) {
         const int i = base + r * 32, place = at + __popc(mask & below);
         out[place] = i;
-        pages[place] = __ldg(p.t.pages + b * p.t.stride + i);
+        pages[place] = kKeys ? page[kKeys ? r : 0] : __ldg(table + i);
         if (i == blocks - 1) newest = 1;
       }
       equal_rank += __popc(same_mask);

@@ -57,10 +57,6 @@ constexpr int kMaxRows = 16;
 constexpr size_t kJoinBytes = sizeof(Join) * kDecodeMaxBlocks;
 constexpr size_t kLseBytes = sizeof(float) * kDecodeMaxBlocks * 2 * kMaxRows;
 
-#ifndef FAT_SB
-#define FAT_SB 3
-#endif
-
 template <int D, int kNT, bool kE4M3>
 struct Layout {
   static constexpr int kRow = D * (kE4M3 ? 1 : 2);  // bytes
@@ -69,7 +65,7 @@ struct Layout {
   static constexpr int kScales = kE4M3 ? 32 : 0;
   // blocks on an SM (their registers allow no more), and a ring as deep as their share of the
   // SM's 228 KiB
-  static constexpr int kBlocks = kNT > 1 ? 2 : kStage < 8192 ? FAT_SB : 3;
+  static constexpr int kBlocks = kNT > 1 ? 2 : 3;
   static constexpr int kRoom = (228 * 1024 / kBlocks - 1024 - 1024) / kWarps;
   static constexpr int kFit = kRoom / (kStage + kScales);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -232,7 +228,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
     for (int e = lo; e < hi; ++e) mine += decode_tiles(table_length(p.t, p.c.page_shift, e));
     const long long upto = block_scan(mine, warp_sums, total);
     total *= copies;
-    share = decode_share(total, gridDim.x, p.least_tiles);
+    // (a 64-bit division is a few hundred cycles)
+    share = total <= 0x7fffffff - kDecodeMaxBlocks
+                ? decode_share(static_cast<int>(total), gridDim.x, p.least_tiles)
+                : decode_share(total, static_cast<int>(gridDim.x), p.least_tiles);
     begin = blockIdx.x * share;
     long long before = (upto - mine) * copies;
     if (begin >= before && begin < upto * copies) {
@@ -269,11 +268,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   };
   load_item();
   const int warp_row = warp * kRowsPerWarp;
-  auto next_page = [&]() {  // (checked where it is used)
-    const int row = load.tile * kDecodeTile + warp_row;
-    return row < load_len ? __ldg(load_pages + (row >> p.c.page_shift)) : 0;
+  // The pages of the warp's rows in 32 tiles from `window`, one to a lane: loaded at an item's
+  // start (and every 32 tiles) well before their use.  Checked where they are used.
+  int window = 0, window_page = 0;
+  auto load_window = [&]() {
+    window = load.tile;
+    const long long row = static_cast<long long>(load.tile + lane) * kDecodeTile + warp_row;
+    window_page = row < load_len ? __ldg(load_pages + (row >> p.c.page_shift)) : 0;
   };
-  int page = next_page();
+  load_window();
   int loaded = 0;
   uint32_t stage_in = ring;  // of the next copy
   const int r0 = lane / L::kChunks, c0 = lane % L::kChunks;  // the lane's first chunk
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
     if (row < load_len) {
       const uint32_t stage = stage_in;
       const int place = row & (p.c.page_size - 1);
+      int page = __shfl_sync(0xffffffffu, window_page, load.tile - window);
       int valid = min(kRowsPerWarp, load_len - row);
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.num_pages)) {
         atomicOr(p.t.error_word, kErrIndex);
@@ -338,8 +342,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       if (load.tile == 0) {
         if (entry) load_len = enter(p, load);
         load_item();
+        load_window();
+      } else if (load.tile == window + 32) {
+        load_window();
       }
-      page = next_page();  // used by the next issue(): its latency is hidden
     }
   };
 #pragma unroll 1
@@ -606,38 +612,62 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           }
         }
         __syncthreads();
-        const int d = threadIdx.x % D;
-#pragma unroll 1
-        for (int col = threadIdx.x / D; col < 8; col += kThreads / D) {
+        // two heads to a warp, D / 32 columns of both to a lane
+        constexpr int kPer = D / 32;
+#pragma unroll
+        for (int i = 0; i < 8 / kWarps; ++i) {
+          const int col = warp + i * kWarps;
           const int qr = it.row0 + n * 8 + col;  // query head within the group
-          if (qr >= p.group) break;
-          const float* r = join_r + n * 8 + col;
-          float m = -INFINITY, mv = -INFINITY;
+          if (qr < p.group) {
+            const float* r = join_r + n * 8 + col;
+            float m = -INFINITY, mv = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            m = fmaxf(m, r[w * kMaxRows]);
-            mv = fmaxf(mv, r[(kWarps + w) * kMaxRows]);
-          }
-          const float base = m == -INFINITY ? 0.f : m, base_v = mv == -INFINITY ? 0.f : mv;
-          float l = 0.f, acc = 0.f;
+            for (int w = 0; w < kWarps; ++w) {
+              m = fmaxf(m, r[w * kMaxRows]);
+              mv = fmaxf(mv, r[(kWarps + w) * kMaxRows]);
+            }
+            const float base = m == -INFINITY ? 0.f : m, base_v = mv == -INFINITY ? 0.f : mv;
+            float l = 0.f, acc[kPer] = {};
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            l += r[(2 * kWarps + w) * kMaxRows] * ex2_approx(r[w * kMaxRows] - base);
-            const float* src = reinterpret_cast<const float*>(smem + w * L::kRing + used);
-            acc += src[col * D + (d ^ (8 * (col >> 1)))] *
-                   ex2_approx(r[(kWarps + w) * kMaxRows] - base_v);
-          }
-          const float out = l == 0.f ? 0.f : acc / l * exp2f(base_v - base);
-          const float lse = l == 0.f ? -INFINITY : base + log2f(l);
-          if (whole) {
-            const long long at =
-                (static_cast<long long>(it.seq) * p.c.heads + it.head) * p.group + qr;
-            reinterpret_cast<uint16_t*>(p.o)[at * D + d] =
-                static_cast<uint16_t>(pack16<kBf16>(out, 0.f));
-            if (d == 0) p.lse[at] = lse * 0.69314718055994531f;
-          } else {
-            ws_o[(n * 8 + col) * D + d] = out;
-            if (d == 0) ws_lse[n * 8 + col] = lse;
+            for (int w = 0; w < kWarps; ++w) {
+              l += r[(2 * kWarps + w) * kMaxRows] * ex2_approx(r[w * kMaxRows] - base);
+              const float f = ex2_approx(r[(kWarps + w) * kMaxRows] - base_v);
+              const float* src = reinterpret_cast<const float*>(smem + w * L::kRing + used) +
+                                 col * D + ((lane * kPer) ^ (8 * (col >> 1)));
+              if constexpr (kPer == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(src);
+                acc[0] = fmaf(x.x, f, acc[0]);
+                acc[1] = fmaf(x.y, f, acc[1]);
+                acc[2] = fmaf(x.z, f, acc[2]);
+                acc[3] = fmaf(x.w, f, acc[3]);
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                acc[0] = fmaf(x.x, f, acc[0]);
+                acc[1] = fmaf(x.y, f, acc[1]);
+              }
+            }
+            const float scale = l == 0.f ? 0.f : exp2f(base_v - base) / l;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) acc[j] *= scale;
+            const float lse = l == 0.f ? -INFINITY : base + log2f(l);
+            if (whole) {
+              const long long at =
+                  (static_cast<long long>(it.seq) * p.c.heads + it.head) * p.group + qr;
+              uint32_t* out = reinterpret_cast<uint32_t*>(p.o) + (at * D + lane * kPer) / 2;
+              if constexpr (kPer == 4)
+                *reinterpret_cast<uint2*>(out) =
+                    make_uint2(pack16<kBf16>(acc[0], acc[1]), pack16<kBf16>(acc[2], acc[3]));
+              else
+                *out = pack16<kBf16>(acc[0], acc[1]);
+              if (lane == 0) p.lse[at] = lse * 0.69314718055994531f;
+            } else {
+              float* out = ws_o + (n * 8 + col) * D + lane * kPer;
+              if constexpr (kPer == 4)
+                *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+              else
+                *reinterpret_cast<float2*>(out) = make_float2(acc[0], acc[1]);
+              if (lane == 0) ws_lse[n * 8 + col] = lse;
+            }
           }
         }
         __syncthreads();

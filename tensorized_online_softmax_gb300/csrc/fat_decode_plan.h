@@ -29,8 +29,9 @@ FAT_HD int decode_tiles(int len) {
 
 // Tiles of one block: an equal share, but at least `least` (a split costs the
 // join of its parts).
-FAT_HD long long decode_share(long long total, int blocks, int least) {
-  const long long n = (total + blocks - 1) / blocks;
+template <typename T>
+FAT_HD T decode_share(T total, int blocks, int least) {
+  const T n = (total + blocks - 1) / blocks;
   return n > least ? n : least;
 }
 
@@ -44,7 +45,8 @@ FAT_HD DecodePlace decode_place(int entry, long long offset, int tiles) {
   DecodePlace p;
   p.entry = entry;
   p.tiles = tiles;
-  p.item = static_cast<int>(offset / tiles);
+  p.item = offset <= 0x7fffffff ? static_cast<int>(offset) / tiles
+                                : static_cast<int>(offset / tiles);
   p.tile = static_cast<int>(offset - static_cast<long long>(p.item) * tiles);
   return p;
 }
