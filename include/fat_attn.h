@@ -373,8 +373,10 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
  * q_heads].  A sequence of length 0 gives o = 0 and lse = -inf.
  * workspace: at least fat_attn_decode_workspace_bytes(...) bytes of device
  * memory, 16-byte aligned, any contents; calls sharing it must not overlap on
- * the device.
+ * the device.  It may be NULL if width * page_size <= FAT_DECODE_DIRECT: no
+ * sequence is split then.
  */
+#define FAT_DECODE_DIRECT 512
 int fat_attn_decode_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
                           int dtype, long long q_batch_stride, long long q_head_stride,
                           int q_heads, float scale, void* o, float* lse, void* workspace,

@@ -7,6 +7,9 @@
 
 #include "../../include/fat_attn.h"
 #include "fat_cache.cuh"
+#include "fat_decode_plan.h"
+
+static_assert(FAT_DECODE_DIRECT == fat::kDirectTiles * fat::kDecodeTile, "one rule");
 
 namespace {
 
@@ -182,7 +185,9 @@ int fat_attn_decode_paged(const fat_kv_cache* cache, const fat_page_table* table
   int st = decode_common(cache, table, q, dtype, q_batch_stride, q_head_stride, q_heads, scale, o,
                          lse, &p);
   if (st != FAT_OK) return st;
-  if (!workspace || workspace_bytes < fat::decode_workspace_bytes(cache->d))
+  const bool direct =
+      (static_cast<long long>(table->width) << p.c.page_shift) <= FAT_DECODE_DIRECT;
+  if (!direct && (!workspace || workspace_bytes < fat::decode_workspace_bytes(cache->d)))
     return FAT_ERR_INVALID_ARG;
   if (!aligned(workspace, 16)) return FAT_ERR_ALIGNMENT;
   int dev = 0;

@@ -830,7 +830,7 @@ int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
   const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
   const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
   const long long tiles = (positions + kDecodeTile - 1) / kDecodeTile;
-  if (tiles <= kDirectTiles && static_cast<long long>(copies) * p.t.batch <= 0x7fffffffll) {
+  if (tiles <= kDirectTiles) {  // (the items are at most the query heads: below 2^31)
     DecodeParams one = p;
     one.direct = 1;
     const unsigned items = static_cast<unsigned>(copies) * static_cast<unsigned>(p.t.batch);

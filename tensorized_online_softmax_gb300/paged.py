@@ -66,6 +66,7 @@ def declare(lib) -> None:
 _WIDE = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
 _CACHE = {**_WIDE, torch.float8_e4m3fn: DTYPES["e4m3"]}
 _E4M3 = DTYPES["e4m3"]
+_DIRECT = 512  # FAT_DECODE_DIRECT: positions of a table that need no workspace
 _HERE = contextlib.nullcontext()
 
 # The checks below run for every call of a serving loop, where a few microseconds count: each
@@ -96,8 +97,8 @@ def _rows(name, t, shape, writable):
     a, b, c, row = t.stride()
     if row != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if 1 in shape:
-        a, b, c = (x if n > 1 else 0 for x, n in zip((a, b, c), shape))
+    if shape[0] == 1 or shape[1] == 1:  # (a page has 16 rows at least)
+        a, b = a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
     if writable and not (a and b and c) and any(
             n > 1 and not x for x, n in zip((a, b, c), shape)):
         raise ValueError(f"{name} is a broadcast view: its rows share memory")
@@ -135,13 +136,17 @@ def _cache(k, v, k_scale, v_scale, writable=False):
 
 
 def _table(page_table, seq_lens, device):
-    _tensor("page_table", page_table, (torch.int32,), 2, device)
-    _tensor("seq_lens", seq_lens, (torch.int32,), 1, device)
+    if not (isinstance(page_table, torch.Tensor) and isinstance(seq_lens, torch.Tensor)
+            and page_table.device == seq_lens.device == device
+            and page_table.dtype is seq_lens.dtype is torch.int32
+            and page_table.dim() == 2 and seq_lens.dim() == 1):
+        _wrong("page_table", page_table, (torch.int32,), 2, device)
+        _wrong("seq_lens", seq_lens, (torch.int32,), 1, device)
     batch, width = page_table.shape
     stride, step = page_table.stride()
     if seq_lens.shape[0] != batch or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be contiguous [B], page_table [B, width]")
-    if width > 1 and step != 1:
+    if step != 1 and width > 1:
         raise ValueError("the rows of page_table must be contiguous")
     return FatPageTable(page_table.data_ptr(), stride if batch > 1 else width, width, batch,
                         seq_lens.data_ptr())
@@ -278,14 +283,15 @@ def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, scale, k_scale,
 
 
 def _workspace(workspace, nbytes, device, fresh):
+    """The workspace's address and size; allocated if not given."""
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         fresh.append(workspace)
-        return workspace
+        return workspace.data_ptr(), nbytes
     _tensor("workspace", workspace, (torch.uint8,), 1, device)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace
+    return workspace.data_ptr(), workspace.numel()
 
 
 def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale: float | None = None, *,
@@ -296,16 +302,19 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale: float | 
     e4m3), ``q_heads`` a multiple of the cached heads.  ``scale`` defaults to
     1/sqrt(d).  Returns ``(o, lse)``: o of q's shape and type, lse fp32
     [B, q_heads]; a sequence of length 0 gives zeros and -inf.  ``workspace``:
-    a CUDA uint8 tensor of :func:`attn_decode_workspace_bytes` bytes.
+    a CUDA uint8 tensor of :func:`attn_decode_workspace_bytes` bytes; a table for
+    512 positions at most needs none.
     """
     lib = load_library()
     c, t, query, scale, o, lse, fresh = _decode_arguments(
         q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out)
-    nbytes = lib.fat_attn_decode_workspace_bytes(t.batch, q.shape[1], c.heads, c.d)
-    workspace = _workspace(workspace, nbytes, q.device, fresh)
+    if workspace is None and t.width * c.page_size <= _DIRECT:
+        work = None, 0
+    else:
+        work = _workspace(workspace, lib.fat_attn_decode_workspace_bytes(
+            t.batch, query[4], c.heads, c.d), q.device, fresh)
     with _on(q.device):
-        _done(lib.fat_attn_decode_paged(c, t, *query, scale, o.data_ptr(), lse.data_ptr(),
-                                        workspace.data_ptr(), workspace.numel(),
+        _done(lib.fat_attn_decode_paged(c, t, *query, scale, o.data_ptr(), lse.data_ptr(), *work,
                                         _stream(stream, q.device, fresh)),
               "fat_attn_decode_paged")
     return o, lse
@@ -402,12 +411,12 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
         blocks = _output("blocks", out[2], shape, torch.int32, device)
     nbytes = lib.fat_attn_decode_sparse_workspace_bytes(t.batch, q.shape[1], c.heads, c.d,
                                                         num_blocks)
-    workspace = _workspace(workspace, nbytes, device, fresh)
+    work = _workspace(workspace, nbytes, device, fresh)
     with _on(device):
         _done(lib.fat_attn_decode_sparse(
             c, t, *query, scores.data_ptr(), num_blocks, int(first_blocks), int(last_blocks),
-            scale, o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _stream(stream, device, fresh)), "fat_attn_decode_sparse")
+            scale, o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work,
+            _stream(stream, device, fresh)), "fat_attn_decode_sparse")
     return o, lse, blocks
 
 

@@ -470,7 +470,7 @@ def test_calls_on_two_streams_at_once(cuda_device):
 
 
 def test_refusals(cuda_device):
-    cache, table, lens, q = setup([40], 2, 2, 16, 64, "bf16", "bf16")
+    cache, table, lens, q = setup([40], 2, 2, 16, 64, "bf16", "bf16", width=40)
     table, lens, q = table.cuda(), lens.cuda(), q.cuda()
     good = dict(q=q, k_cache=cache.k, v_cache=cache.v, page_table=table, seq_lens=lens)
     for bad in (dict(q=q[:, :3]), dict(q=q.half()), dict(q=q.float()), dict(q=q.cpu()),

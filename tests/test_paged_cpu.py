@@ -32,8 +32,9 @@ def cache(**kw):
 
 
 def table(**kw):
-    return FatPageTable(**{**dict(pages=0x50000, stride=8, width=8, batch=3, seq_lens=0x60000),
-                           **kw})
+    # (room for 1024 positions: more than a call without workspace takes)
+    return FatPageTable(**{**dict(pages=0x50000, stride=64, width=64, batch=3,
+                                  seq_lens=0x60000), **kw})
 
 
 BAD_CACHES = [
@@ -51,7 +52,7 @@ BAD_V = [(dict(v=None), "INVALID_ARG"), (dict(v=0x20004), "ALIGNMENT"),
          (dict(v_page_stride=4), "ALIGNMENT"), (dict(dtype=E4M3, v_scale=None), "INVALID_ARG")]
 BAD_TABLES = [(dict(pages=None), "INVALID_ARG"), (dict(seq_lens=None), "INVALID_ARG"),
               (dict(width=0), "INVALID_ARG"), (dict(batch=0), "INVALID_ARG"),
-              (dict(stride=7), "INVALID_ARG"), (dict(pages=0x50002), "ALIGNMENT"),
+              (dict(stride=63), "INVALID_ARG"), (dict(pages=0x50002), "ALIGNMENT"),
               (dict(seq_lens=0x60001), "ALIGNMENT")]
 BAD_QUERIES = [(dict(q=None), "INVALID_ARG"), (dict(q=0x70008), "ALIGNMENT"),
                (dict(dtype=E4M3), "INVALID_ARG"), (dict(batch_stride=1028), "ALIGNMENT"),
@@ -104,6 +105,9 @@ def test_good_arguments_reach_the_device_check(lib):
         assert call(lib, c=e4m3, dtype=FP16) in REACHED, call.__name__
     assert bounds(lib, c=cache(v=None)) in REACHED
     assert write(lib, tokens=0) == fat.FAT_OK
+    # 32 pages of 16 positions: no sequence is split, and no workspace is needed
+    assert decode(lib, t=table(width=32), work=None, size=0) in REACHED
+    refused(decode(lib, t=table(width=33), work=None, size=0), "INVALID_ARG")
 
 
 @pytest.mark.parametrize("kw,name", BAD_CACHES, ids=str)
