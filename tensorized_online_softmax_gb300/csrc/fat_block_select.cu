@@ -20,11 +20,20 @@ __device__ __forceinline__ int blocks_of(const TableView& t, int page_shift, int
 // of 2 d terms, [q-, q+] . [lo, hi], so the scores of 16 blocks for 8 query
 // heads are m16n8k16 MMAs over the blocks' bounds, which lie in memory as the
 // rows of that matrix.  Each byte of them is used once: the kernel is bound by
-// memory, and loads straight into the MMA's fragments, 16 bytes a lane: the
-// order of the columns within a row is free as long as both operands agree, so
-// a lane takes the eight adjacent ones of its 16 bytes.
+// memory.  A warp keeps a ring of tiles of 16 blocks in shared memory, filled by
+// asynchronous copies, and reads 16 bytes a lane from it as the MMA's fragment:
+// the order of the columns within a row is free as long as both operands agree,
+// so a lane takes the eight adjacent ones of its 16 bytes.
 // ---------------------------------------------------------------------------
-constexpr int kScoreWarps = 4;
+constexpr int kScoreWarps = 4, kScoreStages = 3;
+
+template <int D>
+struct ScoreLayout {
+  static constexpr int kRow = 4 * D;            // bytes of a block's bounds
+  static constexpr int kCopies = kRow / 16;     // 16-byte pieces of a row: 32 or 16
+  static constexpr int kStage = 16 * kRow;      // a tile
+  static constexpr int kSmem = kScoreWarps * kScoreStages * kStage;
+};
 
 template <bool kBf16>
 __device__ __forceinline__ void score_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -43,24 +52,72 @@ __device__ __forceinline__ void score_mma(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Where 16-byte piece c of row r of a tile goes: the halves of a 128-byte line
+// change places in odd rows, so that the eight lanes that are served together
+// (four adjacent pieces of two rows) meet no bank twice.
+__device__ __forceinline__ uint32_t score_piece(int row_bytes, int r, int c) {
+  return static_cast<uint32_t>(r * row_bytes + ((c ^ ((r & 1) << 2)) << 4));
+}
+
 // A warp takes `tiles` tiles of 16 blocks, all of one (sequence, cached head);
 // the heads of the group go by eight.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreParams p, int tiles) {
-  constexpr int kChunks = 2 * D / 32;  // 32 columns of a row: one 16-byte load of four lanes
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreParams p, int tiles) {
+  using L = ScoreLayout<D>;
+  constexpr int kChunks = 2 * D / 32;  // 32 columns of a row: 16 bytes of four lanes
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
+  const uint32_t ring = smem_u32(smem) + warp * kScoreStages * L::kStage;
   const long long bh_count = static_cast<long long>(p.t.batch) * p.heads;
   for (long long bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
-    const int b = static_cast<int>(bh / p.heads), h = static_cast<int>(bh - static_cast<long long>(b) * p.heads);
+    const int b = static_cast<int>(bh / p.heads);
+    const int h = static_cast<int>(bh - static_cast<long long>(b) * p.heads);
     int len;
     const int blocks = blocks_of(p.t, p.page_shift, b, len);
     const int first = (blockIdx.x * kScoreWarps + warp) * tiles * 16;
-    const int end = min(first + tiles * 16, p.t.width);
+    const int end = min(first + tiles * 16, p.t.width), stop = min(end, blocks);
     for (int head0 = 0; head0 < p.group; head0 += 8) {
+      // the pages of 32 blocks (two tiles), one to a lane, a step ahead
+      auto pages_at = [&](int i0) {
+        const int i = i0 + lane;
+        return i < stop ? table_page(p.t, p.num_pages, b, i) : -1;
+      };
+      int page = pages_at(first), page_next = pages_at(first + 32);
+      int loaded = first;
+      uint32_t stage_in = ring, stage_out = ring;
+      auto issue = [&]() {
+        if (loaded < stop) {
+          // (a row without a page, behind the end or flagged, is filled with zeros)
+          constexpr int kRows = 32 / L::kCopies;  // that one copy of the warp covers
+          const int mine = lane / L::kCopies, c = lane % L::kCopies;
+#pragma unroll
+          for (int r0 = 0; r0 < 16; r0 += kRows) {
+            const int r = r0 + mine;
+            const int pg = __shfl_sync(0xffffffffu, page, ((loaded - first) & 16) + r);
+            const uint8_t* from =
+                p.bounds + (static_cast<long long>(max(pg, 0)) * p.heads + h) * L::kRow + c * 16;
+            const uint32_t bytes = pg >= 0 ? 16u : 0u;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             stage_in + score_piece(L::kRow, r, c)),
+                         "l"(from), "r"(bytes)
+                         : "memory");
+          }
+          if ((loaded - first) & 16) {
+            page = page_next;
+            page_next = pages_at(loaded + 48);
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        loaded += 16;
+        stage_in += L::kStage;
+        if (stage_in == ring + kScoreStages * L::kStage) stage_in = ring;
+      };
+#pragma unroll 1
+      for (int i = 0; i < kScoreStages - 1; ++i) issue();
       // q- and q+ of head g, as the other operand's fragments
       uint32_t qf[kChunks][4];
-      if (first < blocks) {
+      if (first < stop) {
         const bool in = head0 + g < p.group;
         const uint4* q = reinterpret_cast<const uint4*>(
             p.q + b * p.q_batch + (h * p.group + head0 + (in ? g : 0)) * p.q_head);
@@ -76,61 +133,32 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
           }
         }
       }
-      // units of four chunks, one ahead in registers; the pages two tiles ahead
-      constexpr int kUnits = kChunks / 4;
-      const int stop = min(end, blocks);
-      int page[2];
-      auto pages_at = [&](int i0) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = i0 + g + 8 * r;
-          page[r] = i < stop ? table_page(p.t, p.num_pages, b, i) : 0;
-        }
-      };
-      const uint4* row[2];
-      auto rows_of_pages = [&]() {  // (a flagged page: its score is unspecified)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          row[r] = reinterpret_cast<const uint4*>(p.bounds) +
-                   (static_cast<long long>(max(page[r], 0)) * p.heads + h) * (D / 4) + t;
-      };
-      uint4 x[2][4], y[2][4];
-      auto load = [&](uint4(&to)[2][4], int unit) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          to[0][c] = __ldg(row[0] + (unit * 4 + c) * 4);
-          to[1][c] = __ldg(row[1] + (unit * 4 + c) * 4);
-        }
-      };
-      if (first < stop) {
-        pages_at(first);
-        rows_of_pages();
-        load(x, 0);
-        pages_at(first + 16);
-      }
 #pragma unroll 1
       for (int i0 = first; i0 < end; i0 += 16) {
         float s[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (i0 < stop) {
+          issue();
+          asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+          __syncwarp();
           float acc[2][4] = {};
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            if (u + 1 < kUnits) {
-              load(y, u + 1);
-            } else if (i0 + 16 < stop) {
-              rows_of_pages();
-              load(y, 0);
-              pages_at(i0 + 32);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t(&f)[4] = qf[u * 4 + c];
-              score_mma<kBf16>(acc[0], x[0][c].x, x[1][c].x, x[0][c].y, x[1][c].y, f[0], f[1]);
-              score_mma<kBf16>(acc[1], x[0][c].z, x[1][c].z, x[0][c].w, x[1][c].w, f[2], f[3]);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[0][c] = y[0][c], x[1][c] = y[1][c];
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t x[4], y[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(stage_out + score_piece(L::kRow, g, 4 * c + t))
+                         : "memory");
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "r"(stage_out + score_piece(L::kRow, g + 8, 4 * c + t))
+                         : "memory");
+            const uint32_t(&f)[4] = qf[c];
+            score_mma<kBf16>(acc[0], x[0], y[0], x[1], y[1], f[0], f[1]);
+            score_mma<kBf16>(acc[1], x[2], y[2], x[3], y[3], f[2], f[3]);
           }
+          __syncwarp();  // the stage may be filled again
+          stage_out += L::kStage;
+          if (stage_out == ring + kScoreStages * L::kStage) stage_out = ring;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (head0 + 2 * t + (j & 1) < p.group && i0 + g + 8 * (j >> 1) < blocks)
@@ -421,23 +449,37 @@ int run_select(const SelectParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_kv_scores(const ScoreParams& p, int d, bool bf16, int sms, cudaStream_t stream) {
+template <int D, bool kBf16>
+static int run_scores(const ScoreParams& p, int dev, int sms, cudaStream_t stream) {
+  using L = ScoreLayout<D>;
+  static std::once_flag once[kMaxDevices];
+  static bool ready[kMaxDevices];
+  std::call_once(once[dev], [&] {
+    ready[dev] = cudaFuncSetAttribute(score_kernel<D, kBf16>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      L::kSmem) == cudaSuccess;
+  });
+  if (!ready[dev]) return -4;
   const long long bh = static_cast<long long>(p.t.batch) * p.heads;
-  // tiles to a warp: as many as leave 16 warps for each SM (q is loaded once for them), 4 at most
-  const int row_tiles = (p.t.width + 15) / 16;
-  long long tiles = bh * row_tiles / (16ll * sms);
-  tiles = tiles < 1 ? 1 : tiles > 4 ? 4 : tiles;
+  // tiles to a warp: as many as leave eight warps for each SM (the ring fills and q is loaded
+  // once for them), 8 at most
+  const int row_tiles = p.t.width / 16 + (p.t.width % 16 != 0);
+  long long tiles = bh * row_tiles / (8ll * sms);
+  tiles = tiles < 1 ? 1 : tiles > 8 ? 8 : tiles;
   const long long per_block = tiles * kScoreWarps;
   const dim3 grid(static_cast<unsigned>((row_tiles + per_block - 1) / per_block),
                   static_cast<unsigned>(bh < 65535 ? bh : 65535));
-  const int n = static_cast<int>(tiles);
-  if (d == 128)
-    bf16 ? score_kernel<128, true><<<grid, 32 * kScoreWarps, 0, stream>>>(p, n)
-         : score_kernel<128, false><<<grid, 32 * kScoreWarps, 0, stream>>>(p, n);
-  else
-    bf16 ? score_kernel<64, true><<<grid, 32 * kScoreWarps, 0, stream>>>(p, n)
-         : score_kernel<64, false><<<grid, 32 * kScoreWarps, 0, stream>>>(p, n);
+  score_kernel<D, kBf16><<<grid, 32 * kScoreWarps, L::kSmem, stream>>>(p, static_cast<int>(tiles));
   return launched();
+}
+
+int launch_kv_scores(const ScoreParams& p, int d, bool bf16, int dev, int sms,
+                     cudaStream_t stream) {
+  if (d == 128)
+    return bf16 ? run_scores<128, true>(p, dev, sms, stream)
+                : run_scores<128, false>(p, dev, sms, stream);
+  return bf16 ? run_scores<64, true>(p, dev, sms, stream)
+              : run_scores<64, false>(p, dev, sms, stream);
 }
 
 int launch_select(const SelectParams& p, cudaStream_t stream) {

@@ -155,7 +155,8 @@ struct ScoreParams {
   int heads, group, page_shift;
   float* scores;
 };
-int launch_kv_scores(const ScoreParams& p, int d, bool bf16, int sms, cudaStream_t stream);
+int launch_kv_scores(const ScoreParams& p, int d, bool bf16, int dev, int sms,
+                     cudaStream_t stream);
 
 // Sequences of a decode call are its table's entries: one per sequence, whose
 // cached heads share it, or (per_head) one per (sequence, cached head).

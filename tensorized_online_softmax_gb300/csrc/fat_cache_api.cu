@@ -240,7 +240,7 @@ int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
   p.scores = scores;
   const int sms = sm_count(dev);
   if (sms < 1) return FAT_ERR_LAUNCH;
-  return status(fat::launch_kv_scores(p, d, dtype == FAT_DTYPE_BF16, sms, stream));
+  return status(fat::launch_kv_scores(p, d, dtype == FAT_DTYPE_BF16, dev, sms, stream));
 }
 
 static size_t choice_bytes(long long bh, long long list) {

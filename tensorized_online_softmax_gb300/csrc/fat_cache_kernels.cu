@@ -216,30 +216,46 @@ __global__ void __launch_bounds__(128) kv_bounds_kernel(const BoundsParams p) {
       float lo[8], hi[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) lo[j] = INFINITY, hi[j] = -INFINITY;
-      for (int r = group; r < rows; r += kGroups) {
-        const uint8_t* row = p.c.k + page * p.c.k_page + h * p.c.k_head + r * p.c.k_token;
-        float x[8];
-        if constexpr (kE4M3) {
-          const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-          const float s =
-              scale_value(__ldg(p.c.k_scale + (page * p.c.heads + h) * p.c.page_size + r));
-          const uint32_t two[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+      constexpr int kBatch = 4;  // rows whose loads are in flight together
+      const uint8_t* base = p.c.k + page * p.c.k_page + h * p.c.k_head;
+      const uint8_t* scales = p.c.k_scale + (page * p.c.heads + h) * p.c.page_size;
+      for (int r0 = group; r0 < rows; r0 += kBatch * kGroups) {
+        uint4 c[kBatch];
+        uint32_t e[kBatch];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
-            x[2 * j] = f.x * s, x[2 * j + 1] = f.y * s;
-          }
-        } else {
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(row) + lane);
-          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16<kBf16>(w[j]);
-            x[2 * j] = f.x, x[2 * j + 1] = f.y;
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = min(r0 + i * kGroups, rows - 1);  // (the last row again changes nothing)
+          const uint8_t* row = base + r * p.c.k_token;
+          if constexpr (kE4M3) {
+            const uint2 two = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+            c[i].x = two.x, c[i].y = two.y;
+            e[i] = __ldg(scales + r);
+          } else {
+            c[i] = __ldg(reinterpret_cast<const uint4*>(row) + lane);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) lo[j] = min_nan(lo[j], x[j]), hi[j] = max_nan(hi[j], x[j]);
+        for (int i = 0; i < kBatch; ++i) {
+          float x[8];
+          if constexpr (kE4M3) {
+            const float s = scale_value(e[i]);
+            const uint32_t two[4] = {c[i].x, c[i].x >> 16, c[i].y, c[i].y >> 16};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+              x[2 * j] = f.x * s, x[2 * j + 1] = f.y * s;
+            }
+          } else {
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack16<kBf16>(w[j]);
+              x[2 * j] = f.x, x[2 * j + 1] = f.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) lo[j] = min_nan(lo[j], x[j]), hi[j] = max_nan(hi[j], x[j]);
+        }
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) lo_s[group][lane * 8 + j] = lo[j], hi_s[group][lane * 8 + j] = hi[j];
