@@ -104,6 +104,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True):
     """Load the in-tree CUDA library (building it first if it is missing)."""
     global _lib
+    if _lib is not None:  # (set once, when everything is declared)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

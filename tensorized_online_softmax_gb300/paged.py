@@ -19,17 +19,20 @@ given.  A given workspace must not be shared by calls that overlap.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import struct
 
 import torch
 
-from . import DTYPES, FAT_OK, FatError, load_library
+from . import DTYPES, FatError, load_library
 
 _P, _I, _L, _F, _Z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
                       ctypes.c_size_t)
 
 
+# The structs go to the library as packed bytes (half the time of a ctypes struct); the classes
+# mirror them for whoever calls the C entry points directly.
 class FatKvCache(ctypes.Structure):
     """Mirror of ``fat_kv_cache`` in include/fat_attn.h (same field order)."""
     _fields_ = [
@@ -45,9 +48,13 @@ class FatPageTable(ctypes.Structure):
     _fields_ = [("pages", _P), ("stride", _L), ("width", _I), ("batch", _I), ("seq_lens", _P)]
 
 
+_pack_cache = struct.Struct("@PPPPqiiiiqqqqqq").pack
+_pack_table = struct.Struct("@PqiiP").pack
+
+
 def declare(lib) -> None:
     """Argument and result types of the entry points used here."""
-    cache, table = ctypes.POINTER(FatKvCache), ctypes.POINTER(FatPageTable)
+    cache = table = _P
     query = [_P, _I, _L, _L, _I]
     for name, args, result in (
             ("fat_kv_write", [cache, _P, _P, _I, _L, _L, _L, _L, _P, _I, _P], _I),
@@ -67,7 +74,6 @@ _WIDE = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
 _CACHE = {**_WIDE, torch.float8_e4m3fn: DTYPES["e4m3"]}
 _E4M3 = DTYPES["e4m3"]
 _DIRECT = 512  # FAT_DECODE_DIRECT: positions of a table that need no workspace
-_HERE = contextlib.nullcontext()
 
 # The checks below run for every call of a serving loop, where a few microseconds count: each
 # function first asks everything at once, and only finds out what is wrong if something is.
@@ -115,27 +121,31 @@ def _scale(name, t, shape, device):
 
 
 def _cache(k, v, k_scale, v_scale, writable=False):
-    """The checked cache as a struct; v None where only the keys are read."""
+    """The checked cache, v None where only the keys are read: the packed struct, the device, the
+    fat_dtype, and (pages, heads, page_size, d)."""
     _tensor("k_cache", k, _CACHE, 4)
     device, kind, shape = k.device, _CACHE[k.dtype], k.shape
+    pages, heads, page_size, d = shape
     k_rows = _rows("k_cache", k, shape, writable)
-    at, v_rows = None, (0, 0, 0)
+    at, v_rows = 0, (0, 0, 0)
     if v is not None:
-        _tensor("v_cache", v, (k.dtype,), 4, device)
-        if v.shape != shape:
+        if not (isinstance(v, torch.Tensor) and v.device == device and v.dtype is k.dtype
+                and v.shape == shape):
+            _tensor("v_cache", v, (k.dtype,), 4, device)
             raise ValueError("k_cache and v_cache must have the same shape")
         at, v_rows = v.data_ptr(), _rows("v_cache", v, shape, writable)
-    ks = vs = None
+    ks = vs = 0
     if kind == _E4M3:
         ks = _scale("k_scale", k_scale, shape, device)
-        vs = _scale("v_scale", v_scale, shape, device) if v is not None else None
+        vs = _scale("v_scale", v_scale, shape, device) if v is not None else 0
     elif k_scale is not None or v_scale is not None:
         raise ValueError("scales go with an e4m3 cache only")
-    return FatKvCache(k.data_ptr(), at, ks, vs, shape[0], shape[1], shape[2], shape[3], kind,
-                      *k_rows, *v_rows)
+    return _pack_cache(k.data_ptr(), at, ks, vs, pages, heads, page_size, d, kind, *k_rows,
+                       *v_rows), device, kind, shape
 
 
 def _table(page_table, seq_lens, device):
+    """The checked table as a packed struct, the batch and the entries of a sequence."""
     if not (isinstance(page_table, torch.Tensor) and isinstance(seq_lens, torch.Tensor)
             and page_table.device == seq_lens.device == device
             and page_table.dtype is seq_lens.dtype is torch.int32
@@ -148,8 +158,8 @@ def _table(page_table, seq_lens, device):
         raise ValueError("seq_lens must be contiguous [B], page_table [B, width]")
     if step != 1 and width > 1:
         raise ValueError("the rows of page_table must be contiguous")
-    return FatPageTable(page_table.data_ptr(), stride if batch > 1 else width, width, batch,
-                        seq_lens.data_ptr())
+    return _pack_table(page_table.data_ptr(), stride if batch > 1 else width, width, batch,
+                       seq_lens.data_ptr()), batch, width
 
 
 def _query(q, batch, heads, d, device):
@@ -183,11 +193,6 @@ def _output(name, t, shape, dtype, device):
     return t
 
 
-def _on(device):
-    """The device as the current one, for the launch."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
 def _stream(stream, device, fresh):
     """The stream's handle; tensors allocated by this call are kept for a stream that is not the
     one they were allocated on."""
@@ -200,9 +205,16 @@ def _stream(stream, device, fresh):
     return stream.cuda_stream
 
 
-def _done(status, what):
-    if status != FAT_OK:
-        raise FatError(status, what)
+def _call(name, device, *args):
+    """The library's function on the tensors' device."""
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        raise FatError(status, name)
 
 
 def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
@@ -216,23 +228,19 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
     least power of two as its scale that brings its largest magnitude to at
     most 448.
     """
-    lib = load_library()
-    c = _cache(k_cache, v_cache, k_scale, v_scale, writable=True)
-    device = k_cache.device
+    cache, device, kind, (_, heads, _, d) = _cache(k_cache, v_cache, k_scale, v_scale, True)
     _tensor("slots", slots, (torch.int64,), 1, device)
-    shape = torch.Size((slots.shape[0], c.heads, c.d))
+    shape = (slots.shape[0], heads, d)
     k_strides = _tokens("k", k, shape, _WIDE, device)
     v_strides = _tokens("v", v, shape, (k.dtype,), device)
-    if c.dtype != _E4M3 and k.dtype != k_cache.dtype:
+    if kind != _E4M3 and k.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} tokens, not {k.dtype}")
     if not shape[0]:
         return
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
-    with _on(device):
-        _done(lib.fat_kv_write(c, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype], *k_strides,
-                               *v_strides, slots.data_ptr(), shape[0],
-                               _stream(stream, device, ())), "fat_kv_write")
+    _call("fat_kv_write", device, cache, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype], *k_strides,
+          *v_strides, slots.data_ptr(), shape[0], _stream(stream, device, ()))
 
 
 def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype=None,
@@ -242,49 +250,58 @@ def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype
     ``dtype``: bf16 or fp16; the cache's own type (the default) unless it is
     e4m3 (default bf16).  Rows from a sequence's length on are zeros.
     """
-    lib = load_library()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    device = k_cache.device
-    t = _table(page_table, seq_lens, device)
+    cache, device, kind, (_, heads, _, d) = _cache(k_cache, v_cache, k_scale, v_scale)
+    table, batch, _ = _table(page_table, seq_lens, device)
     if dtype is None:
-        dtype = torch.bfloat16 if c.dtype == _E4M3 else k_cache.dtype
-    if dtype not in _WIDE or (c.dtype != _E4M3 and dtype != k_cache.dtype):
+        dtype = torch.bfloat16 if kind == _E4M3 else k_cache.dtype
+    if dtype not in _WIDE or (kind != _E4M3 and dtype != k_cache.dtype):
         raise ValueError(f"a {k_cache.dtype} cache is not read as {dtype}")
-    shape = (t.batch, c.heads, int(max_len), c.d)
+    shape = (batch, heads, int(max_len), d)
     if shape[2] < 1:
         raise ValueError("max_len must be at least 1")
     fresh = ()
     if out is None:
-        fresh = out = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
-    k, v = (_output(n, x, shape, dtype, device) for n, x in zip(("k", "v"), out))
-    with _on(device):
-        _done(lib.fat_kv_read(c, t, k.data_ptr(), v.data_ptr(), _WIDE[dtype], shape[2],
-                              _stream(stream, device, fresh)), "fat_kv_read")
+        fresh = k, v = (torch.empty(shape, dtype=dtype, device=device),
+                        torch.empty(shape, dtype=dtype, device=device))
+    else:
+        k, v = (_output(n, x, shape, dtype, device) for n, x in zip(("k", "v"), out))
+    _call("fat_kv_read", device, cache, table, k.data_ptr(), v.data_ptr(), _WIDE[dtype], shape[2],
+          _stream(stream, device, fresh))
     return k, v
 
 
-def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out):
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    device = k_cache.device
-    t = _table(page_table, seq_lens, device)
-    query = _query(q, t.batch, c.heads, c.d, device)
-    if c.dtype != _E4M3 and q.dtype != k_cache.dtype:
+def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out):
+    cache, device, kind, shape = _cache(k_cache, v_cache, k_scale, v_scale)
+    table, batch, width = _table(page_table, seq_lens, device)
+    query = _query(q, batch, shape[1], shape[3], device)
+    if kind != _E4M3 and q.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} queries, not {q.dtype}")
-    shape = q.shape
     fresh = []
     if out is None:
         o = torch.empty_like(q, memory_format=torch.contiguous_format)
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
+        lse = torch.empty((batch, query[4]), dtype=torch.float32, device=device)
         fresh += [o, lse]
     else:
-        o = _output("o", out[0], shape, q.dtype, device)
-        lse = _output("lse", out[1], shape[:2], torch.float32, device)
-    return c, t, query, c.d ** -0.5 if scale is None else float(scale), o, lse, fresh
+        o = _output("o", out[0], q.shape, q.dtype, device)
+        lse = _output("lse", out[1], (batch, query[4]), torch.float32, device)
+    return (cache, table, *query), device, shape, batch, width, o, lse, fresh
 
 
-def _workspace(workspace, nbytes, device, fresh):
+@functools.lru_cache(maxsize=256)
+def attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, d: int,
+                                num_blocks: int | None = None) -> int:
+    """Workspace size of :func:`attn_decode_paged`, or with ``num_blocks`` of
+    :func:`attn_decode_sparse` (0 for invalid arguments)."""
+    lib = load_library()
+    if num_blocks is None:
+        return lib.fat_attn_decode_workspace_bytes(batch, q_heads, kv_heads, d)
+    return lib.fat_attn_decode_sparse_workspace_bytes(batch, q_heads, kv_heads, d, num_blocks)
+
+
+def _workspace(workspace, sizes, device, fresh):
     """The workspace's address and size; allocated if not given."""
     if workspace is None:
+        nbytes = attn_decode_workspace_bytes(*sizes)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         fresh.append(workspace)
         return workspace.data_ptr(), nbytes
@@ -305,18 +322,14 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale: float | 
     a CUDA uint8 tensor of :func:`attn_decode_workspace_bytes` bytes; a table for
     512 positions at most needs none.
     """
-    lib = load_library()
-    c, t, query, scale, o, lse, fresh = _decode_arguments(
-        q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out)
-    if workspace is None and t.width * c.page_size <= _DIRECT:
+    args, device, (_, heads, page_size, d), batch, width, o, lse, fresh = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out)
+    if workspace is None and width * page_size <= _DIRECT:
         work = None, 0
     else:
-        work = _workspace(workspace, lib.fat_attn_decode_workspace_bytes(
-            t.batch, query[4], c.heads, c.d), q.device, fresh)
-    with _on(q.device):
-        _done(lib.fat_attn_decode_paged(c, t, *query, scale, o.data_ptr(), lse.data_ptr(), *work,
-                                        _stream(stream, q.device, fresh)),
-              "fat_attn_decode_paged")
+        work = _workspace(workspace, (batch, q.shape[1], heads, d), device, fresh)
+    _call("fat_attn_decode_paged", device, *args, d ** -0.5 if scale is None else scale,
+          o.data_ptr(), lse.data_ptr(), *work, _stream(stream, device, fresh))
     return o, lse
 
 
@@ -330,19 +343,16 @@ def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | Non
     a sequence are computed anew (all of them if None); the others keep what
     they have.  Returns ``bounds``.
     """
-    lib = load_library()
-    c = _cache(k_cache, None, k_scale, None)
-    device = k_cache.device
-    t = _table(page_table, seq_lens, device)
-    dtypes = _WIDE if c.dtype == _E4M3 else (k_cache.dtype,)
-    _tensor("bounds", bounds, dtypes, 4, device)
-    _output("bounds", bounds, (c.num_pages, c.heads, 2, c.d), bounds.dtype, device)
+    cache, device, kind, (pages, heads, _, d) = _cache(k_cache, None, k_scale, None)
+    table = _table(page_table, seq_lens, device)[0]
+    _tensor("bounds", bounds, _WIDE if kind == _E4M3 else (k_cache.dtype,), 4, device)
+    if bounds.shape != (pages, heads, 2, d) or not bounds.is_contiguous():
+        raise ValueError("bounds must be contiguous [num_pages, heads, 2, d]")
     new_tokens = 0x7fffffff if new_tokens is None else int(new_tokens)
     if not 1 <= new_tokens <= 0x7fffffff:
         raise ValueError("new_tokens must be at least 1")
-    with _on(device):
-        _done(lib.fat_kv_block_bounds(c, t, new_tokens, bounds.data_ptr(), _WIDE[bounds.dtype],
-                                      _stream(stream, device, ())), "fat_kv_block_bounds")
+    _call("fat_kv_block_bounds", device, cache, table, new_tokens, bounds.data_ptr(),
+          _WIDE[bounds.dtype], _stream(stream, device, ()))
     return bounds
 
 
@@ -354,27 +364,24 @@ def kv_block_scores(q, bounds, page_table, seq_lens, page_size: int, *, out=None
     the query heads that share a cached head, of an upper bound on q . k over
     the block's keys; -inf behind a sequence's last block.
     """
-    lib = load_library()
     _tensor("bounds", bounds, _WIDE, 4)
     device = bounds.device
     pages, heads, two, d = bounds.shape
     if two != 2 or not bounds.is_contiguous():
         raise ValueError("bounds must be contiguous [num_pages, heads, 2, d]")
-    t = _table(page_table, seq_lens, device)
-    query = _query(q, t.batch, heads, d, device)
-    if q.dtype != bounds.dtype:
+    table, batch, width = _table(page_table, seq_lens, device)
+    query = _query(q, batch, heads, d, device)
+    if q.dtype is not bounds.dtype:
         raise ValueError("q and bounds must have the same type")
-    shape = (t.batch, heads, t.width)
     fresh = ()
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=device)
+        out = torch.empty((batch, heads, width), dtype=torch.float32, device=device)
         fresh = (out,)
-    scores = _output("out", out, shape, torch.float32, device)
-    with _on(device):
-        _done(lib.fat_kv_block_scores(*query, bounds.data_ptr(), pages, heads, int(page_size), d,
-                                      t, scores.data_ptr(), _stream(stream, device, fresh)),
-              "fat_kv_block_scores")
-    return scores
+    else:
+        _output("out", out, (batch, heads, width), torch.float32, device)
+    _call("fat_kv_block_scores", device, *query, bounds.data_ptr(), pages, heads, int(page_size),
+          d, table, out.data_ptr(), _stream(stream, device, fresh))
+    return out
 
 
 def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_blocks: int,
@@ -393,38 +400,22 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
     num_blocks], the choice in rising order, then -1.  ``out``: optional
     ``(o, lse, blocks)``.
     """
-    lib = load_library()
-    c, t, query, scale, o, lse, fresh = _decode_arguments(
-        q, k_cache, v_cache, page_table, seq_lens, scale, k_scale, v_scale, out)
-    device = q.device
+    args, device, (_, heads, _, d), batch, width, o, lse, fresh = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out)
     num_blocks = int(num_blocks)
     if num_blocks < 1 or first_blocks < 0 or last_blocks < 0 or \
             first_blocks + last_blocks > num_blocks:
         raise ValueError("num_blocks must be at least 1 and at least first_blocks + last_blocks")
-    _tensor("scores", scores, (torch.float32,), 3, device)
-    _output("scores", scores, (t.batch, c.heads, t.width), torch.float32, device)
-    shape = (t.batch, c.heads, num_blocks)
+    _output("scores", scores, (batch, heads, width), torch.float32, device)
+    shape = (batch, heads, num_blocks)
     if out is None:
         blocks = torch.empty(shape, dtype=torch.int32, device=device)
         fresh.append(blocks)
     else:
         blocks = _output("blocks", out[2], shape, torch.int32, device)
-    nbytes = lib.fat_attn_decode_sparse_workspace_bytes(t.batch, q.shape[1], c.heads, c.d,
-                                                        num_blocks)
-    work = _workspace(workspace, nbytes, device, fresh)
-    with _on(device):
-        _done(lib.fat_attn_decode_sparse(
-            c, t, *query, scores.data_ptr(), num_blocks, int(first_blocks), int(last_blocks),
-            scale, o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work,
-            _stream(stream, device, fresh)), "fat_attn_decode_sparse")
+    work = _workspace(workspace, (batch, q.shape[1], heads, d, num_blocks), device, fresh)
+    _call("fat_attn_decode_sparse", device, *args, scores.data_ptr(), num_blocks,
+          int(first_blocks), int(last_blocks), d ** -0.5 if scale is None else scale,
+          o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work,
+          _stream(stream, device, fresh))
     return o, lse, blocks
-
-
-def attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, d: int,
-                                num_blocks: int | None = None) -> int:
-    """Workspace size of :func:`attn_decode_paged`, or with ``num_blocks`` of
-    :func:`attn_decode_sparse` (0 for invalid arguments)."""
-    lib = load_library()
-    if num_blocks is None:
-        return lib.fat_attn_decode_workspace_bytes(batch, q_heads, kv_heads, d)
-    return lib.fat_attn_decode_sparse_workspace_bytes(batch, q_heads, kv_heads, d, num_blocks)

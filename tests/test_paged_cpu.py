@@ -11,6 +11,7 @@ import torch
 
 import paged_reference as ref
 import tensorized_online_softmax_gb300 as fat
+from tensorized_online_softmax_gb300 import paged
 from tensorized_online_softmax_gb300.paged import FatKvCache, FatPageTable
 
 BF16, E4M3, FP16 = 0, 1, 2
@@ -28,13 +29,13 @@ def cache(**kw):
     c = dict(k=0x10000, v=0x20000, k_scale=0x30000, v_scale=0x40000, num_pages=10, heads=2,
              page_size=16, d=128, dtype=BF16, k_page_stride=4096, k_head_stride=2048,
              k_token_stride=128, v_page_stride=4096, v_head_stride=2048, v_token_stride=128)
-    return FatKvCache(**{**c, **kw})
+    return ctypes.byref(FatKvCache(**{**c, **kw}))
 
 
 def table(**kw):
     # (room for 1024 positions: more than a call without workspace takes)
-    return FatPageTable(**{**dict(pages=0x50000, stride=64, width=64, batch=3,
-                                  seq_lens=0x60000), **kw})
+    return ctypes.byref(FatPageTable(**{**dict(pages=0x50000, stride=64, width=64, batch=3,
+                                               seq_lens=0x60000), **kw}))
 
 
 BAD_CACHES = [
@@ -218,3 +219,6 @@ def test_struct_sizes():
     """The structs' layouts: 4 pointers, a 64-bit count, 4 ints, 6 strides; and the table's."""
     assert ctypes.sizeof(FatKvCache) == 4 * 8 + 8 + 4 * 4 + 6 * 8
     assert ctypes.sizeof(FatPageTable) == 8 + 8 + 4 + 4 + 8
+    c = FatKvCache(*range(1, 16))
+    assert bytes(c) == paged._pack_cache(*range(1, 16))
+    assert bytes(FatPageTable(1, 2, 3, 4, 5)) == paged._pack_table(1, 2, 3, 4, 5)
