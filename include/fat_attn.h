@@ -334,7 +334,7 @@ typedef struct fat_kv_cache {
 typedef struct fat_page_table {
   const int* pages;    /* page of position i * page_size of sequence b: pages[b * stride + i] */
   long long stride;    /* >= width */
-  int width;           /* entries of a sequence */
+  int width;           /* entries of a sequence; width * page_size <= 2^30 */
   int batch;           /* sequences */
   const int* seq_lens; /* [batch] cached positions of each sequence (0 allowed) */
 } fat_page_table;
@@ -393,7 +393,9 @@ size_t fat_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int
  * This call renews the blocks that hold any of the last new_tokens positions
  * of each sequence (new_tokens >= 1; all blocks if it is at least the
  * length), over their positions below the length; other blocks keep what
- * they have.  A NaN key makes its bound NaN.  cache->v is not used.
+ * they have.  A NaN key makes its bound NaN; a value of an e4m3 cache that
+ * `dtype` cannot hold is rounded to nearest.  A page in two sequences' lines
+ * gets the bounds of one of them.  cache->v is not used.
  */
 int fat_kv_block_bounds(const fat_kv_cache* cache, const fat_page_table* table, int new_tokens,
                         void* bounds, int dtype, cudaStream_t stream);

@@ -65,8 +65,10 @@ int cache_view(const fat_kv_cache* c, bool need_v, fat::CacheView* out) {
   return FAT_OK;
 }
 
-int table_view(const fat_page_table* t, fat::TableView* out) {
-  if (!t || !t->pages || !t->seq_lens || t->width < 1 || t->batch < 1 || t->stride < t->width)
+// (positions below 2^30 + 1, so that 32-bit places and a tile more never overflow)
+int table_view(const fat_page_table* t, int page_shift, fat::TableView* out) {
+  if (!t || !t->pages || !t->seq_lens || t->width < 1 || t->batch < 1 || t->stride < t->width ||
+      (static_cast<long long>(t->width) << page_shift) > (1ll << 30))
     return FAT_ERR_INVALID_ARG;
   if (!aligned(t->pages, 4) || !aligned(t->seq_lens, 4)) return FAT_ERR_ALIGNMENT;
   out->pages = t->pages;
@@ -132,7 +134,7 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
                 int dtype, int max_len, cudaStream_t stream) {
   fat::ReadParams p = {};
   int st = cache_view(cache, true, &p.c);
-  if (st == FAT_OK) st = table_view(table, &p.t);
+  if (st == FAT_OK) st = table_view(table, p.c.page_shift, &p.t);
   if (st != FAT_OK) return st;
   const bool e4m3 = cache->dtype == FAT_DTYPE_E4M3;
   if (!wide_type(dtype) || (!e4m3 && dtype != cache->dtype) || max_len < 1 || !k || !v)
@@ -150,7 +152,7 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
 
 size_t fat_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int d) {
   if (batch < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
-      (d != 64 && d != 128))
+      static_cast<long long>(batch) * q_heads > (1ll << 30) || (d != 64 && d != 128))
     return 0;
   return fat::decode_workspace_bytes(d);
 }
@@ -159,7 +161,7 @@ static int decode_common(const fat_kv_cache* cache, const fat_page_table* table,
                          int dtype, long long q_batch_stride, long long q_head_stride,
                          int q_heads, float scale, void* o, float* lse, fat::DecodeParams* p) {
   int st = cache_view(cache, true, &p->c);
-  if (st == FAT_OK) st = table_view(table, &p->t);
+  if (st == FAT_OK) st = table_view(table, p->c.page_shift, &p->t);
   if (st == FAT_OK)
     st = query_ok(q, dtype, q_batch_stride, q_head_stride, q_heads, cache->heads, table->batch,
                   &p->q_batch, &p->q_head);
@@ -201,7 +203,7 @@ int fat_kv_block_bounds(const fat_kv_cache* cache, const fat_page_table* table, 
                         void* bounds, int dtype, cudaStream_t stream) {
   fat::BoundsParams p = {};
   int st = cache_view(cache, false, &p.c);
-  if (st == FAT_OK) st = table_view(table, &p.t);
+  if (st == FAT_OK) st = table_view(table, p.c.page_shift, &p.t);
   if (st != FAT_OK) return st;
   const bool e4m3 = cache->dtype == FAT_DTYPE_E4M3;
   if (!wide_type(dtype) || (!e4m3 && dtype != cache->dtype) || new_tokens < 1 || !bounds)
@@ -219,13 +221,13 @@ int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
                         long long num_pages, int kv_heads, int page_size, int d,
                         const fat_page_table* table, float* scores, cudaStream_t stream) {
   fat::ScoreParams p = {};
-  int st = table_view(table, &p.t);
-  if (st != FAT_OK) return st;
   if (!bounds || !scores || kv_heads < 1 || kv_heads > (1 << 20) || num_pages < 1 ||
       num_pages > 0x7fffffffll || (d != 64 && d != 128))
     return FAT_ERR_INVALID_ARG;
   p.page_shift = page_shift_of(page_size);
   if (p.page_shift < 0) return FAT_ERR_INVALID_ARG;
+  int st = table_view(table, p.page_shift, &p.t);
+  if (st != FAT_OK) return st;
   st = query_ok(q, dtype, q_batch_stride, q_head_stride, q_heads, kv_heads, table->batch,
                 &p.q_batch, &p.q_head);
   if (st != FAT_OK) return st;
@@ -250,7 +252,7 @@ static size_t choice_bytes(long long bh, long long list) {
 size_t fat_attn_decode_sparse_workspace_bytes(int batch, int q_heads, int kv_heads, int d,
                                               int num_blocks) {
   const size_t n = fat_attn_decode_workspace_bytes(batch, q_heads, kv_heads, d);
-  if (n == 0 || num_blocks < 1) return 0;
+  if (n == 0 || num_blocks < 1 || num_blocks > (1 << 30)) return 0;
   return n + choice_bytes(static_cast<long long>(batch) * kv_heads, num_blocks);
 }
 
@@ -263,7 +265,7 @@ int fat_attn_decode_sparse(const fat_kv_cache* cache, const fat_page_table* tabl
   int st = decode_common(cache, table, q, dtype, q_batch_stride, q_head_stride, q_heads, scale, o,
                          lse, &p);
   if (st != FAT_OK) return st;
-  if (!scores || !blocks || num_blocks < 1 || first_blocks < 0 || last_blocks < 0 ||
+  if (!scores || !blocks || num_blocks < 1 || num_blocks > (1 << 30) || first_blocks < 0 || last_blocks < 0 ||
       static_cast<long long>(first_blocks) + last_blocks > num_blocks || !workspace ||
       workspace_bytes < fat_attn_decode_sparse_workspace_bytes(table->batch, q_heads,
                                                                cache->heads, cache->d, num_blocks))

@@ -53,7 +53,8 @@ BAD_V = [(dict(v=None), "INVALID_ARG"), (dict(v=0x20004), "ALIGNMENT"),
          (dict(v_page_stride=4), "ALIGNMENT"), (dict(dtype=E4M3, v_scale=None), "INVALID_ARG")]
 BAD_TABLES = [(dict(pages=None), "INVALID_ARG"), (dict(seq_lens=None), "INVALID_ARG"),
               (dict(width=0), "INVALID_ARG"), (dict(batch=0), "INVALID_ARG"),
-              (dict(stride=63), "INVALID_ARG"), (dict(pages=0x50002), "ALIGNMENT"),
+              (dict(stride=63), "INVALID_ARG"),
+              (dict(stride=1 << 28, width=(1 << 26) + 1), "INVALID_ARG"), (dict(pages=0x50002), "ALIGNMENT"),
               (dict(seq_lens=0x60001), "ALIGNMENT")]
 BAD_QUERIES = [(dict(q=None), "INVALID_ARG"), (dict(q=0x70008), "ALIGNMENT"),
                (dict(dtype=E4M3), "INVALID_ARG"), (dict(batch_stride=1028), "ALIGNMENT"),
@@ -169,6 +170,8 @@ def test_workspace_sizes(lib):
         assert lib.fat_attn_decode_workspace_bytes(*bad) == 0
         assert lib.fat_attn_decode_sparse_workspace_bytes(*bad, 4) == 0
     assert lib.fat_attn_decode_sparse_workspace_bytes(3, 8, 2, 128, 0) == 0
+    assert lib.fat_attn_decode_sparse_workspace_bytes(3, 8, 2, 128, 2 ** 31 - 1) == 0
+    assert lib.fat_attn_decode_workspace_bytes(2 ** 31 - 1, 8, 2, 128) == 0
 
 
 def test_binding_refuses_cpu_tensors():
