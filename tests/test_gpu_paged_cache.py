@@ -203,6 +203,24 @@ def test_refusals(cuda_device):
     fat.kv_cache_write(x[:0], x[:0], plain.k, plain.v, slots[:0])
 
 
+def test_read_of_part_of_a_sequence_into_given_tensors(cuda_device):
+    """Positions from max_len on are left out; rows of a shorter sequence are zeros."""
+    lens, ps = [100, 7, 0], 16
+    cache = Cache(pages_for(lens, ps), 2, ps, 64, "fp16", "pthd", seed=3)
+    table = make_table(lens, ps, cache.k.shape[0], seed=3)
+    out = tuple(torch.full((3, 2, 33, 64), 9.0, dtype=torch.float16, device="cuda")
+                for _ in range(2))
+    got = fat.kv_cache_read(cache.k, cache.v, table.cuda(),
+                            torch.tensor(lens, dtype=torch.int32).cuda(), 33, out=out)
+    assert got[0] is out[0] and got[1] is out[1]
+    for t, values in zip(out, cache.values):
+        want = torch.zeros((3, 2, 33, 64), dtype=torch.float64)
+        for b, n in enumerate(lens):
+            want[b, :, :min(n, 33)] = ref.gather(values, table[b], min(n, 33), ps)
+        assert torch.equal(t.cpu().double(), want)
+    assert fat.check_device_error() == fat.FAT_OK
+
+
 def test_write_and_read_on_another_stream(cuda_device):
     cache = Cache(pages_for([50], 16), 2, 16, 128, "bf16")
     x = torch.randn((50, 2, 128), device="cuda").to(torch.bfloat16)

@@ -349,6 +349,41 @@ def test_sparse_of_many_blocks(cuda_device):
             assert blocks[0, 0].cpu().tolist() == want
 
 
+@pytest.mark.parametrize("count", [8192, 8193, 32768, 33000])
+def test_sparse_of_very_many_blocks(cuda_device, count):
+    """A sequence whose table repeats a few pages, around the counts where the choice changes its
+    way: the blocks, and the attention over the first and the last of them."""
+    n, ps, d = 16 * count - 5, 16, 64
+    cache = Cache(8, 1, ps, d, "bf16", seed=count)
+    g = torch.Generator().manual_seed(count)
+    table = torch.randint(0, 8, (1, count + 3), generator=g, dtype=torch.int32)
+    q = queries(1, 2, d, "bf16", seed=count)
+    scores = torch.randn((1, 1, count + 3), generator=g)
+    scores[0, 0, ::7] = scores[0, 0, 3]  # many equal ones
+    for num_blocks in (5, count // 3, count - 1, count + 1):
+        o, lse, blocks = fat.attn_decode_sparse(
+            q.cuda(), cache.k, cache.v, table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+            scores.cuda(), num_blocks)
+        want = ref.choose(scores[0, 0].tolist(), n, ps, num_blocks, 0, 1)
+        got = blocks[0, 0].cpu().tolist()
+        assert got[:len(want)] == want and set(got[len(want):]) <= {-1}
+        keep = torch.tensor(want)
+        place = (keep[:, None] * ps + torch.arange(ps)).flatten()
+        ids = table[0].long()[keep]
+        k, v = (x[ids, 0].reshape(-1, d)[place < n] for x in (cache.k_values, cache.v_values))
+        check_attention(o, lse, *(x[None] for x in ref.attend(q[0].double(), k, v, 0.125)),
+                        what=f"{count} {num_blocks}")
+    assert fat.check_device_error() == fat.FAT_OK
+
+
+def test_sparse_of_many_sequences(cuda_device):
+    """More (sequence, head) pairs than threads in a block."""
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 70, (90,), generator=g).tolist()
+    cache, table, lens_t, q = setup(lens, 3, 2, 16, 64, "fp16", "e4m3", seed=28)
+    check_sparse(cache, table, lens_t, q, torch.randn((90, 3, table.shape[1]), generator=g), 2)
+
+
 def test_all_blocks_chosen_equals_the_whole(cuda_device):
     lens = [100, 0, 640, 333]
     cache, table, lens_t, q = setup(lens, 2, 4, 16, 128, "bf16", "bf16", seed=27)
@@ -467,6 +502,53 @@ def test_calls_on_two_streams_at_once(cuda_device):
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(w[0], o) and torch.equal(w[1], l) for o, l in g)
+
+
+def test_on_the_current_stream(cuda_device):
+    """Calls go to torch's current stream, also where it is not the default one."""
+    cache, table, lens_t, q = setup([3000, 77], 2, 4, 64, 128, "bf16", "e4m3", seed=53)
+    want = run_decode(cache, table, lens_t, q)
+    args = (torch.zeros_like(q.cuda()), cache.k, cache.v, table.cuda(), lens_t.cuda())
+    real = q.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()) as _:
+        torch.cuda._sleep(2_000_000)  # a call on another stream would see the zeros
+        args[0].copy_(real)
+        o, lse = fat.attn_decode_paged(*args, **cache.scale_args)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_two_graphs_share_a_workspace(cuda_device):
+    """Two captured calls of different shapes with one workspace, replayed in turn."""
+    work = torch.empty(fat.attn_decode_workspace_bytes(2, 8, 2, 128, 40), dtype=torch.uint8,
+                       device="cuda")
+    work.fill_(0xA5)
+    graphs, want, got, keep = [], [], [], []  # (keep: a graph does not own its inputs)
+    for i, lens in enumerate(([5000, 700], [1300, 4000])):
+        cache, table, lens_t, q = setup(lens, 2, 4, 64, 128, "bf16", ("bf16", "e4m3")[i],
+                                        seed=60 + i)
+        scores = torch.randn((2, 2, table.shape[1]), generator=torch.Generator().manual_seed(i))
+        args = (q.cuda(), cache.k, cache.v, table.cuda(), lens_t.cuda())
+        scores = scores.cuda()
+
+        def call(args=args, scores=scores, kw=cache.scale_args):
+            whole = fat.attn_decode_paged(*args, workspace=work, **kw)
+            return (*whole, *fat.attn_decode_sparse(*args, scores, 40, workspace=work, **kw))
+
+        keep.append((args, scores, cache))
+        want.append([t.clone() for t in call()])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(call())
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        for t in got[i]:
+            t.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
 
 
 def test_refusals(cuda_device):
