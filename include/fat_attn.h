@@ -308,8 +308,10 @@ size_t fat_attn_bwd_workspace_bytes(int B, int H, int N);
  *    page_size]): the row's values are code * 2^(e - 127), e = 1..254; e = 255
  *    marks a row that holds an inf or a NaN, and every element reads as NaN.
  *  - Strides are in elements, between pages, heads and tokens (the d elements
- *    of a row are adjacent); each is a multiple of 16 bytes.  Any order of
- *    the three dimensions is allowed, as are k and v as parts of one tensor.
+ *    of a row are adjacent); each is a multiple of 16 bytes below 4 GiB, and
+ *    so are those of q and of the tokens (FAT_ERR_ALIGNMENT otherwise).  Any
+ *    order of the three dimensions is allowed, as are k and v as parts of one
+ *    tensor.
  *  - k and v are 16-byte aligned, the scales 16-byte aligned.
  *
  * Indexes that live on the device (pages, lengths, slots) cannot be checked

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScorePara
             const int r = r0 + mine;
             const int pg = __shfl_sync(0xffffffffu, page, ((loaded - first) & 16) + r);
             const uint8_t* from =
-                p.bounds + (static_cast<long long>(max(pg, 0)) * p.heads + h) * L::kRow + c * 16;
+                p.bounds + (wide(max(pg, 0), p.heads) + h) * L::kRow + c * 16;
             const uint32_t bytes = pg >= 0 ? 16u : 0u;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                              stage_in + score_piece(L::kRow, r, c)),
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScorePara
       if (first < stop) {
         const bool in = head0 + g < p.group;
         const uint4* q = reinterpret_cast<const uint4*>(
-            p.q + b * p.q_batch + (h * p.group + head0 + (in ? g : 0)) * p.q_head);
+            p.q + wide(b, p.q_batch) + wide(h * p.group + head0 + (in ? g : 0), p.q_head));
 #pragma unroll
         for (int c = 0; c < kChunks / 2; ++c) {
           const uint4 x = in ? __ldg(q + c * 4 + t) : make_uint4(0, 0, 0, 0);

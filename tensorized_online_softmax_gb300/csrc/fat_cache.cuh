@@ -18,17 +18,33 @@
 
 namespace fat {
 
-// strides in bytes
+// strides in bytes, in 32 bits: a row's address is then a few multiply-adds that
+// widen, not 64-bit products
 struct CacheView {
   uint8_t* k;
   uint8_t* v;
   uint8_t* k_scale;  // [num_pages, heads, page_size]
   uint8_t* v_scale;
-  long long k_page, k_head, k_token;
-  long long v_page, v_head, v_token;
-  long long num_pages;
+  uint32_t k_page, k_head, k_token;
+  uint32_t v_page, v_head, v_token;
+  uint32_t num_pages;
   int heads, page_size, page_shift;
 };
+
+__device__ __forceinline__ unsigned long long wide(uint32_t a, uint32_t b) {
+  return static_cast<unsigned long long>(a) * b;
+}
+// Row `place` of head h of a page: its byte offset, and its place among the scales.
+__device__ __forceinline__ unsigned long long row_offset(uint32_t page, uint32_t h, uint32_t place,
+                                                         uint32_t page_stride,
+                                                         uint32_t head_stride,
+                                                         uint32_t token_stride) {
+  return wide(page, page_stride) + wide(h, head_stride) + wide(place, token_stride);
+}
+__device__ __forceinline__ unsigned long long scale_offset(const CacheView& c, uint32_t page,
+                                                           uint32_t h, uint32_t place) {
+  return ((wide(page, c.heads) + h) << c.page_shift) + place;
+}
 
 struct TableView {
   const int* pages;
@@ -51,9 +67,9 @@ __device__ __forceinline__ int table_length(const TableView& t, int page_shift, 
 }
 
 // Page i of sequence b, or -1 (flagged) if it is not a page of the cache.
-__device__ __forceinline__ int table_page(const TableView& t, long long num_pages, int b, int i) {
+__device__ __forceinline__ int table_page(const TableView& t, uint32_t num_pages, int b, int i) {
   const int p = __ldg(t.pages + b * t.stride + i);
-  if (p < 0 || p >= num_pages) {
+  if (static_cast<uint32_t>(p) >= num_pages) {
     atomicOr(t.error_word, kErrIndex);
     return -1;
   }
@@ -120,7 +136,7 @@ struct WriteParams {
   CacheView c;
   const uint8_t* k;
   const uint8_t* v;
-  long long k_token, k_head, v_token, v_head;  // bytes
+  uint32_t k_token, k_head, v_token, v_head;  // bytes
   const long long* slots;
   int tokens;
   unsigned int* error_word;
@@ -149,9 +165,9 @@ int launch_kv_bounds(const BoundsParams& p, int d, bool e4m3, bool bf16, cudaStr
 struct ScoreParams {
   TableView t;
   const uint8_t* q;
-  long long q_batch, q_head;  // bytes
+  uint32_t q_batch, q_head;  // bytes
   const uint8_t* bounds;
-  long long num_pages;
+  uint32_t num_pages;
   int heads, group, page_shift;
   float* scores;
 };
@@ -166,7 +182,7 @@ struct DecodeParams {
   int per_head;
   int batch;
   const uint8_t* q;
-  long long q_batch, q_head;  // bytes
+  uint32_t q_batch, q_head;  // bytes
   int group;                  // query heads per cached head
   float scale_log2;           // scale * log2(e)
   uint8_t* o;

@@ -24,10 +24,11 @@ int page_shift_of(int page_size) {
   return -1;
 }
 
-// strides in elements of `bytes` -> bytes; false if a row would not start on 16 bytes
-bool stride_ok(long long elements, int bytes, long long* out) {
-  if (elements < 0 || elements > (1ll << 50)) return false;
-  *out = elements * bytes;
+// strides in elements of `bytes` -> bytes; false if a row would not start on 16 bytes or the
+// stride is 4 GiB or more
+bool stride_ok(long long elements, int bytes, uint32_t* out) {
+  if (elements < 0 || elements > 0xffffffffll / bytes) return false;
+  *out = static_cast<uint32_t>(elements * bytes);
   return *out % 16 == 0;
 }
 
@@ -57,7 +58,7 @@ int cache_view(const fat_kv_cache* c, bool need_v, fat::CacheView* out) {
   v.v = static_cast<uint8_t*>(c->v);
   v.k_scale = c->k_scale;
   v.v_scale = c->v_scale;
-  v.num_pages = c->num_pages;
+  v.num_pages = static_cast<uint32_t>(c->num_pages);
   v.heads = c->heads;
   v.page_size = c->page_size;
   v.page_shift = shift;
@@ -81,7 +82,7 @@ int table_view(const fat_page_table* t, int page_shift, fat::TableView* out) {
 
 // query rows against a cache (or bounds) of `heads` heads and type `dtype`
 int query_ok(const void* q, int q_dtype, long long batch_stride, long long head_stride,
-             int q_heads, int heads, int batch, long long* batch_bytes, long long* head_bytes) {
+             int q_heads, int heads, int batch, uint32_t* batch_bytes, uint32_t* head_bytes) {
   if (!q || !wide_type(q_dtype) || q_heads < 1 || q_heads % heads != 0) return FAT_ERR_INVALID_ARG;
   if (static_cast<long long>(batch) * q_heads > (1ll << 30)) return FAT_ERR_INVALID_ARG;
   if (!stride_ok(batch_stride, 2, batch_bytes) || !stride_ok(head_stride, 2, head_bytes) ||
@@ -236,7 +237,7 @@ int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,
   if ((st = fat::host_device(&dev, &p.t.error_word)) != FAT_OK) return st;
   p.q = static_cast<const uint8_t*>(q);
   p.bounds = static_cast<const uint8_t*>(bounds);
-  p.num_pages = num_pages;
+  p.num_pages = static_cast<uint32_t>(num_pages);
   p.heads = kv_heads;
   p.group = q_heads / kv_heads;
   p.scores = scores;

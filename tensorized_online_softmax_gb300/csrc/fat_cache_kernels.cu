@@ -13,24 +13,28 @@ constexpr int kThreads = 256;
 // write
 // ---------------------------------------------------------------------------
 
-// Eight fp32 values of one row's lane -> eight codes and the row's scale byte.
+// Eight 16-bit values of one row's lane -> eight codes and the row's scale byte.
 // kLanes lanes hold the row (a power of two, adjacent).
 //
 // The scale: the largest magnitude is m 2^E, 1 <= m < 2, and 448 = 1.75 2^8,
 // so the least power of two s with amax / s <= 448 is 2^(E - 8), or 2^(E - 7)
 // if m > 1.75.  A row below 2^-118 keeps s = 2^-126 (its byte is 1).
-template <int kLanes>
-__device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t& e) {
-  uint32_t top = 0;  // magnitudes compare as integers; an inf or NaN is the largest
+template <int kLanes, bool kBf16>
+__device__ __forceinline__ uint2 quantise_row(const uint4& x, uint32_t& e) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // magnitudes compare as integers, two at a time; an inf or NaN is the largest
+  uint32_t two = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 4; ++i) two = __vmaxu2(two, w[i] & 0x7FFF7FFFu);
 #pragma unroll
   for (int s = kLanes / 2; s > 0; s >>= 1)
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-  if (top >= 0x7F800000u) {
+    two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, s));
+  const uint32_t most = max(two >> 16, two & 0xFFFFu);
+  if (most >= (kBf16 ? 0x7F80u : 0x7C00u)) {
     e = 255u;
     return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   }
+  const uint32_t top = __float_as_uint(unpack16<kBf16>(most).x);
   int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   b = top == 0 ? 127 : max(b, 1);
   e = static_cast<uint32_t>(b);
@@ -38,10 +42,12 @@ __device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t& e) 
   uint2 r;
   uint16_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16<kBf16>(w[i]);
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
         : "=h"(h[i])
-        : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
+        : "f"(f.y * inv), "f"(f.x * inv));
+  }
   r.x = h[0] | (static_cast<uint32_t>(h[1]) << 16);
   r.y = h[2] | (static_cast<uint32_t>(h[3]) << 16);
   return r;
@@ -67,43 +73,38 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p)
     k[i] = v[i] = make_uint4(0, 0, 0, 0);
     if (row < rows) {
       slot[i] = __ldg(p.slots + t);
-      k[i] = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_token + head[i] * p.k_head) + lane);
-      v[i] = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_token + head[i] * p.v_head) + lane);
+      k[i] = __ldcs(reinterpret_cast<const uint4*>(p.k + wide(t, p.k_token) +
+                                                   wide(head[i], p.k_head)) + lane);
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(p.v + wide(t, p.v_token) +
+                                                   wide(head[i], p.v_head)) + lane);
     }
   }
 #pragma unroll
   for (int i = 0; i < kWriteRows; ++i) {
-    const long long page = slot[i] >> p.c.page_shift;
+    const long long slot_page = slot[i] >> p.c.page_shift;
     bool ok = slot[i] >= 0;
-    if (ok && page >= p.c.num_pages) {
+    if (ok && slot_page >= p.c.num_pages) {
       atomicOr(p.error_word, kErrIndex);
       ok = false;
     }
-    const long long place = slot[i] & (p.c.page_size - 1);
-    uint8_t* kd = p.c.k + page * p.c.k_page + head[i] * p.c.k_head + place * p.c.k_token;
-    uint8_t* vd = p.c.v + page * p.c.v_page + head[i] * p.c.v_head + place * p.c.v_token;
+    const uint32_t page = static_cast<uint32_t>(slot_page);
+    const uint32_t place = static_cast<uint32_t>(slot[i]) & (p.c.page_size - 1);
+    uint8_t* kd = p.c.k + row_offset(page, head[i], place, p.c.k_page, p.c.k_head, p.c.k_token);
+    uint8_t* vd = p.c.v + row_offset(page, head[i], place, p.c.v_page, p.c.v_head, p.c.v_token);
     if constexpr (!kE4M3) {
       if (ok) {
         reinterpret_cast<uint4*>(kd)[lane] = k[i];
         reinterpret_cast<uint4*>(vd)[lane] = v[i];
       }
     } else {
-      const uint32_t kw[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
-      const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      float kf[8], vf[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = unpack16<kBf16>(kw[j]), b = unpack16<kBf16>(vw[j]);
-        kf[2 * j] = a.x, kf[2 * j + 1] = a.y;
-        vf[2 * j] = b.x, vf[2 * j + 1] = b.y;
-      }
       uint32_t ke, ve;
-      const uint2 kc = quantise_row<kLanes>(kf, ke), vc = quantise_row<kLanes>(vf, ve);
+      const uint2 kc = quantise_row<kLanes, kBf16>(k[i], ke);
+      const uint2 vc = quantise_row<kLanes, kBf16>(v[i], ve);
       if (ok) {
         reinterpret_cast<uint2*>(kd)[lane] = kc;
         reinterpret_cast<uint2*>(vd)[lane] = vc;
         if (lane == 0) {
-          const long long at = (page * p.c.heads + head[i]) * p.c.page_size + place;
+          const unsigned long long at = scale_offset(p.c, page, head[i], place);
           p.c.k_scale[at] = static_cast<uint8_t>(ke);
           p.c.v_scale[at] = static_cast<uint8_t>(ve);
         }
@@ -145,9 +146,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
     const int b = static_cast<int>(bh / p.c.heads);
     const int h = static_cast<int>(bh - static_cast<long long>(b) * p.c.heads);
     const int len = min(table_length(p.t, p.c.page_shift, b), p.max_len);
-    const uint8_t* k0 = p.c.k + h * p.c.k_head;
-    const uint8_t* v0 = p.c.v + h * p.c.v_head;
-    long long page[kReadRows];
+    const uint8_t* k0 = p.c.k + wide(h, p.c.k_head) + lane * (kE4M3 ? 8 : 16);
+    const uint8_t* v0 = p.c.v + wide(h, p.c.v_head) + lane * (kE4M3 ? 8 : 16);
+    int page[kReadRows];
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
       const int n = n0 + i * kBlockRows;
@@ -161,22 +162,25 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
       ks[i] = vs[i] = 0;
       if (page[i] >= 0) {
         const int place = (n0 + i * kBlockRows) & (p.c.page_size - 1);
-        const uint8_t* kr = k0 + page[i] * p.c.k_page + place * p.c.k_token;
-        const uint8_t* vr = v0 + page[i] * p.c.v_page + place * p.c.v_token;
+        const uint8_t* kr = k0 + wide(page[i], p.c.k_page) + wide(place, p.c.k_token);
+        const uint8_t* vr = v0 + wide(page[i], p.c.v_page) + wide(place, p.c.v_token);
         if constexpr (kE4M3) {
-          const long long at = (page[i] * p.c.heads + h) * p.c.page_size + place;
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(kr) + lane);
-          const uint2 c = __ldg(reinterpret_cast<const uint2*>(vr) + lane);
+          const unsigned long long at = scale_offset(p.c, page[i], h, place);
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(kr));
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(vr));
           k[i].x = a.x, k[i].y = a.y;
           v[i].x = c.x, v[i].y = c.y;
           ks[i] = __ldg(p.c.k_scale + at);
           vs[i] = __ldg(p.c.v_scale + at);
         } else {
-          k[i] = __ldg(reinterpret_cast<const uint4*>(kr) + lane);
-          v[i] = __ldg(reinterpret_cast<const uint4*>(vr) + lane);
+          k[i] = __ldg(reinterpret_cast<const uint4*>(kr));
+          v[i] = __ldg(reinterpret_cast<const uint4*>(vr));
         }
       }
     }
+    const long long out = (bh * p.max_len + n0) * kLanes + lane;
+    uint4* out_k = reinterpret_cast<uint4*>(p.k) + out;
+    uint4* out_v = reinterpret_cast<uint4*>(p.v) + out;
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
       const int n = n0 + i * kBlockRows;
@@ -185,9 +189,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
         k[i] = widen<kBf16>(make_uint2(k[i].x, k[i].y), scale_value(ks[i]));
         v[i] = widen<kBf16>(make_uint2(v[i].x, v[i].y), scale_value(vs[i]));
       }
-      const long long out = (bh * p.max_len + n) * kLanes + lane;
-      __stcs(reinterpret_cast<uint4*>(p.k) + out, k[i]);
-      __stcs(reinterpret_cast<uint4*>(p.v) + out, v[i]);
+      __stcs(out_k + i * kThreads, k[i]);
+      __stcs(out_v + i * kThreads, v[i]);
     }
   }
 }
@@ -210,22 +213,22 @@ __global__ void __launch_bounds__(128) kv_bounds_kernel(const BoundsParams p) {
     const int first = max(0, len - p.new_tokens) >> p.c.page_shift;
     const int blocks = static_cast<int>((static_cast<long long>(len) + p.c.page_size - 1) >> p.c.page_shift);
     for (int i = first + blockIdx.y; i < blocks; i += gridDim.y) {
-      const long long page = table_page(p.t, p.c.num_pages, b, i);
+      const int page = table_page(p.t, p.c.num_pages, b, i);
       if (page < 0) continue;
       const int rows = min(p.c.page_size, len - (i << p.c.page_shift));
       float lo[8], hi[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) lo[j] = INFINITY, hi[j] = -INFINITY;
       constexpr int kBatch = 4;  // rows whose loads are in flight together
-      const uint8_t* base = p.c.k + page * p.c.k_page + h * p.c.k_head;
-      const uint8_t* scales = p.c.k_scale + (page * p.c.heads + h) * p.c.page_size;
+      const uint8_t* base = p.c.k + wide(page, p.c.k_page) + wide(h, p.c.k_head);
+      const uint8_t* scales = p.c.k_scale + scale_offset(p.c, page, h, 0);
       for (int r0 = group; r0 < rows; r0 += kBatch * kGroups) {
         uint4 c[kBatch];
         uint32_t e[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int r = min(r0 + i * kGroups, rows - 1);  // (the last row again changes nothing)
-          const uint8_t* row = base + r * p.c.k_token;
+          const uint8_t* row = base + wide(r, p.c.k_token);
           if constexpr (kE4M3) {
             const uint2 two = __ldg(reinterpret_cast<const uint2*>(row) + lane);
             c[i].x = two.x, c[i].y = two.y;
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(128) kv_bounds_kernel(const BoundsParams p) {
       for (int j = 0; j < 8; ++j) lo_s[group][lane * 8 + j] = lo[j], hi_s[group][lane * 8 + j] = hi[j];
       __syncthreads();
       // D / 2 pairs of columns, low then high
-      uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds) + (page * p.c.heads + h) * D;
+      uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds) + (wide(page, p.c.heads) + h) * D;
       for (int c = threadIdx.x; c < D; c += 128) {
         const bool high = c >= D / 2;
         const int col = 2 * (high ? c - D / 2 : c);

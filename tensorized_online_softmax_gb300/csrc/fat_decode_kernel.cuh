@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   int load_head;
   auto load_item = [&]() {
     load_head = item_of(p, load, kR, blocks_of_rows).head;
-    load_k = p.c.k + load_head * p.c.k_head;
-    load_v = p.c.v + load_head * p.c.v_head;
+    load_k = p.c.k + wide(load_head, p.c.k_head);
+    load_v = p.c.v + wide(load_head, p.c.v_head);
     load_pages = p.t.pages + load.entry * p.t.stride;
   };
   load_item();
@@ -287,18 +287,18 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       const int place = row & (p.c.page_size - 1);
       int page = __shfl_sync(0xffffffffu, window_page, load.tile - window);
       int valid = min(kRowsPerWarp, load_len - row);
-      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.num_pages)) {
+      if (static_cast<uint32_t>(page) >= p.c.num_pages) {
         atomicOr(p.t.error_word, kErrIndex);
         page = valid = 0;  // zeros in place of rows, and no address made of the page
       }
       const uint32_t pg = static_cast<uint32_t>(page);
-      const uint8_t* k = load_k + pg * p.c.k_page + place * p.c.k_token;
-      const uint8_t* v = load_v + pg * p.c.v_page + place * p.c.v_token;
+      const uint8_t* k = load_k + wide(pg, p.c.k_page) + wide(place, p.c.k_token);
+      const uint8_t* v = load_v + wide(pg, p.c.v_page) + wide(place, p.c.v_token);
       constexpr int kPer = kRowsPerWarp * L::kChunks / 32;  // chunks of K to a lane
       constexpr int kStep = 32 / L::kChunks;                // rows from one to the next
       if (valid == kRowsPerWarp) {
-        const uint8_t* kl = k + r0 * p.c.k_token + c0 * 16;
-        const uint8_t* vl = v + r0 * p.c.v_token + c0 * 16;
+        const uint8_t* kl = k + wide(r0, p.c.k_token) + c0 * 16;
+        const uint8_t* vl = v + wide(r0, p.c.v_token) + c0 * 16;
         if (p.c.k_token == L::kRow && p.c.v_token == L::kRow) {  // rows follow one another
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
             const uint32_t to = stage + chunk_at<L::kChunks>(r0 + i * kStep, c0);
             copy16(to, kl);
             copy16(to + L::kStage / 2, vl);
-            kl += kStep * p.c.k_token;
-            vl += kStep * p.c.v_token;
+            kl += wide(kStep, p.c.k_token);
+            vl += wide(kStep, p.c.v_token);
           }
         }
       } else {
@@ -323,15 +323,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           const uint32_t to = stage + chunk_at<L::kChunks>(r, c0);
           const uint32_t bytes = r < valid ? 16u : 0u;
           const int from = r < valid ? r : 0;
-          copy16(to, k + from * p.c.k_token + c0 * 16, bytes);
-          copy16(to + L::kStage / 2, v + from * p.c.v_token + c0 * 16, bytes);
+          copy16(to, k + wide(from, p.c.k_token) + c0 * 16, bytes);
+          copy16(to + L::kStage / 2, v + wide(from, p.c.v_token) + c0 * 16, bytes);
         }
       }
       if constexpr (kE4M3) {
         if (lane < 2) {
-          const long long at = (static_cast<long long>(pg) * p.c.heads + load_head) * p.c.page_size;
           copy16(stage + L::kStage + lane * 16,
-                 (lane == 0 ? p.c.k_scale : p.c.v_scale) + at + place, valid ? 16u : 0u);
+                 (lane == 0 ? p.c.k_scale : p.c.v_scale) +
+                     scale_offset(p.c, pg, load_head, place),
+                 valid ? 16u : 0u);
         }
       }
     }
@@ -373,11 +374,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       fresh = false;
       const Item it = item_of(p, cur, kR, blocks_of_rows);
       const int row0 = it.row0;
-      const uint8_t* q0 = p.q + it.seq * p.q_batch + (it.head * p.group + row0) * p.q_head;
+      const uint8_t* q0 = p.q + wide(it.seq, p.q_batch) + wide(it.head * p.group + row0, p.q_head);
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         const bool in = row0 + n * 8 + g < p.group;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(q0 + (n * 8 + (in ? g : 0)) * p.q_head);
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(q0 + wide(n * 8 + (in ? g : 0), p.q_head));
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           // the columns of K that this lane's fragment multiplies: 2t, 2t + 1 and 2t + 8, 2t + 9

@@ -45,7 +45,8 @@ BAD_CACHES = [
     (dict(page_size=48), "INVALID_ARG"), (dict(page_size=2048), "INVALID_ARG"),
     (dict(d=96), "INVALID_ARG"), (dict(dtype=3), "INVALID_ARG"), (dict(dtype=-1), "INVALID_ARG"),
     (dict(dtype=E4M3, k_scale=None), "INVALID_ARG"), (dict(k=0x10008), "ALIGNMENT"),
-    (dict(k_token_stride=132), "ALIGNMENT"), (dict(k_head_stride=-2048), "ALIGNMENT"),
+    (dict(k_token_stride=132), "ALIGNMENT"), (dict(k_page_stride=1 << 31), "ALIGNMENT"),
+    (dict(k_head_stride=-2048), "ALIGNMENT"),
     (dict(dtype=E4M3, k_page_stride=4104), "ALIGNMENT"),
     (dict(dtype=E4M3, k_scale=0x30008), "ALIGNMENT"),
 ]
