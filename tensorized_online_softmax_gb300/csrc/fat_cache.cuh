@@ -81,11 +81,12 @@ __device__ __forceinline__ float scale_value(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7FFFFFFFu : e << 23);
 }
 
-// two e4m3 codes -> two fp16 (exact; a NaN code becomes NaN)
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
+// four e4m3 codes -> four fp16 (exact; a NaN code becomes NaN)
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 template <bool kBf16>

@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p)
 // Eight codes of a row with scale s as 16-bit values.
 template <bool kBf16>
 __device__ __forceinline__ uint4 widen(uint2 c, float s) {
-  const uint32_t two[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
-  uint32_t r[4];
+  uint32_t two[4], r[4];
+  e4m3x4_to_f16(c.x, two[0], two[1]);
+  e4m3x4_to_f16(c.y, two[2], two[3]);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+    const float2 f = unpack16<false>(two[j]);
     // exact in bf16 down to its subnormals; fp16 rounds outside its range
     r[j] = pack16<kBf16>(f.x * s, f.y * s);
   }
@@ -242,10 +243,12 @@ __global__ void __launch_bounds__(128) kv_bounds_kernel(const BoundsParams p) {
           float x[8];
           if constexpr (kE4M3) {
             const float s = scale_value(e[i]);
-            const uint32_t two[4] = {c[i].x, c[i].x >> 16, c[i].y, c[i].y >> 16};
+            uint32_t two[4];
+            e4m3x4_to_f16(c[i].x, two[0], two[1]);
+            e4m3x4_to_f16(c[i].y, two[2], two[3]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 f = unpack16<false>(e4m3x2_to_f16x2(two[j]));
+              const float2 f = unpack16<false>(two[j]);
               x[2 * j] = f.x * s, x[2 * j + 1] = f.y * s;
             }
           } else {

@@ -368,8 +368,13 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   bool fresh = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
-    if (loaded < count) issue();
-    copy_commit();
+    // With stages to spare the next copies are issued behind the first MMAs, whose results take a
+    // while (1 to 2 % of the time); two or three stages need them at once.
+    constexpr bool kLate = L::kStages >= 4;
+    if constexpr (!kLate) {
+      if (loaded < count) issue();
+      copy_commit();
+    }
     if (fresh) {
       fresh = false;
       const Item it = item_of(p, cur, kR, blocks_of_rows);
@@ -426,19 +431,20 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           for (int j = 0; j < 4; ++j) o[c][n][j] = 0.f;
       }
     }
-    copy_wait<L::kStages - 1>();
+    copy_wait<kLate ? L::kStages - 2 : L::kStages - 1>();
     __syncwarp();
     const int row = cur.tile * kDecodeTile + warp_row;
     const uint32_t used = stage_out - ring;  // the same in every warp
+    bool issued = !kLate;
     if (row < cur_len) {
       const uint32_t stage = stage_out;
       const int mat = lane / 8, mr = lane % 8;
-      // S = K Q^T, in two chains
-      float s0[kNT][4], s1[kNT][4];
+      // S = K Q^T, in four chains
+      float s0[kNT][4], s1[kNT][4], s2[kNT][4], s3[kNT][4];
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s0[n][j] = s1[n][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s0[n][j] = s1[n][j] = s2[n][j] = s3[n][j] = 0.f;
       {
         const int r = mr + (mat & 1) * 8;
 #pragma unroll
@@ -448,19 +454,24 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           if constexpr (!kE4M3) {
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              mma<kMmaBf16>(s & 1 ? s1[n] : s0[n], a, qf[s][n][0], qf[s][n][1]);
+              mma<kMmaBf16>(s & 2 ? (s & 1 ? s3[n] : s2[n]) : (s & 1 ? s1[n] : s0[n]), a, qf[s][n][0], qf[s][n][1]);
           } else {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t f[4] = {e4m3x2_to_f16x2(a[2 * x]), e4m3x2_to_f16x2(a[2 * x + 1]),
-                                     e4m3x2_to_f16x2(a[2 * x] >> 16),
-                                     e4m3x2_to_f16x2(a[2 * x + 1] >> 16)};
+              uint32_t f[4];
+              e4m3x4_to_f16(a[2 * x], f[0], f[2]);
+              e4m3x4_to_f16(a[2 * x + 1], f[1], f[3]);
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
-                mma<false>(x ? s1[n] : s0[n], f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
+                mma<false>(s & 1 ? (x ? s3[n] : s2[n]) : (x ? s1[n] : s0[n]), f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
             }
           }
         }
+      }
+      if constexpr (kLate) {
+        if (loaded < count) issue();
+        copy_commit();
+        issued = true;
       }
       float ks[2] = {1.f, 1.f}, vs[2] = {0.f, 0.f};
       if constexpr (kE4M3) {
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int rr = j >> 1, cc = j & 1;
-          z[n][j] = (s0[n][j] + s1[n][j]) * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
+          z[n][j] = ((s0[n][j] + s1[n][j]) + (s2[n][j] + s3[n][j])) * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
           zv[n][j] = z[n][j] + vs[rr];
         }
       if (row + kRowsPerWarp > cur_len) {
@@ -564,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
             // of each column together; row i of the MMA tile is column 2 i, row i + 8 is 2 i + 1
             const uint32_t w0 = __byte_perm(a[2 * x], 0, 0x3120);
             const uint32_t w1 = __byte_perm(a[2 * x + 1], 0, 0x3120);
-            const uint32_t f[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w0 >> 16),
-                                   e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w1 >> 16)};
+            uint32_t f[4];
+            e4m3x4_to_f16(w0, f[0], f[1]);
+            e4m3x4_to_f16(w1, f[2], f[3]);
 #pragma unroll
             for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, hi[n][0], hi[n][1]);
 #pragma unroll
@@ -573,6 +585,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           }
         }
       }
+    }
+    if (!issued) {
+      if (loaded < count) issue();
+      copy_commit();
     }
     __syncwarp();  // the stage may be filled again
     stage_out += L::kStage + L::kScales;
