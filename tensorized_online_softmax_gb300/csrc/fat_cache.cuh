@@ -55,9 +55,12 @@ struct TableView {
   unsigned int* error_word;
 };
 
+// (Lengths and pages by plain loads: the choice of blocks writes them while the
+// decode kernel that waits for it has started, which read-only loads forbid.)
+
 // Length of sequence b: at most what the table can hold, never negative.
 __device__ __forceinline__ int table_length(const TableView& t, int page_shift, int b) {
-  const int n = __ldg(t.seq_lens + b);
+  const int n = t.seq_lens[b];
   const long long most = static_cast<long long>(t.width) << page_shift;
   if (n < 0 || n > most) {
     atomicOr(t.error_word, kErrIndex);
@@ -68,7 +71,7 @@ __device__ __forceinline__ int table_length(const TableView& t, int page_shift, 
 
 // Page i of sequence b, or -1 (flagged) if it is not a page of the cache.
 __device__ __forceinline__ int table_page(const TableView& t, uint32_t num_pages, int b, int i) {
-  const int p = __ldg(t.pages + b * t.stride + i);
+  const int p = t.pages[b * t.stride + i];
   if (static_cast<uint32_t>(p) >= num_pages) {
     atomicOr(t.error_word, kErrIndex);
     return -1;

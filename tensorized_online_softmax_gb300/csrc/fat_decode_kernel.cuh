@@ -191,7 +191,8 @@ __device__ __forceinline__ int enter(const DecodeParams& p, DecodePlace& at) {
 }
 
 template <int D, int kNT, bool kE4M3, bool kBf16>
-__global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
+    decode_kernel(const DecodeParams p) {
   using L = Layout<D, kNT, kE4M3>;
   constexpr bool kMmaBf16 = kBf16 && !kE4M3;
   constexpr int kR = 8 * kNT;  // query heads of a block of rows
@@ -200,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   __shared__ DecodePlace start_s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
-  float* join_r = reinterpret_cast<float*>(smem + kWarps * L::kRing);  // [3][warp][kMaxRows]: r, r', l
+  // [3][warp][kMaxRows]: r, r', l
+  float* join_r = reinterpret_cast<float*>(smem + kWarps * L::kRing);
 
   grid_dep_launch();
   grid_dep_wait();
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
   auto load_window = [&]() {
     window = load.tile;
     const long long row = static_cast<long long>(load.tile + lane) * kDecodeTile + warp_row;
-    window_page = row < load_len ? __ldg(load_pages + (row >> p.c.page_shift)) : 0;
+    window_page = row < load_len ? load_pages[row >> p.c.page_shift] : 0;
   };
   load_window();
   int loaded = 0;
@@ -383,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         const bool in = row0 + n * 8 + g < p.group;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(q0 + wide(n * 8 + (in ? g : 0), p.q_head));
+        const uint32_t* q =
+            reinterpret_cast<const uint32_t*>(q0 + wide(n * 8 + (in ? g : 0), p.q_head));
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           // the columns of K that this lane's fragment multiplies: 2t, 2t + 1 and 2t + 8, 2t + 9
@@ -440,11 +443,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
       const uint32_t stage = stage_out;
       const int mat = lane / 8, mr = lane % 8;
       // S = K Q^T, in four chains
-      float s0[kNT][4], s1[kNT][4], s2[kNT][4], s3[kNT][4];
+      float s4[4][kNT][4];
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s0[n][j] = s1[n][j] = s2[n][j] = s3[n][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s4[0][n][j] = s4[1][n][j] = s4[2][n][j] = s4[3][n][j] = 0.f;
       {
         const int r = mr + (mat & 1) * 8;
 #pragma unroll
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
           if constexpr (!kE4M3) {
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              mma<kMmaBf16>(s & 2 ? (s & 1 ? s3[n] : s2[n]) : (s & 1 ? s1[n] : s0[n]), a, qf[s][n][0], qf[s][n][1]);
+              mma<kMmaBf16>(s4[s & 3][n], a, qf[s][n][0], qf[s][n][1]);
           } else {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
               e4m3x4_to_f16(a[2 * x + 1], f[1], f[3]);
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
-                mma<false>(s & 1 ? (x ? s3[n] : s2[n]) : (x ? s1[n] : s0[n]), f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
+                mma<false>(s4[(2 * s + x) & 3][n], f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
             }
           }
         }
@@ -491,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks) deco
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int rr = j >> 1, cc = j & 1;
-          z[n][j] = ((s0[n][j] + s1[n][j]) + (s2[n][j] + s3[n][j])) * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
+          const float s = (s4[0][n][j] + s4[1][n][j]) + (s4[2][n][j] + s4[3][n][j]);
+          z[n][j] = s * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
           zv[n][j] = z[n][j] + vs[rr];
         }
       if (row + kRowsPerWarp > cur_len) {
