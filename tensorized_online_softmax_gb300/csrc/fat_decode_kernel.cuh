@@ -17,14 +17,16 @@
 // when a score exceeds it by more than 8 binades, so the usual tile needs one
 // vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
 // the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and the only
-// rounding that counts is that of the output (without the remainder the e4m3
-// batch below is 3.4 % faster).
+// rounding that counts is that of the output.  fp16 weights are 2^7 at the
+// maximum: they lose nothing above 2^-32 of it.
 //
 // e4m3 caches: the codes become fp16 exactly, the keys' scales multiply S, and
 // the values' scales join the weights, w = 2^(z + log2 s - r'), with a running
 // reference r' of its own: fp16 weights keep their precision relative to the
 // largest weighted row whatever the scales are.  q is brought into fp16's range
-// by a power of two for each head.
+// by a power of two for each head.  For a bf16 output the weights go without
+// the remainder: at most 2^-11 each, 2^-12 on average, against the output's own
+// 2^-9 (with it the batch of 64 sequences is 3.4 % slower).
 //
 // The warps' (r, r', l, O) are joined through shared memory at an item's end;
 // an item that other blocks share leaves a normalised O and its LSE in the
@@ -43,7 +45,7 @@ namespace decode {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRowsPerWarp = kDecodeTile / kWarps;  // 16
 static_assert(kRowsPerWarp == 16, "one MMA tile of positions to a warp");
-constexpr float kRaise = 8.f;  // binades above the reference that are let pass
+constexpr float kRaise = 8.f;  // binades above the maximum at the last raise that are let pass
 
 struct Join {  // what the join kernel needs of the item that starts, unfinished, in a block
   int entry, item;
@@ -63,13 +65,18 @@ struct Layout {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kStage = 2 * kRowsPerWarp * kRow;  // K and V of 16 positions
   static constexpr int kScales = kE4M3 ? 32 : 0;
-  // blocks on an SM (their registers allow no more), and a ring as deep as their share of the
-  // SM's 228 KiB
-  static constexpr int kBlocks = kNT > 1 ? 2 : 3;
-  static constexpr int kRoom = (228 * 1024 / kBlocks - 1024 - 1024) / kWarps;
+  // blocks on an SM: what their registers allow, but three where memory is the bound already
+  // (a fourth saves 7 % of the e4m3 kernel at d = 64, and costs 1 % of the 16-bit one)
+  static constexpr int kBlocks = kNT > 1 ? (D == 64 ? 3 : 2) : (D == 64 && kE4M3 ? 4 : 3);
+  // S is summed in so many chains: an MMA's result takes a while, but registers are scarce
+  // where there are 16 heads (one chain: 2 % there)
+  static constexpr int kChains = kNT > 1 ? 1 : D == 64 ? 2 : 4;
+  // the rings of an SM: enough to cover HBM's latency, and no more, as what is asked for beyond
+  // that slows HBM down (e4m3, d = 128: 2 stages 223 us, 3 226, 4 234 for the batch of 64
+  // sequences; 16-bit, d = 64: 3 stages 29.5 us, 2 30.1, 4 30.0)
+  static constexpr int kRoom = (kE4M3 ? 112 : 150) * 1024 / (kBlocks * kWarps);  // of one warp
   static constexpr int kFit = kRoom / (kStage + kScales);
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static_assert(kStages >= 2, "one stage is filled while another is used");
+  static constexpr int kStages = kFit < 2 ? 2 : kFit;
   static constexpr int kRing = kStages * (kStage + kScales);  // of one warp
   static_assert(8 * D * 4 <= kStage, "a stage holds a warp's O for the join");
   static constexpr int kJoinRows = 3 * kWarps * kMaxRows * 4;
@@ -195,6 +202,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     decode_kernel(const DecodeParams p) {
   using L = Layout<D, kNT, kE4M3>;
   constexpr bool kMmaBf16 = kBf16 && !kE4M3;
+  constexpr bool kRemainder = !(kE4M3 && kBf16);
+  // fp16 weights fill the type's range: 2^7 at the maximum, 2^15 where it was let pass
+  constexpr float kShift = kMmaBf16 ? 0.f : 7.f;
   constexpr int kR = 8 * kNT;  // query heads of a block of rows
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sums[kWarps];
@@ -370,9 +380,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   bool fresh = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
-    // With stages to spare the next copies are issued behind the first MMAs, whose results take a
-    // while (1 to 2 % of the time); two or three stages need them at once.
-    constexpr bool kLate = L::kStages >= 4;
+    // With a stage to spare the next copies are issued behind the first MMAs, whose results take a
+    // while (1 to 3 % of the time); two stages need them at once.
+    constexpr bool kLate = L::kStages >= 3;
     if constexpr (!kLate) {
       if (loaded < count) issue();
       copy_commit();
@@ -442,12 +452,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     if (row < cur_len) {
       const uint32_t stage = stage_out;
       const int mat = lane / 8, mr = lane % 8;
-      // S = K Q^T, in four chains
-      float s4[4][kNT][4];
+      // S = K Q^T
+      float sc[L::kChains][kNT][4];
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int c = 0; c < L::kChains; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s4[0][n][j] = s4[1][n][j] = s4[2][n][j] = s4[3][n][j] = 0.f;
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[c][n][j] = 0.f;
       {
         const int r = mr + (mat & 1) * 8;
 #pragma unroll
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           if constexpr (!kE4M3) {
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              mma<kMmaBf16>(s4[s & 3][n], a, qf[s][n][0], qf[s][n][1]);
+              mma<kMmaBf16>(sc[s % L::kChains][n], a, qf[s][n][0], qf[s][n][1]);
           } else {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
               e4m3x4_to_f16(a[2 * x + 1], f[1], f[3]);
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
-                mma<false>(s4[(2 * s + x) & 3][n], f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
+                mma<false>(sc[(2 * s + x) % L::kChains][n], f, qf[2 * s + x][n][0], qf[2 * s + x][n][1]);
             }
           }
         }
@@ -494,7 +506,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int rr = j >> 1, cc = j & 1;
-          const float s = (s4[0][n][j] + s4[1][n][j]) + (s4[2][n][j] + s4[3][n][j]);
+          float s = sc[0][n][j];
+          if constexpr (L::kChains == 2) s += sc[1][n][j];
+          if constexpr (L::kChains == 4) s = (s + sc[1][n][j]) + (sc[2][n][j] + sc[3][n][j]);
           z[n][j] = s * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
           zv[n][j] = z[n][j] + vs[rr];
         }
@@ -514,16 +528,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           if constexpr (kE4M3) raise |= zv[n][j] > top_v[n][j & 1];
         }
       if (__any_sync(0xffffffffu, raise)) {
-        // r <- the maximum so far; what was summed shrinks by 2^(r_old - r)
+        // r <- the maximum so far, less the shift; what was summed shrinks by 2^(r_old - r)
         auto raise_to = [&](float a, float b, float& r, float& limit) {
           float m = fmaxf(a, b);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
           const float old = limit == -INFINITY ? -INFINITY : r;
-          m = fmaxf(m, old);
+          m = fmaxf(m - kShift, old);
           if (m == -INFINITY) return 1.f;
           r = m;
-          limit = m + kRaise;
+          limit = m + (kShift + kRaise);
           return ex2_approx(old - m);
         };
 #pragma unroll
@@ -553,10 +567,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
         }
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t h = pack_below<kMmaBf16>(w[2 * rr], w[2 * rr + 1]);
-          const float2 back = unpack16<kMmaBf16>(h);
-          hi[n][rr] = transpose8(h);
-          lo[n][rr] = transpose8(pack16<kMmaBf16>(w[2 * rr] - back.x, w[2 * rr + 1] - back.y));
+          if constexpr (kRemainder) {
+            const uint32_t h = pack_below<kMmaBf16>(w[2 * rr], w[2 * rr + 1]);
+            const float2 back = unpack16<kMmaBf16>(h);
+            hi[n][rr] = transpose8(h);
+            lo[n][rr] =
+                transpose8(pack16<kMmaBf16>(w[2 * rr] - back.x, w[2 * rr + 1] - back.y));
+          } else {
+            hi[n][rr] = transpose8(pack16<kMmaBf16>(w[2 * rr], w[2 * rr + 1]));
+          }
         }
       }
       // O^T += V^T P^T
@@ -585,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
 #pragma unroll
             for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, hi[n][0], hi[n][1]);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, lo[n][0], lo[n][1]);
+            for (int n = 0; n < kNT; ++n)
+              if constexpr (kRemainder) mma<false>(o[2 * c + x][n], f, lo[n][0], lo[n][1]);
           }
         }
       }

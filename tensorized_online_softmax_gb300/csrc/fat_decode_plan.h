@@ -21,7 +21,7 @@ namespace fat {
 
 constexpr int kDecodeTile = 64;
 constexpr int kDirectTiles = 8;
-constexpr int kDecodeMaxBlocks = 512;  // what the workspace has room for
+constexpr int kDecodeMaxBlocks = 640;  // what the workspace has room for
 
 FAT_HD int decode_tiles(int len) {
   return len > kDecodeTile ? (len - 1) / kDecodeTile + 1 : 1;

@@ -83,14 +83,18 @@ def pages_for(lens, page_size, spare=3):
     return sum(-(-n // page_size) for n in lens) + spare
 
 
-def check_attention(o, lse, want_o, want_lse, magnitude, what=""):
+def check_attention(o, lse, want_o, want_lse, magnitude, what="", kind=""):
     """o against the 64-bit result: half a step of its type for the rounding, and 2^-12 of
     sum_j p_j |v_j| for the weights.  A score is a sum of d <= 128 products in fp32, off by at
     most d 2^-24 of the sum of their magnitudes: for inputs near N(0, 1) and scale 1/sqrt(d)
     that sum is below 12, so a weight and the total are each off by less than 128 * 2^-24 * 12
     = 9.2e-5, together 1.9e-4 < 2^-12 = 2.4e-4.  The LSE: the same 9.2e-5, and 2^-21 of its
-    value for the logarithm."""
+    value for the logarithm.  With an e4m3 cache and bf16 queries each weight is also rounded
+    to fp16, by at most half a step, 2^-11 of the weight: 2^-11 of sum_j p_j |v_j| more."""
     half = HALF[o.dtype]
+    weight = 2.0 ** -12
+    if kind == "e4m3" and o.dtype is torch.bfloat16:
+        weight += 2.0 ** -11
     o, lse = o.cpu().double(), lse.cpu().double()
     assert torch.equal(torch.isnan(o), torch.isnan(want_o)), what
     assert torch.equal(torch.isnan(lse), torch.isnan(want_lse)), what
@@ -99,7 +103,7 @@ def check_attention(o, lse, want_o, want_lse, magnitude, what=""):
     fine = torch.isfinite(want_o)
     least = 2.0 ** -25 if half == HALF[torch.float16] else 0.0  # half of fp16's least step
     off = (o - want_o).abs()[fine]
-    allowed = (half * want_o.abs() + 2.0 ** -12 * magnitude + least)[fine] + 1e-30
+    allowed = (half * want_o.abs() + weight * magnitude + least)[fine] + 1e-30
     worst = (off / allowed).max().item() if off.numel() else 0.0
     assert worst <= 1.0, f"{what}: o off by {worst:.3g} of what rounding allows"
     inf = torch.isinf(want_lse)
