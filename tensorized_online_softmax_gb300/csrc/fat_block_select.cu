@@ -463,10 +463,10 @@ static int run_scores(const ScoreParams& p, int dev, int sms, cudaStream_t strea
   if (!ready[dev]) return -4;
   const long long bh = static_cast<long long>(p.t.batch) * p.heads;
   // tiles to a warp: as many as leave twelve warps for each SM (the ring fills and q is loaded
-  // once for them), 8 at most
+  // once for them), 16 at most
   const int row_tiles = p.t.width / 16 + (p.t.width % 16 != 0);
   long long tiles = bh * row_tiles / (12ll * sms);
-  tiles = tiles < 1 ? 1 : tiles > 8 ? 8 : tiles;
+  tiles = tiles < 1 ? 1 : tiles > 16 ? 16 : tiles;
   const long long per_block = tiles * kScoreWarps;
   const dim3 grid(static_cast<unsigned>((row_tiles + per_block - 1) / per_block),
                   static_cast<unsigned>(bh < 65535 ? bh : 65535));
