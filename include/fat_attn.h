@@ -360,7 +360,7 @@ int fat_kv_write(const fat_kv_cache* cache, const void* k, const void* v, int dt
  * Read sequences back: k, v become contiguous [batch, heads, max_len, d]
  * tensors of `dtype` (bf16 or fp16; the cache's own type unless it is e4m3),
  * 16-byte aligned.  Rows from a sequence's length on are zeros; positions from
- * max_len on are left out.
+ * max_len (at most 2^30) on are left out.
  */
 int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k, void* v,
                 int dtype, int max_len, cudaStream_t stream);

@@ -138,7 +138,8 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
   if (st == FAT_OK) st = table_view(table, p.c.page_shift, &p.t);
   if (st != FAT_OK) return st;
   const bool e4m3 = cache->dtype == FAT_DTYPE_E4M3;
-  if (!wide_type(dtype) || (!e4m3 && dtype != cache->dtype) || max_len < 1 || !k || !v)
+  if (!wide_type(dtype) || (!e4m3 && dtype != cache->dtype) || max_len < 1 ||
+      max_len > (1 << 30) || !k || !v)
     return FAT_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16)) return FAT_ERR_ALIGNMENT;
   int dev = 0;
