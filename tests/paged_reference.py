@@ -33,6 +33,17 @@ def quantise_row(x):
     return round_e4m3(x / 2.0 ** s) * 2.0 ** s, s + 127
 
 
+def quantise_rows(x):
+    """quantise_row of many finite rows at once ([..., d] fp64): the type's own rounding of the
+    scaled rows."""
+    top = x.abs().amax(-1, keepdim=True)
+    s = torch.full_like(top, -126.0)
+    for e in range(-126, 121):
+        s = torch.where(top > 448 * 2.0 ** e, torch.full_like(s, e + 1.0), s)
+    s = torch.where(top == 0, torch.zeros_like(s), s)
+    return (x * 2.0 ** -s).float().to(torch.float8_e4m3fn).double() * 2.0 ** s
+
+
 def gather(values, pages, n, page_size):
     """Positions 0..n-1 of one sequence: values [P, H, page_size, d] -> [H, n, d]."""
     if n == 0:

@@ -82,6 +82,35 @@ def test_write_then_read(cuda_device, case):
     assert fat.check_device_error() == fat.FAT_OK
 
 
+@pytest.mark.parametrize("typ,kind,d", [("bf16", "e4m3", 128), ("fp16", "e4m3", 64),
+                                         ("bf16", "bf16", 128), ("fp16", "fp16", 64)])
+def test_many_tokens(cuda_device, typ, kind, d):
+    """Calls large enough for several rows to a thread, with ragged ends."""
+    H, ps, lens = 9, 32, [4001, 17, 3333]
+    pages = pages_for(lens, ps)
+    cache = Cache(pages, H, ps, d, kind, "pthd", seed=d)
+    table = make_table(lens, ps, pages, seed=d)
+    slots = torch.cat([table[b, torch.arange(n) // ps].long() * ps + torch.arange(n) % ps
+                       for b, n in enumerate(lens)])
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn((2, len(slots), H, d), generator=g)
+    x = (x * 2.0 ** torch.randint(-6, 7, (2, len(slots), H, 1), generator=g)).to(TYPES[typ])
+    fat.kv_cache_write(x[0].cuda(), x[1].cuda(), cache.k, cache.v, slots.cuda(),
+                       **cache.scale_args)
+    out = fat.kv_cache_read(cache.k, cache.v, table.cuda(),
+                            torch.tensor(lens, dtype=torch.int32).cuda(), 4005, dtype=TYPES[typ],
+                            **cache.scale_args)
+    held = ref.quantise_rows(x.double()) if kind == "e4m3" else x.double()
+    for got, rows in zip(out, held):
+        want = torch.zeros((3, H, 4005, d), dtype=torch.float64)
+        at = 0
+        for b, n in enumerate(lens):
+            want[b, :, :n] = rows[at:at + n].transpose(0, 1)
+            at += n
+        assert torch.equal(got.cpu().double(), want.to(TYPES[typ]).double())
+    assert fat.check_device_error() == fat.FAT_OK
+
+
 def test_quantised_rows_at_the_edges(cuda_device):
     """Zeros, a magnitude exactly at and just above 448 times a power of two, subnormals, the
     largest values, infinities and NaN."""

@@ -194,6 +194,15 @@ def test_reference_rounding_equals_the_type():
                        x.float().to(torch.float8_e4m3fn).double())
 
 
+def test_reference_rows_at_once():
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((40, 64), generator=g, dtype=torch.float64)
+    x = (x * 2.0 ** torch.randint(-40, 40, (40, 1), generator=g)).to(torch.bfloat16).double()
+    x[5] = 0
+    want = np.stack([ref.quantise_row(r)[0] for r in x.numpy()])
+    assert torch.equal(ref.quantise_rows(x), torch.tensor(want))
+
+
 def test_reference_scale_is_the_least():
     for top in (448.0, 448.1, 449.0, 1.75, 1.7500001, 3e38, 1e-30, 2.0 ** -133):
         values, e = ref.quantise_row(np.array([top, -top / 3]))
