@@ -267,7 +267,8 @@ int fat_attn_decode_sparse(const fat_kv_cache* cache, const fat_page_table* tabl
   int st = decode_common(cache, table, q, dtype, q_batch_stride, q_head_stride, q_heads, scale, o,
                          lse, &p);
   if (st != FAT_OK) return st;
-  if (!scores || !blocks || num_blocks < 1 || num_blocks > (1 << 30) || first_blocks < 0 || last_blocks < 0 ||
+  if (!scores || !blocks || num_blocks < 1 || num_blocks > (1 << 30) || first_blocks < 0 ||
+      last_blocks < 0 ||
       static_cast<long long>(first_blocks) + last_blocks > num_blocks || !workspace ||
       workspace_bytes < fat_attn_decode_sparse_workspace_bytes(table->batch, q_heads,
                                                                cache->heads, cache->d, num_blocks))

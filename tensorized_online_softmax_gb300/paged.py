@@ -80,7 +80,7 @@ _DIRECT = 512  # FAT_DECODE_DIRECT: positions of a table that need no workspace
 
 
 def _wrong(name, t, dtypes, dim, device=None):
-    """The ValueError for a tensor that is not what `dtypes`, `dim` and `device` say, if it is not."""
+    """Raises if a tensor is not what `dtypes`, `dim` and `device` say."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
