@@ -320,6 +320,10 @@ size_t fat_attn_bwd_workspace_bytes(int B, int H, int N);
  * never used as an address; it sets FAT_ERR_INDEX for fat_check_device_error,
  * and that sequence's (or token's) results are unspecified.  Table entries
  * behind a sequence's last page are not read.
+ *
+ * A captured graph replays these calls with whatever the tensors hold then
+ * (lengths, pages and slots included); make the first call of each kind, which
+ * loads its kernels, before any stream capture.
  */
 typedef struct fat_kv_cache {
   void* k;

@@ -15,7 +15,10 @@ out of range cannot be refused here: the kernels skip it, and
 
 Every call is asynchronous on ``stream`` (default: torch's current stream of
 the tensors' device), and allocates its outputs and workspace unless they are
-given.  A given workspace must not be shared by calls that overlap.
+given.  A given workspace must not be shared by calls that overlap.  Calls can
+be captured in a graph (after a first call of their kind, which loads the
+kernels); replays use the lengths, pages and slots that the tensors hold then.
+Nothing here is differentiable.
 """
 from __future__ import annotations
 

@@ -507,6 +507,53 @@ def test_calls_on_two_streams_at_once(cuda_device):
         assert all(torch.equal(w[0], o) and torch.equal(w[1], l) for o, l in g)
 
 
+def test_calls_from_several_threads(cuda_device):
+    """Host threads with a stream each, writing to caches of their own and attending to them."""
+    import threading
+
+    made = [setup([1500 + 300 * i, 40, 900], 2, 4, 32, 128, "bf16", ("bf16", "e4m3")[i % 2],
+                  seed=70 + i) for i in range(4)]
+    dev = [(c, t.cuda(), n.cuda(), q.cuda()) for c, t, n, q in made]
+    token = torch.randn((3, 2, 128), device="cuda").to(torch.bfloat16)
+
+    def slots(i):  # the newest position of each sequence
+        _, t, n, _ = made[i]
+        return torch.tensor([int(t[b, (int(n[b]) - 1) // 32]) * 32 + (int(n[b]) - 1) % 32
+                             for b in range(3)]).cuda()
+
+    def run(i, out, times):
+        c, t, n, q = dev[i]
+        for _ in range(times):
+            fat.kv_cache_write(token, token, c.k, c.v, at[i], **c.scale_args)
+            out.append(fat.attn_decode_paged(q, c.k, c.v, t, n, **c.scale_args))
+
+    at = [slots(i) for i in range(4)]
+    want, got, errors = [[] for _ in dev], [[] for _ in dev], []
+    for i in range(4):
+        run(i, want[i], 1)
+    torch.cuda.synchronize()
+
+    def thread(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                run(i, got[i], 12)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # told by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for w, g in zip(want, got):
+        assert len(g) == 12
+        assert all(torch.equal(w[0][0], o) and torch.equal(w[0][1], l) for o, l in g)
+    assert fat.check_device_error() == fat.FAT_OK
+
+
 def test_on_the_current_stream(cuda_device):
     """Calls go to torch's current stream, also where it is not the default one."""
     cache, table, lens_t, q = setup([3000, 77], 2, 4, 64, 128, "bf16", "e4m3", seed=53)
