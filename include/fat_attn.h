@@ -319,7 +319,7 @@ size_t fat_attn_bwd_workspace_bytes(int B, int H, int N);
  * a length below 0 or above width * page_size, or a slot beyond the cache is
  * never used as an address; it sets FAT_ERR_INDEX for fat_check_device_error,
  * and that sequence's (or token's) results are unspecified.  Table entries
- * behind a sequence's last page are not read.
+ * behind a sequence's last page are not used.
  *
  * A captured graph replays these calls with whatever the tensors hold then
  * (lengths, pages and slots included); make the first call of each kind, which

@@ -75,17 +75,27 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScorePara
   for (long long bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
     const int b = static_cast<int>(bh / p.heads);
     const int h = static_cast<int>(bh - static_cast<long long>(b) * p.heads);
-    int len;
-    const int blocks = blocks_of(p.t, p.page_shift, b, len);
     const int first = (blockIdx.x * kScoreWarps + warp) * tiles * 16;
-    const int end = min(first + tiles * 16, p.t.width), stop = min(end, blocks);
+    const int end = min(first + tiles * 16, p.t.width);
+    const int* table = p.t.pages + b * p.t.stride;
+    // the first pages are loaded together with the length, which says later which of them count
+    const int early[2] = {first + lane < end ? table[first + lane] : -1,
+                          first + 32 + lane < end ? table[first + 32 + lane] : -1};
+    int len;
+    const int blocks = blocks_of(p.t, p.page_shift, b, len), stop = min(end, blocks);
     for (int head0 = 0; head0 < p.group; head0 += 8) {
-      // the pages of 32 blocks (two tiles), one to a lane, a step ahead
+      // the pages of 32 blocks (two tiles), one to a lane, a step ahead; -1 where there is none
+      auto usable = [&](int entry, int i) {
+        if (i >= stop) return -1;
+        if (static_cast<uint32_t>(entry) < p.num_pages) return entry;
+        atomicOr(p.t.error_word, kErrIndex);
+        return -1;
+      };
       auto pages_at = [&](int i0) {
         const int i = i0 + lane;
-        return i < stop ? table_page(p.t, p.num_pages, b, i) : -1;
+        return i < stop ? usable(table[i], i) : -1;
       };
-      int page = pages_at(first), page_next = pages_at(first + 32);
+      int page = usable(early[0], first + lane), page_next = usable(early[1], first + 32 + lane);
       int loaded = first;
       uint32_t stage_in = ring, stage_out = ring;
       auto issue = [&]() {
@@ -234,19 +244,28 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
   const long long bh_count = static_cast<long long>(p.t.batch) * p.heads;
   for (long long bh = blockIdx.x; bh < bh_count; bh += gridDim.x) {
     const int b = static_cast<int>(bh / p.heads);
+    const float* scores = p.scores + bh * p.t.width;
+    const int* table = p.t.pages + b * p.t.stride;
+    // scores and pages are loaded with the length, not behind it (the pages where registers allow)
+    constexpr bool kPagesEarly = kKeys > 0 && kKeys <= 8;
+    float s[kKeys ? kKeys : 1];
+    int page[kKeys ? kKeys : 1];
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int r = 0; r < kKeys; ++r) {
+        const int i = (warp * kKeys + r) * 32 + lane;
+        s[r] = i < p.t.width ? __ldg(scores + i) : 0.f;
+        if constexpr (kPagesEarly) page[r] = i < p.t.width ? __ldg(table + i) : 0;
+      }
+    }
     int len;
     const int blocks = blocks_of(p.t, p.page_shift, b, len);
-    const float* scores = p.scores + bh * p.t.width;
     const int take = min(p.num_blocks, blocks);
     // a warp's run of keys: rounds of 32
     const int rounds = kKeys ? kKeys : (blocks + kThreads - 1) / kThreads;
     const int base = warp * rounds * 32 + lane;
     uint32_t held[kKeys ? kKeys : 1];
     if constexpr (kKeys > 0) {
-      float s[kKeys];
-#pragma unroll
-      for (int r = 0; r < kKeys; ++r)
-        s[r] = base + r * 32 < blocks ? __ldg(scores + base + r * 32) : 0.f;
 #pragma unroll
       for (int r = 0; r < kKeys; ++r)
         held[r] = select_key(s[r], base + r * 32, blocks, p.first_blocks, p.last_blocks);
@@ -407,9 +426,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     int* out = p.blocks + bh * p.num_blocks;
     int* pages = p.pages + bh * p.list;
     const uint32_t below = (1u << lane) - 1u;
-    const int* table = p.t.pages + b * p.t.stride;
-    int page[kKeys ? kKeys : 1];  // loaded together: one latency, not one a round
-    if constexpr (kKeys > 0) {
+    if constexpr (kKeys > 0 && !kPagesEarly) {  // (together: one latency, not one a round)
 #pragma unroll
       for (int r = 0; r < kKeys; ++r)
         page[r] = base + r * 32 < blocks ? __ldg(table + base + r * 32) : 0;

@@ -101,15 +101,17 @@ def _tensor(name, t, dtypes, dim, device=None):
     return t
 
 
-def _rows(name, t, shape, writable):
-    """Strides between pages, heads and tokens; those of a dimension of one entry do not matter."""
+def _rows(name, t, pages, heads, writable):
+    """Strides between pages, heads and tokens; those of a dimension of one entry do not matter (a
+    page has 16 rows at least)."""
     a, b, c, row = t.stride()
     if row != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if shape[0] == 1 or shape[1] == 1:  # (a page has 16 rows at least)
-        a, b = a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
-    if writable and not (a and b and c) and any(
-            n > 1 and not x for x, n in zip((a, b, c), shape)):
+    if pages == 1:
+        a = 0
+    if heads == 1:
+        b = 0
+    if writable and ((a == 0 and pages > 1) or (b == 0 and heads > 1) or c == 0):
         raise ValueError(f"{name} is a broadcast view: its rows share memory")
     return a, b, c
 
@@ -126,17 +128,20 @@ def _scale(name, t, shape, device):
 def _cache(k, v, k_scale, v_scale, writable=False):
     """The checked cache, v None where only the keys are read: the packed struct, the device, the
     fat_dtype, and (pages, heads, page_size, d)."""
-    _tensor("k_cache", k, _CACHE, 4)
-    device, kind, shape = k.device, _CACHE[k.dtype], k.shape
+    if not (isinstance(k, torch.Tensor) and k.is_cuda and k.dim() == 4 and k.dtype in _CACHE):
+        _wrong("k_cache", k, _CACHE, 4)
+    device, dtype, shape = k.device, k.dtype, k.shape
+    kind = _CACHE[dtype]
     pages, heads, page_size, d = shape
-    k_rows = _rows("k_cache", k, shape, writable)
-    at, v_rows = 0, (0, 0, 0)
-    if v is not None:
-        if not (isinstance(v, torch.Tensor) and v.device == device and v.dtype is k.dtype
+    k_rows = _rows("k_cache", k, pages, heads, writable)
+    if v is None:
+        at, v_rows = 0, (0, 0, 0)
+    else:
+        if not (isinstance(v, torch.Tensor) and v.device == device and v.dtype is dtype
                 and v.shape == shape):
-            _tensor("v_cache", v, (k.dtype,), 4, device)
+            _wrong("v_cache", v, (dtype,), 4, device)
             raise ValueError("k_cache and v_cache must have the same shape")
-        at, v_rows = v.data_ptr(), _rows("v_cache", v, shape, writable)
+        at, v_rows = v.data_ptr(), _rows("v_cache", v, pages, heads, writable)
     ks = vs = 0
     if kind == _E4M3:
         ks = _scale("k_scale", k_scale, shape, device)
@@ -167,7 +172,9 @@ def _table(page_table, seq_lens, device):
 
 def _query(q, batch, heads, d, device):
     """q [B, Hq, d] -> its pointer, type, strides and head count as C arguments."""
-    _tensor("q", q, _WIDE, 3, device)
+    if not (isinstance(q, torch.Tensor) and q.device == device and q.dim() == 3
+            and q.dtype in _WIDE):
+        _wrong("q", q, _WIDE, 3, device)
     b, h, c = q.shape
     if b != batch or c != d or h < 1 or h % heads:
         raise ValueError(f"q must be [{batch}, a multiple of {heads}, {d}], "
@@ -281,9 +288,9 @@ def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scal
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} queries, not {q.dtype}")
     fresh = []
     if out is None:
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-        lse = torch.empty((batch, query[4]), dtype=torch.float32, device=device)
-        fresh += [o, lse]
+        o = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
+        lse = q.new_empty((batch, query[4]), dtype=torch.float32)
+        fresh += (o, lse)
     else:
         o = _output("o", out[0], q.shape, q.dtype, device)
         lse = _output("lse", out[1], (batch, query[4]), torch.float32, device)
