@@ -38,7 +38,7 @@
 // 0.93 of the measured copy rate (the stream itself 0.985; the rest is the plan,
 // 2.5 us to the first rows, and 4 us of end and join); one sequence of 131072
 // (537 MB): 85.2 us; 64 sequences of 4096 to 16384, groups of 8, e4m3 (1417 MB):
-// 223 us, 0.94; 13 of 0 to 4097, 20 heads, d = 64, fp16 (148 MB): 30 us, 0.73.
+// 220 to 223 us, 0.94; 13 of 0 to 4097, 20 heads, d = 64, fp16 (148 MB): 30 us, 0.73.
 #pragma once
 
 #include "fat_cache.cuh"
@@ -78,9 +78,9 @@ struct Layout {
   // S is summed in so many chains: an MMA's result takes a while, but registers are scarce
   // where there are 16 heads (one chain: 2 % there)
   static constexpr int kChains = kNT > 1 ? 1 : D == 64 ? 2 : 4;
-  // the rings of an SM: enough to cover HBM's latency, and no more, as what is asked for beyond
-  // that slows HBM down (e4m3, d = 128: 2 stages 223 us, 3 226, 4 234 for the 64 sequences
-  // above; 16-bit, d = 64: 3 stages 29.5 us, 2 30.1, 4 30.0 for the 13)
+  // the rings of an SM: deeper ones gain nothing once HBM's latency is covered (e4m3, d = 128:
+  // 2 stages 223 us, 3 226, 4 234 for the 64 sequences above, when they were compared; 16-bit,
+  // d = 64: 3 stages 29.5 us, 2 30.1, 4 30.0 for the 13)
   static constexpr int kRoom = (kE4M3 ? 112 : 150) * 1024 / (kBlocks * kWarps);  // of one warp
   static constexpr int kFit = kRoom / (kStage + kScales);
   static constexpr int kStages = kFit < 2 ? 2 : kFit;
