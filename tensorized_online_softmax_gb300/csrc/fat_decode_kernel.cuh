@@ -22,8 +22,9 @@
 //
 // e4m3 caches: the codes become fp16 exactly, the keys' scales multiply S, and
 // the values' scales join the weights, w = 2^(z + log2 s - r'), with a running
-// reference r' of its own: fp16 weights keep their precision relative to the
-// largest weighted row whatever the scales are.  q is brought into fp16's range
+// reference r' of its own, set by the rows that are not all zeros: fp16 weights
+// keep their precision relative to the largest w 2^8 (a row's largest code is
+// near 2^8, as written) whatever the scales are.  q is brought into fp16's range
 // by a power of two for each head.  For a bf16 output the weights go without
 // the remainder: at most 2^-11 each, 2^-12 on average, against the output's own
 // 2^-9 (the MMAs and packing saved are 3 to 13 % of the time).
@@ -538,6 +539,31 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           if constexpr (kE4M3) raise |= zv[n][j] > top_v[n][j & 1];
         }
       if (__any_sync(0xffffffffu, raise)) {
+        if constexpr (kE4M3) {
+          // A row of zeros in V adds nothing whatever its scale byte says (a written one says 1,
+          // far above its neighbours'): it must not set r'.  Two lanes look at a row's codes.
+          uint32_t held = 0;
+#pragma unroll
+          for (int c = 0; c < L::kChunks / 2; ++c) {
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(stage + L::kStage / 2 +
+                               chunk_at<L::kChunks>(lane >> 1, (lane & 1) * (L::kChunks / 2) + c))
+                         : "memory");
+            held |= x[0] | x[1] | x[2] | x[3];
+          }
+          held &= 0x7F7F7F7Fu;  // (-0 is zero)
+          const uint32_t rows = __ballot_sync(0xffffffffu, held != 0);
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            const bool zero = (rows >> (2 * (g + 8 * rr)) & 3u) == 0;
+            if (zero && vs[rr] == vs[rr]) {  // (scale byte 255: NaN, not zeros)
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) zv[n][2 * rr] = zv[n][2 * rr + 1] = -INFINITY;
+            }
+          }
+        }
         // r <- the maximum so far, less the shift; what was summed shrinks by 2^(r_old - r)
         auto raise_to = [&](float a, float b, float& r, float& limit) {
           float m = fmaxf(a, b);
@@ -677,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
               m = fmaxf(m, r[w * kMaxRows]);
               mv = fmaxf(mv, r[(kWarps + w) * kMaxRows]);
             }
-            const float base = m == -INFINITY ? 0.f : m, base_v = mv == -INFINITY ? 0.f : mv;
+            // (no r': all of V is zeros, and so is O)
+            const float base = m == -INFINITY ? 0.f : m, base_v = mv == -INFINITY ? base : mv;
             float l = 0.f, acc[kPer] = {};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -697,9 +724,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
                 acc[1] = fmaf(x.y, f, acc[1]);
               }
             }
-            const float scale = l == 0.f ? 0.f : exp2f(base_v - base) / l;
+            const float scale = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) acc[j] *= scale;
+            if constexpr (kE4M3) {  // (2^(r' - r) / l could be a subnormal)
+              const float f = exp2f(base_v - base);
+#pragma unroll
+              for (int j = 0; j < kPer; ++j) acc[j] *= f;
+            }
             const float lse = l == 0.f ? -INFINITY : base + log2f(l);
             if (whole) {
               const long long at =
