@@ -15,7 +15,8 @@ out of range cannot be refused here: the kernels skip it, and
 
 Every call is asynchronous on ``stream`` (default: torch's current stream of
 the tensors' device), and allocates its outputs and workspace unless they are
-given.  A given workspace must not be shared by calls that overlap.  Calls can
+given, from that stream's memory: they need no wait for the current stream.
+(Inputs, and outputs that are given, are the caller's to order.)  A given workspace must not be shared by calls that overlap.  Calls can
 be captured in a graph (after a first call of their kind, which loads the
 kernels); replays use the lengths, pages and slots that the tensors hold then.
 Nothing here is differentiable.
@@ -203,16 +204,28 @@ def _output(name, t, shape, dtype, device):
     return t
 
 
-def _stream(stream, device, fresh):
-    """The stream's handle; tensors allocated by this call are kept for a stream that is not the
-    one they were allocated on."""
+def _given(stream, device):
+    """A given stream as a torch stream; None stands for the current one."""
+    if stream is None or hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (from _given).  It comes from that stream's own memory:
+    a block of another stream's may still be in use there.  The current stream is noted as a
+    user, so that it may read the tensor until it is done, whenever the caller lets go of it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    for t in fresh:
-        t.record_stream(stream)
-    return stream.cuda_stream
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _handle(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None \
+        else stream.cuda_stream
 
 
 def _call(name, device, *args):
@@ -250,7 +263,7 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
     _call("fat_kv_write", device, cache, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype], *k_strides,
-          *v_strides, slots.data_ptr(), shape[0], _stream(stream, device, ()))
+          *v_strides, slots.data_ptr(), shape[0], _handle(_given(stream, device), device))
 
 
 def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype=None,
@@ -269,32 +282,33 @@ def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype
     shape = (batch, heads, int(max_len), d)
     if shape[2] < 1:
         raise ValueError("max_len must be at least 1")
-    fresh = ()
+    stream = _given(stream, device)
     if out is None:
-        fresh = k, v = (torch.empty(shape, dtype=dtype, device=device),
-                        torch.empty(shape, dtype=dtype, device=device))
+        k, v = (_empty(shape, dtype, device, stream) for _ in range(2))
     else:
         k, v = (_output(n, x, shape, dtype, device) for n, x in zip(("k", "v"), out))
     _call("fat_kv_read", device, cache, table, k.data_ptr(), v.data_ptr(), _WIDE[dtype], shape[2],
-          _stream(stream, device, fresh))
+          _handle(stream, device))
     return k, v
 
 
-def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out):
+def _decode_arguments(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out, stream):
     cache, device, kind, shape = _cache(k_cache, v_cache, k_scale, v_scale)
     table, batch, width = _table(page_table, seq_lens, device)
     query = _query(q, batch, shape[1], shape[3], device)
     if kind != _E4M3 and q.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} queries, not {q.dtype}")
-    fresh = []
-    if out is None:
+    stream = _given(stream, device)
+    if out is None and stream is None:  # (the quickest way to the same)
         o = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
         lse = q.new_empty((batch, query[4]), dtype=torch.float32)
-        fresh += (o, lse)
+    elif out is None:
+        o = _empty(q.shape, q.dtype, device, stream)
+        lse = _empty((batch, query[4]), torch.float32, device, stream)
     else:
         o = _output("o", out[0], q.shape, q.dtype, device)
         lse = _output("lse", out[1], (batch, query[4]), torch.float32, device)
-    return (cache, table, *query), device, shape, batch, width, o, lse, fresh
+    return (cache, table, *query), device, shape, batch, width, o, lse, stream
 
 
 @functools.lru_cache(maxsize=256)
@@ -308,13 +322,11 @@ def attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, d: int,
     return lib.fat_attn_decode_sparse_workspace_bytes(batch, q_heads, kv_heads, d, num_blocks)
 
 
-def _workspace(workspace, sizes, device, fresh):
+def _workspace(workspace, sizes, device, stream):
     """The workspace's address and size; allocated if not given."""
     if workspace is None:
         nbytes = attn_decode_workspace_bytes(*sizes)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        fresh.append(workspace)
-        return workspace.data_ptr(), nbytes
+        return _empty((nbytes,), torch.uint8, device, stream).data_ptr(), nbytes
     _tensor("workspace", workspace, (torch.uint8,), 1, device)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -332,14 +344,14 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale: float | 
     a CUDA uint8 tensor of :func:`attn_decode_workspace_bytes` bytes; a table for
     512 positions at most needs none.
     """
-    args, device, (_, heads, page_size, d), batch, width, o, lse, fresh = _decode_arguments(
-        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out)
+    args, device, (_, heads, page_size, d), batch, width, o, lse, stream = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out, stream)
     if workspace is None and width * page_size <= _DIRECT:
         work = None, 0
     else:
-        work = _workspace(workspace, (batch, q.shape[1], heads, d), device, fresh)
+        work = _workspace(workspace, (batch, q.shape[1], heads, d), device, stream)
     _call("fat_attn_decode_paged", device, *args, d ** -0.5 if scale is None else scale,
-          o.data_ptr(), lse.data_ptr(), *work, _stream(stream, device, fresh))
+          o.data_ptr(), lse.data_ptr(), *work, _handle(stream, device))
     return o, lse
 
 
@@ -362,7 +374,7 @@ def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | Non
     if not 1 <= new_tokens <= 0x7fffffff:
         raise ValueError("new_tokens must be at least 1")
     _call("fat_kv_block_bounds", device, cache, table, new_tokens, bounds.data_ptr(),
-          _WIDE[bounds.dtype], _stream(stream, device, ()))
+          _WIDE[bounds.dtype], _handle(_given(stream, device), device))
     return bounds
 
 
@@ -383,14 +395,13 @@ def kv_block_scores(q, bounds, page_table, seq_lens, page_size: int, *, out=None
     query = _query(q, batch, heads, d, device)
     if q.dtype is not bounds.dtype:
         raise ValueError("q and bounds must have the same type")
-    fresh = ()
+    stream = _given(stream, device)
     if out is None:
-        out = torch.empty((batch, heads, width), dtype=torch.float32, device=device)
-        fresh = (out,)
+        out = _empty((batch, heads, width), torch.float32, device, stream)
     else:
         _output("out", out, (batch, heads, width), torch.float32, device)
     _call("fat_kv_block_scores", device, *query, bounds.data_ptr(), pages, heads, int(page_size),
-          d, table, out.data_ptr(), _stream(stream, device, fresh))
+          d, table, out.data_ptr(), _handle(stream, device))
     return out
 
 
@@ -410,8 +421,8 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
     num_blocks], the choice in rising order, then -1.  ``out``: optional
     ``(o, lse, blocks)``.
     """
-    args, device, (_, heads, _, d), batch, width, o, lse, fresh = _decode_arguments(
-        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out)
+    args, device, (_, heads, _, d), batch, width, o, lse, stream = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out, stream)
     num_blocks = int(num_blocks)
     if num_blocks < 1 or first_blocks < 0 or last_blocks < 0 or \
             first_blocks + last_blocks > num_blocks:
@@ -419,13 +430,11 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
     _output("scores", scores, (batch, heads, width), torch.float32, device)
     shape = (batch, heads, num_blocks)
     if out is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=device)
-        fresh.append(blocks)
+        blocks = _empty(shape, torch.int32, device, stream)
     else:
         blocks = _output("blocks", out[2], shape, torch.int32, device)
-    work = _workspace(workspace, (batch, q.shape[1], heads, d, num_blocks), device, fresh)
+    work = _workspace(workspace, (batch, q.shape[1], heads, d, num_blocks), device, stream)
     _call("fat_attn_decode_sparse", device, *args, scores.data_ptr(), num_blocks,
           int(first_blocks), int(last_blocks), d ** -0.5 if scale is None else scale,
-          o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work,
-          _stream(stream, device, fresh))
+          o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work, _handle(stream, device))
     return o, lse, blocks
