@@ -160,12 +160,35 @@ def status_string(status: int) -> str:
     return names.get(status, "FAT_ERR_UNKNOWN")
 
 
-def _stream_handle(stream):
+def _stream_handle(stream, device=None):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _given(stream, device):
+    """A given stream as a torch stream; None stands for the current one."""
+    import torch
+
+    if stream is None or hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (from _given).  It comes from that stream's own memory:
+    a block of another stream's may still be in use there.  The current stream is noted as a
+    user, so that it may read the tensor until it is done, whenever the caller lets go of it."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _check_inputs(q, k, v, dtypes):
@@ -202,7 +225,8 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, X: int =
     subtract a reference offset (fat_zmode: bf16, X = 128, tensorized only).
     ``block_mode="per_tile"`` launches one thread block per 128-row query tile
     instead of one per SM taking tiles in turn (fat_block_mode).
-    The call is asynchronous on ``stream`` (default: torch's current stream).
+    The call is asynchronous on ``stream`` (default: torch's current stream);
+    outputs and workspaces that it allocates come from that stream's memory.
     """
     import torch
 
@@ -213,9 +237,10 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, X: int =
     B, H, N, d = q.shape
     if scale is None:
         scale = d ** -0.5
+    stream = _given(stream, q.device)
     if out is None:
-        o = torch.empty((B, H, N, d), dtype=torch.float32, device=q.device)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        o = _empty((B, H, N, d), torch.float32, q.device, stream)
+        lse = _empty((B, H, N), torch.float32, q.device, stream)
     else:
         o, lse = out
     p = FatParams()
@@ -235,7 +260,7 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, X: int =
     p.fallback_rows = fallback_rows.data_ptr() if fallback_rows is not None else None
     p.wait_poll_limit = int(wait_poll_limit)
     p.wait_timeout_ns = int(wait_timeout_ns)
-    p.stream = _stream_handle(stream).value
+    p.stream = _stream_handle(stream, q.device).value
     p.trace = trace.data_ptr() if trace is not None else None
     with torch.cuda.device(q.device):
         st = lib.fat_attn_fwd_ex(ctypes.byref(p))
@@ -279,22 +304,23 @@ def attn_fwd_splitkv(q, k, v, causal: bool = False, scale: float | None = None, 
         raise ValueError("k and v must be [B, H, Nk, d] with q's B, H, d")
     if scale is None:
         scale = d ** -0.5
+    stream = _given(stream, q.device)
     with torch.cuda.device(q.device):
         if num_splits is None:
             num_splits = lib.fat_attn_splitkv_default_splits(B, H, Nq, Nk)
         nbytes = lib.fat_attn_splitkv_workspace_bytes(B, H, Nq, d, int(num_splits))
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty((nbytes,), torch.uint8, q.device, stream)
         if out is None:
-            o = torch.empty((B, H, Nq, d), dtype=torch.float32, device=q.device)
-            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+            o = _empty((B, H, Nq, d), torch.float32, q.device, stream)
+            lse = _empty((B, H, Nq), torch.float32, q.device, stream)
         else:
             o, lse = out
         st = lib.fat_attn_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                       lse.data_ptr(), B, H, Nq, Nk, d, int(bool(causal)),
                                       float(scale), int(X), int(num_splits),
                                       workspace.data_ptr(), workspace.numel(),
-                                      _stream_handle(stream))
+                                      _stream_handle(stream, q.device))
     if st != FAT_OK:
         raise FatError(st, "fat_attn_fwd_splitkv")
     return o, lse
@@ -323,19 +349,21 @@ def attn_bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
         raise ValueError("o must be fp32 [B, H, N, d] and lse fp32 [B, H, N]")
     if scale is None:
         scale = d ** -0.5
+    stream = _given(stream, q.device)
     with torch.cuda.device(q.device):
         nbytes = lib.fat_attn_bwd_workspace_bytes(B, H, N)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty((nbytes,), torch.uint8, q.device, stream)
         if out is None:
-            dq, dk, dv = (torch.empty((B, H, N, d), dtype=torch.float32, device=q.device)
+            dq, dk, dv = (_empty((B, H, N, d), torch.float32, q.device, stream)
                           for _ in range(3))
         else:
             dq, dk, dv = out
         st = lib.fat_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                               lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                               dv.data_ptr(), B, H, N, d, int(bool(causal)), float(scale),
-                              workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+                              workspace.data_ptr(), workspace.numel(),
+                              _stream_handle(stream, q.device))
     if st != FAT_OK:
         raise FatError(st, "fat_attn_bwd")
     return dq, dk, dv
@@ -373,14 +401,15 @@ def attn_fwd_host(q, k, v, causal: bool = False, scale: float | None = None, X: 
     for name, t, shape in (("o", o, (B, H, N, d)), ("lse", lse, (B, H, N))):
         if t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_pinned():
             raise ValueError(f"{name} must be a page-locked fp32 host tensor of shape {shape}")
+    stream = _given(stream, dev)
     with torch.cuda.device(dev):
         nbytes = lib.fat_attn_fwd_host_workspace_bytes(B, H, N, d, int(heads_per_chunk))
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = _empty((nbytes,), torch.uint8, dev, stream)
         st = lib.fat_attn_fwd_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                    lse.data_ptr(), B, H, N, d, int(bool(causal)), float(scale),
                                    int(X), int(heads_per_chunk), workspace.data_ptr(),
-                                   workspace.numel(), _stream_handle(stream))
+                                   workspace.numel(), _stream_handle(stream, dev))
     if st != FAT_OK:
         raise FatError(st, "fat_attn_fwd_host")
     return o, lse

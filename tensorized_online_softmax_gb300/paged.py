@@ -29,7 +29,7 @@ import struct
 
 import torch
 
-from . import DTYPES, FatError, load_library
+from . import DTYPES, FatError, _empty, _given, load_library
 
 _P, _I, _L, _F, _Z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
                       ctypes.c_size_t)
@@ -201,25 +201,6 @@ def _output(name, t, shape, dtype, device):
     _tensor(name, t, (dtype,), len(shape), device)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)}")
-    return t
-
-
-def _given(stream, device):
-    """A given stream as a torch stream; None stands for the current one."""
-    if stream is None or hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor for work on `stream` (from _given).  It comes from that stream's own memory:
-    a block of another stream's may still be in use there.  The current stream is noted as a
-    user, so that it may read the tensor until it is done, whenever the caller lets go of it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
