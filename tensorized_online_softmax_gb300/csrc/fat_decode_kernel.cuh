@@ -25,7 +25,9 @@
 // reference r' of its own, set by the rows that are not all zeros: fp16 weights
 // keep their precision relative to the largest w 2^8 (a row's largest code is
 // near 2^8, as written) whatever the scales are.  q is brought into fp16's range
-// by a power of two for each head.  For a bf16 output the weights go without
+// by a power of two for each head, without loss: a query with elements more than
+// 32 binades apart takes its low parts by a second pass over the staged keys.
+// For a bf16 output the weights go without
 // the remainder: at most 2^-11 each, 2^-12 on average, against the output's own
 // 2^-9 (the MMAs and packing saved are 3 to 13 % of the time).
 //
@@ -167,6 +169,18 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return static_cast<uint32_t>(r * kChunks + (c ^ ((r >> 1) & 3))) * 16u;
 }
 
+// bf16 queries as fp16 scaled by a power of two, `down`: the parts that are left
+// behind, as fp16 times 2^39 (an element below 2^-17 there is a subnormal, off by
+// 2^-25 at most; larger ones are exact).
+constexpr float kLowScale = 0x1p39f;
+__device__ __forceinline__ uint32_t low_part(uint32_t two, float down) {
+  const float2 f = unpack16<true>(two);
+  const float x = f.x * down, y = f.y * down;
+  const float2 held = unpack16<false>(pack16<false>(x, y));
+  return pack16<false>(fabsf(x) < 0x1p-16f ? (x - held.x) * kLowScale : 0.f,
+                       fabsf(y) < 0x1p-16f ? (y - held.y) * kLowScale : 0.f);
+}
+
 // Inclusive prefix sum over the block's threads.
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,
                                                 long long& total) {
@@ -219,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sums[kWarps];
   __shared__ DecodePlace start_s;
+  __shared__ float down_s[kWarps][kR];  // the power of two that a head's query was scaled by
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   // [3][warp][kMaxRows]: r, r', l
@@ -388,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   // the references r and r' (0 while there is none), what raises them (-inf), and the sums
   float ref[kNT][2], ref_v[kNT][2], top[kNT][2], top_v[kNT][2], sum[kNT][2];
   bool fresh = true;
+  bool low = false;  // the queries have a part below fp16's range
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     // With a stage to spare the next copies are issued behind the first MMAs, whose results take a
@@ -399,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     }
     if (fresh) {
       fresh = false;
+      low = false;
       const Item it = item_of(p, cur, kR, blocks_of_rows);
       const int row0 = it.row0;
       const uint8_t* q0 = p.q + wide(it.seq, p.q_batch) + wide(it.head * p.group + row0, p.q_head);
@@ -415,21 +432,27 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           qf[s][n][1] = in ? __ldg(q + s * 8 + (kE4M3 ? 2 * t + 1 : t + 4)) : 0u;
         }
         if constexpr (kE4M3) {
-          float most = 0.f;
+          // magnitudes compare as integers, two at a time: the largest, and the least but zero, - 1
+          uint32_t most = 0, least = 0xFFFFFFFFu;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float2 f = unpack16<kBf16>(qf[s][n][j]);
-              most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+              const uint32_t m = qf[s][n][j] & 0x7FFF7FFFu;
+              most = __vmaxu2(most, m);
+              if constexpr (kBf16) least = __vminu2(least, __vsub2(m, 0x00010001u));
             }
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          // largest magnitude into [1, 2) (a row with an infinity stays as it is)
-          const uint32_t e = most > 0.f && most < INFINITY
-                                 ? min(max(__float_as_uint(most) >> 23, 1u), 253u)
-                                 : 127u;
-          const float down = __uint_as_float((254u - e) << 23);
+          most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          most = __float_as_uint(unpack16<kBf16>(max(most >> 16, most & 0xFFFFu)).x);
+          // The largest magnitude into [2^15, 2^16): fp16 queries stay exact, and a bf16 element
+          // keeps all its bits down to 2^-32 of the largest; what is below goes by a second pass
+          // over the keys (`low`).  (255: an infinity, beside which all others stay finite.)
+          const uint32_t e = most > 0 ? min(max(most >> 23, 16u), 254u) : 142u;
+          if constexpr (kBf16)
+            low |= ((min(least >> 16, least & 0xFFFFu) + 1u) >> 7) + 32u < e;
+          const float down = __uint_as_float((269u - e) << 23);
+          if (t == 0) down_s[warp][n * 8 + g] = down;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -437,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
               const float2 f = unpack16<kBf16>(qf[s][n][j]);
               qf[s][n][j] = pack16<false>(f.x * down, f.y * down);
             }
-          const float up = __uint_as_float(e << 23) * p.scale_log2;
+          const float up = __uint_as_float((e - 15u) << 23) * p.scale_log2;
           factor[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
           factor[n][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
         } else {
@@ -453,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[c][n][j] = 0.f;
       }
+      if constexpr (kE4M3 && kBf16) low = __any_sync(0xffffffffu, low);
     }
     copy_wait<kLate ? L::kStages - 2 : L::kStages - 1>();
     __syncwarp();
@@ -470,6 +494,39 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sc[c][n][j] = 0.f;
+      if constexpr (kE4M3 && kBf16) {
+        if (low) {  // (hardly ever: the low parts of q, made again from q)
+          const Item it = item_of(p, cur, kR, blocks_of_rows);
+          const uint8_t* q0 =
+              p.q + wide(it.seq, p.q_batch) + wide(it.head * p.group + it.row0, p.q_head);
+          const int r = mr + (mat & 1) * 8;
+#pragma unroll 1
+          for (int s = 0; s < L::kChunks / 2; ++s) {
+            uint32_t a[4];
+            ldsm4(a, stage + chunk_at<L::kChunks>(r, 2 * s + (mat >> 1)));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t f[4];
+              e4m3x4_to_f16(a[2 * x], f[0], f[2]);
+              e4m3x4_to_f16(a[2 * x + 1], f[1], f[3]);
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) {
+                const bool in = it.row0 + n * 8 + g < p.group;
+                const uint32_t* q =
+                    reinterpret_cast<const uint32_t*>(q0 + wide(n * 8 + (in ? g : 0), p.q_head)) +
+                    (2 * s + x) * 8 + 2 * t;
+                const float down = down_s[warp][n * 8 + g];
+                mma<false>(sc[0][n], f, low_part(in ? __ldg(q) : 0u, down),
+                           low_part(in ? __ldg(q + 1) : 0u, down));
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[0][n][j] *= 1.f / kLowScale;
+        }
+      }
       {
         const int r = mr + (mat & 1) * 8;
 #pragma unroll

@@ -100,3 +100,53 @@ def test_e4m3_values_all_zeros(cuda_device, typ, lens):
         # a score is off by at most 64 * 2^-24 of its sum of magnitudes, |want| here
         off = (lse.cpu().double() - want).abs() - 2.0 ** -18 * want.abs()
         assert off.max() <= 2.0 ** -21 * want.abs().max()
+
+
+@pytest.mark.parametrize("typ,binades", [("bf16", 16), ("bf16", 23), ("bf16", 30), ("fp16", 16),
+                                         ("fp16", 22)])
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 1), (64, 12)])
+def test_e4m3_queries_of_a_wide_range(cuda_device, typ, binades, d, group):
+    """Half of a query's elements lie `binades` below the others and decide alone: the keys are
+    zero where the query is large.  The scores' standard deviation is 2, and their sums of
+    magnitudes are below 15, for which check_attention's 2^-12 holds: 128 * 2^-24 * 15 = 1.14e-4,
+    of the weight and of the total."""
+    lens, heads = [300, 77], 2
+    g = torch.Generator().manual_seed(binades + d)
+    q = torch.randn((len(lens), heads * group, d), generator=g) * 2.0 ** 12
+    q[..., d // 2:] *= 2.0 ** -binades
+    k = torch.randn((sum(lens), heads, d), generator=g)
+    k *= 2.0 * math.sqrt(2.0) * 2.0 ** (binades - 12)  # (sqrt(d / 2) terms, scale 1 / sqrt(d))
+    k[..., :d // 2] = 0
+    v = torch.randn((sum(lens), heads, d), generator=g)
+    q, k, v = (t.to(TYPES[typ]) for t in (q, k, v))
+    assert all(torch.isfinite(t).all() for t in (q, k, v))
+    cache, table = filled(lens, heads, 16, d, "e4m3", k, v, seed=6)
+    check(cache, table, lens, q)
+
+
+def test_e4m3_queries_of_extreme_magnitude(cuda_device):
+    """bf16 queries near the type's largest and least values, over keys that undo it."""
+    lens, d = [100] * 6, 64
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn((6, 1, d), generator=g)
+    k = torch.randn((600, 1, d), generator=g)
+    powers = [125, 110, 0, -110, -115, -124]
+    for b, p in enumerate(powers):
+        q[b] *= 2.0 ** p
+        k[100 * b:100 * (b + 1)] *= 2.0 ** max(-110, min(110, -p))
+        q[b] = q[b].clamp(-3e38, 3e38)
+    v = torch.randn((600, 1, d), generator=g)
+    q, k, v = (t.to(torch.bfloat16) for t in (q, k, v))
+    assert torch.isfinite(q).all() and (q != 0).float().mean() > 0.9
+    cache, table = filled(lens, 1, 16, d, "e4m3", k, v, seed=7)
+    o, lse = fat.attn_decode_paged(q.cuda(), cache.k, cache.v, table.cuda(),
+                                   torch.tensor(lens, dtype=torch.int32).cuda(),
+                                   **cache.scale_args)
+    kk, vv = cache.held()
+    want = ref.decode(q.double(), kk, vv, table, lens, 16, 0.125)
+    for b in (1, 2, 3):
+        check_attention(o[b], lse[b], *(x[b] for x in want), what=f"2^{powers[b]}", kind="e4m3")
+    # scores that a power more or less on one side makes huge (NaN only where fp32 has no value)
+    # or nothing at all
+    assert (lse[4:].cpu().double() - want[1][4:]).abs().max() <= 2e-4
+    assert torch.isfinite(o[4:]).all()
