@@ -14,11 +14,12 @@
 //     S[16, heads] = K Q^T,   z = scale log2(e) S   (-inf behind the length)
 //     p = 2^(z - r),  l += p,   O^T[d, heads] += V^T P^T
 // r is a running reference for each head, raised to the running maximum only
-// when a score exceeds it by more than 8 binades, so the usual tile needs one
-// vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
+// when a score exceeds it by more than 8 binades (fp16 weights: 4), so the usual
+// tile needs one vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
 // the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and the only
-// rounding that counts is that of the output.  fp16 weights are 2^7 at the
-// maximum: they lose nothing above 2^-32 of it.
+// rounding that counts is that of the output.  fp16 weights are 2^11 at
+// the maximum, up to 2^15 where it was let pass: a weight is off by at most 2^-25,
+// 2^-36 of the largest, besides its relative rounding.
 //
 // e4m3 caches: the codes become fp16 exactly, the keys' scales multiply S, and
 // the values' scales join the weights, w = 2^(z + log2 s - r'), with a running
@@ -55,7 +56,11 @@ namespace decode {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRowsPerWarp = kDecodeTile / kWarps;  // 16
 static_assert(kRowsPerWarp == 16, "one MMA tile of positions to a warp");
-constexpr float kRaise = 8.f;  // binades above the maximum at the last raise that are let pass
+// Binades above the maximum at the last raise that are let pass: of scores, and of fp16 weights,
+// which are 2^kShiftF16 at that maximum.  The fewer, the further down they reach, and the more
+// often they are raised: with 8, 4, 3 and 2 (e4m3, d = 64, 16 heads) 61.9, 62.5, 63.5 and 64.7 us;
+// d = 128, 8 heads 219.8, 220.0, 220.3, 220.8; fp16 caches alike.
+constexpr float kRaise = 8.f, kRaiseF16 = 4.f, kShiftF16 = 15.f - kRaiseF16;
 
 struct Join {  // what the join kernel needs of the item that starts, unfinished, in a block
   int entry, item;
@@ -145,17 +150,21 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 
 // Two weights rounded down to 16 bits, strictly below the weight itself, so that
 // the remainder is positive: with an infinite value both products have its sign
-// (a remainder of zero or of the other sign would make their sum a NaN).
+// (a remainder of zero or of the other sign would make their sum a NaN).  In fp16
+// that holds for weights from 2^-23 on, 2^-34 of the largest; below, an infinite
+// value gives NaN.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack_below(float a, float b) {
   constexpr float kLess = 1.f - 0x1p-10f;  // less than a step of either type away
-  a *= kLess;
-  b *= kLess;
   uint32_t r;
-  if constexpr (kBf16)
-    r = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  else
+  if constexpr (kBf16) {
+    r = __byte_perm(__float_as_uint(a * kLess), __float_as_uint(b * kLess), 0x7632);
+  } else {
+    constexpr float kLeast = 0x1p-24f;  // what fp16 can still hold
+    a = fmaxf(fminf(a * kLess, a - kLeast), 0.f);
+    b = fmaxf(fminf(b * kLess, b - kLeast), 0.f);
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  }
   return r;
 }
 
@@ -227,8 +236,6 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   using L = Layout<D, kNT, kE4M3>;
   constexpr bool kMmaBf16 = kBf16 && !kE4M3;
   constexpr bool kRemainder = !(kE4M3 && kBf16);
-  // fp16 weights fill the type's range: 2^7 at the maximum, 2^15 where it was let pass
-  constexpr float kShift = kMmaBf16 ? 0.f : 7.f;
   constexpr int kR = 8 * kNT;  // query heads of a block of rows
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sums[kWarps];
@@ -622,25 +629,27 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           }
         }
         // r <- the maximum so far, less the shift; what was summed shrinks by 2^(r_old - r)
-        auto raise_to = [&](float a, float b, float& r, float& limit) {
+        auto raise_to = [&](float a, float b, float& r, float& limit, bool f16) {
+          const float shift = f16 ? kShiftF16 : 0.f, pass = f16 ? kRaiseF16 : kRaise;
           float m = fmaxf(a, b);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
           const float old = limit == -INFINITY ? -INFINITY : r;
-          m = fmaxf(m - kShift, old);
+          m = fmaxf(m - shift, old);
           if (m == -INFINITY) return 1.f;
           r = m;
-          limit = m + (kShift + kRaise);
+          limit = m + (shift + pass);
           return ex2_approx(old - m);
         };
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            float f = raise_to(z[n][cc], z[n][2 + cc], ref[n][cc], top[n][cc]);
+            float f = raise_to(z[n][cc], z[n][2 + cc], ref[n][cc], top[n][cc],
+                               !kMmaBf16 && !kE4M3);
             sum[n][cc] *= f;
             if constexpr (kE4M3)
-              f = raise_to(zv[n][cc], zv[n][2 + cc], ref_v[n][cc], top_v[n][cc]);
+              f = raise_to(zv[n][cc], zv[n][2 + cc], ref_v[n][cc], top_v[n][cc], true);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               o[c][n][cc] *= f;

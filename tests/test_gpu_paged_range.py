@@ -150,3 +150,82 @@ def test_e4m3_queries_of_extreme_magnitude(cuda_device):
     # or nothing at all
     assert (lse[4:].cpu().double() - want[1][4:]).abs().max() <= 2e-4
     assert torch.isfinite(o[4:]).all()
+
+
+@pytest.mark.parametrize("kind,typ", [("fp16", "fp16"), ("bf16", "bf16"), ("e4m3", "fp16"),
+                                      ("e4m3", "bf16")])
+@pytest.mark.parametrize("lens", [[200, 17], [8192, 700]], ids=["direct", "split"])
+@pytest.mark.parametrize("gap", [14.0, 15.3, 16.1, 17.2, 18.5, 19.4, 20.3])
+def test_weights_far_below_the_largest(cuda_device, kind, typ, lens, gap):
+    """One key's score is `gap` above all others, which are equal (their weights round alike), and
+    its value is zero in all columns but one: the others alone make up the rest.
+
+    fp16 weights are off by at most 2^-25 where the largest is at least 2^11, of an e4m3 cache in
+    units of p_j 2^s_j with s_j the power that scales row j: 2^-36 max_j (p_j 2^s_j) of the sum of
+    the codes' magnitudes, v_j / 2^s_j, beside what check_attention allows."""
+    d, group, heads = 64, 4, 1
+    q, k, v, at = sink_inputs(lens, heads, group, d, typ, gap, seed=21)
+    sink = k[at].clone()
+    k.zero_()
+    k[at] = sink
+    v[at] = 0
+    v[at, :, 7] = 1.0
+    v = (v * (1.0 if kind == "bf16" else 64.0)).to(TYPES[typ])
+    cache, table = filled(lens, heads, 16, d, kind, k, v, seed=9)
+    o, lse = fat.attn_decode_paged(q.cuda(), cache.k, cache.v, table.cuda(),
+                                   torch.tensor(lens, dtype=torch.int32).cuda(),
+                                   **cache.scale_args)
+    kk, vv = cache.held()
+    scale = float(np.float32(d ** -0.5))
+    want = ref.decode(q.double(), kk, vv, table, lens, 16, scale)
+    if kind != "bf16":
+        power = torch.ones(vv.shape[:3], dtype=torch.float64) if kind == "fp16" \
+            else 2.0 ** (cache.scales[1].cpu().double() - 127)
+        for b, n in enumerate(lens):
+            x = ref.gather(kk, table[b], n, 16)[0]
+            s = ref.gather(power[..., None], table[b], n, 16)[0]
+            codes = (ref.gather(vv, table[b], n, 16)[0] / s).abs().sum(0)
+            for h in range(group):
+                p = torch.softmax((x @ q[b, h].double()) * scale, 0)
+                # (as part of the magnitudes, of which check_attention allows 2^-12)
+                want[2][b, h] += 2.0 ** 12 * 2.0 ** -36 * (p[:, None] * s).max() * codes
+    check_attention(o, lse, *want, kind=kind)
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens", [[300], [6000]], ids=["direct", "split"])
+def test_infinite_values_of_little_weight(cuda_device, typ, lens):
+    """An infinite value makes its column infinite, 20 nats (2^-29 of the largest weight) below the
+    largest score as well."""
+    d = 64
+    q, k, v, at = sink_inputs(lens, 1, 4, d, typ, 1.0, seed=31)
+    u = torch.sign(k[at[0], 0])
+    k = k * 0.02
+    k[at[0]] = u * (20.0 / math.sqrt(d))
+    low = [5, 110, 111, 250, lens[0] - 2]
+    for i, (j, gap) in enumerate(zip(low, (0.0, 4.0, 8.0, 12.0, 17.0))):
+        k[j] = u * (gap / math.sqrt(d))
+        v[j, 0, 2 * i] = math.inf
+        v[j, 0, 2 * i + 1] = -math.inf
+    cache, table = filled(lens, 1, 16, d, typ, k.to(TYPES[typ]), v.to(TYPES[typ]), seed=9)
+    o, _ = check(cache, table, lens, q)
+    assert torch.isinf(o[0, :, :10]).all() and torch.isfinite(o[0, :, 10:]).all()
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens", [[300, 40], [6000, 40]], ids=["direct", "split"])
+def test_infinite_keys(cuda_device, typ, lens):
+    """A score of +inf has no softmax: NaN, for the heads whose query is positive there; a score of
+    -inf has no weight.  The other sequence is as it was."""
+    d = 64
+    q, k, v, _ = sink_inputs(lens, 1, 4, d, typ, 2.0, seed=32)
+    q[0, :, 3] = torch.tensor([1.0, -1.0, 0.5, -0.25])
+    k[77, 0, 3] = math.inf
+    cache, table = filled(lens, 1, 16, d, typ, k.to(TYPES[typ]), v.to(TYPES[typ]), seed=9)
+    o, lse = fat.attn_decode_paged(q.cuda(), cache.k, cache.v, table.cuda(),
+                                   torch.tensor(lens, dtype=torch.int32).cuda())
+    want = ref.decode(q.double(), *cache.held(), table, lens, 16, 0.125)
+    assert torch.isnan(want[0][0, ::2]).all() and torch.isfinite(want[0][0, 1::2]).all()
+    assert torch.isnan(o[0, ::2]).all() and not torch.isfinite(lse[0, ::2]).any()
+    check_attention(o[0, 1::2], lse[0, 1::2], *(x[0, 1::2] for x in want), kind=typ)
+    check_attention(o[1], lse[1], *(x[1] for x in want), kind=typ)
