@@ -27,10 +27,8 @@
 // keep their precision relative to the largest w 2^8 (a row's largest code is
 // near 2^8, as written) whatever the scales are.  q is brought into fp16's range
 // by a power of two for each head, without loss: a query with elements more than
-// 32 binades apart takes its low parts by a second pass over the staged keys.
-// For a bf16 output the weights go without
-// the remainder: at most 2^-11 each, 2^-12 on average, against the output's own
-// 2^-9 (the MMAs and packing saved are 3 to 13 % of the time).
+// 32 binades apart takes its low parts, down to 2^-70 of the largest, by a second
+// pass over the staged keys.
 //
 // The warps' (r, r', l, O) are joined through shared memory at an item's end;
 // an item that other blocks share leaves a normalised O and its LSE in the
@@ -235,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     decode_kernel(const DecodeParams p) {
   using L = Layout<D, kNT, kE4M3>;
   constexpr bool kMmaBf16 = kBf16 && !kE4M3;
-  constexpr bool kRemainder = !(kE4M3 && kBf16);
   constexpr int kR = 8 * kNT;  // query heads of a block of rows
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sums[kWarps];
@@ -669,15 +666,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
         }
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          if constexpr (kRemainder) {
-            const uint32_t h = pack_below<kMmaBf16>(w[2 * rr], w[2 * rr + 1]);
-            const float2 back = unpack16<kMmaBf16>(h);
-            hi[n][rr] = transpose8(h);
-            lo[n][rr] =
-                transpose8(pack16<kMmaBf16>(w[2 * rr] - back.x, w[2 * rr + 1] - back.y));
-          } else {
-            hi[n][rr] = transpose8(pack16<kMmaBf16>(w[2 * rr], w[2 * rr + 1]));
-          }
+          // (e4m3 has no infinities: the nearest fp16, with a remainder of either sign)
+          const uint32_t h = kE4M3 ? pack16<false>(w[2 * rr], w[2 * rr + 1])
+                                   : pack_below<kMmaBf16>(w[2 * rr], w[2 * rr + 1]);
+          const float2 back = unpack16<kMmaBf16>(h);
+          hi[n][rr] = transpose8(h);
+          lo[n][rr] = transpose8(pack16<kMmaBf16>(w[2 * rr] - back.x, w[2 * rr + 1] - back.y));
         }
       }
       // O^T += V^T P^T
@@ -706,8 +700,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
 #pragma unroll
             for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, hi[n][0], hi[n][1]);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n)
-              if constexpr (kRemainder) mma<false>(o[2 * c + x][n], f, lo[n][0], lo[n][1]);
+            for (int n = 0; n < kNT; ++n) mma<false>(o[2 * c + x][n], f, lo[n][0], lo[n][1]);
           }
         }
       }

@@ -229,3 +229,30 @@ def test_infinite_keys(cuda_device, typ, lens):
     assert torch.isnan(o[0, ::2]).all() and not torch.isfinite(lse[0, ::2]).any()
     check_attention(o[0, 1::2], lse[0, 1::2], *(x[0, 1::2] for x in want), kind=typ)
     check_attention(o[1], lse[1], *(x[1] for x in want), kind=typ)
+
+
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 1), (128, 16), (64, 16)])
+def test_e4m3_weights_keep_more_bits_than_the_output(cuda_device, d, group):
+    """Two values that nearly cancel under weights near 2/3 and 1/3: a rounding of the weights to
+    11 bits would show in a bf16 output.  The scores' sums of magnitudes are below 1.5 (a key of
+    signs times 0.7 / sqrt(d)), so a weight and the total are each off by less than
+    128 * 2^-24 * 1.5 = 1.2e-5, together less than 2^-15, and the rest (2^-22 of an exponential,
+    2^-16 of a weight in two parts) below that again: 2^-14 of the sum of p_j |v_j|."""
+    heads, b = 2, 150
+    g = torch.Generator().manual_seed(d + group)
+    lens = [2] * b
+    u = torch.sign(torch.randn((heads, d), generator=g))
+    q = u[:, None] + 0.2 * torch.randn((b, heads, group, d), generator=g)
+    q = q.reshape(b, heads * group, d).to(torch.bfloat16)
+    k = torch.zeros((2 * b, heads, d))
+    k[::2] = u * (0.66 / math.sqrt(d))
+    v = torch.full((2 * b, heads, d), -1.0)
+    v[::2] = 0.5
+    cache, table = filled(lens, heads, 16, d, "e4m3", k.to(torch.bfloat16), v.to(torch.bfloat16),
+                          seed=2)
+    o, _ = fat.attn_decode_paged(q.cuda(), cache.k, cache.v, table.cuda(),
+                                 torch.tensor(lens, dtype=torch.int32).cuda(), **cache.scale_args)
+    want = ref.decode(q.double(), *cache.held(), table, lens, 16, float(np.float32(d ** -0.5)))
+    off = (o.cpu().double() - want[0]).abs()
+    assert want[0].abs().min() < 1e-3  # (where the output's own rounding is far below the rest)
+    assert (off <= 2.0 ** -8 * want[0].abs() + 2.0 ** -14 * want[2]).all()
