@@ -19,7 +19,8 @@ given, from that stream's memory: they need no wait for the current stream.
 (Inputs, and outputs that are given, are the caller's to order.)  A given workspace must not be shared by calls that overlap.  Calls can
 be captured in a graph (after a first call of their kind, which loads the
 kernels); replays use the lengths, pages and slots that the tensors hold then.
-Nothing here is differentiable.
+Nothing here is differentiable: a tensor that requires a gradient is refused
+unless gradients are off (``torch.no_grad()``, ``torch.inference_mode()``).
 """
 from __future__ import annotations
 
@@ -102,6 +103,13 @@ def _tensor(name, t, dtypes, dim, device=None):
     return t
 
 
+def _gradient():
+    """Some argument requires a gradient, which would be lost without a word."""
+    if torch.is_grad_enabled():
+        raise ValueError("no gradient flows through the paged operators: call them under "
+                         "torch.no_grad(), or detach what requires one")
+
+
 def _rows(name, t, pages, heads, writable):
     """Strides between pages, heads and tokens; those of a dimension of one entry do not matter (a
     page has 16 rows at least)."""
@@ -143,6 +151,8 @@ def _cache(k, v, k_scale, v_scale, writable=False):
             _wrong("v_cache", v, (dtype,), 4, device)
             raise ValueError("k_cache and v_cache must have the same shape")
         at, v_rows = v.data_ptr(), _rows("v_cache", v, pages, heads, writable)
+    if k.requires_grad or (at and v.requires_grad):
+        _gradient()
     ks = vs = 0
     if kind == _E4M3:
         ks = _scale("k_scale", k_scale, shape, device)
@@ -177,6 +187,8 @@ def _query(q, batch, heads, d, device):
             and q.dtype in _WIDE):
         _wrong("q", q, _WIDE, 3, device)
     b, h, c = q.shape
+    if q.requires_grad:
+        _gradient()
     if b != batch or c != d or h < 1 or h % heads:
         raise ValueError(f"q must be [{batch}, a multiple of {heads}, {d}], "
                          f"not {list(q.shape)}")
@@ -201,6 +213,8 @@ def _output(name, t, shape, dtype, device):
     _tensor(name, t, (dtype,), len(shape), device)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)}")
+    if t.requires_grad:
+        _gradient()
     return t
 
 
@@ -239,6 +253,8 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
     v_strides = _tokens("v", v, shape, (k.dtype,), device)
     if kind != _E4M3 and k.dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache takes {k_cache.dtype} tokens, not {k.dtype}")
+    if k.requires_grad or v.requires_grad:
+        _gradient()
     if not shape[0]:
         return
     if not slots.is_contiguous():
@@ -351,6 +367,8 @@ def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | Non
     _tensor("bounds", bounds, _WIDE if kind == _E4M3 else (k_cache.dtype,), 4, device)
     if bounds.shape != (pages, heads, 2, d) or not bounds.is_contiguous():
         raise ValueError("bounds must be contiguous [num_pages, heads, 2, d]")
+    if bounds.requires_grad:
+        _gradient()
     new_tokens = 0x7fffffff if new_tokens is None else int(new_tokens)
     if not 1 <= new_tokens <= 0x7fffffff:
         raise ValueError("new_tokens must be at least 1")
@@ -376,6 +394,8 @@ def kv_block_scores(q, bounds, page_table, seq_lens, page_size: int, *, out=None
     query = _query(q, batch, heads, d, device)
     if q.dtype is not bounds.dtype:
         raise ValueError("q and bounds must have the same type")
+    if bounds.requires_grad:
+        _gradient()
     stream = _given(stream, device)
     if out is None:
         out = _empty((batch, heads, width), torch.float32, device, stream)
