@@ -400,8 +400,11 @@ size_t fat_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int
  * of each sequence (new_tokens >= 1; all blocks if it is at least the
  * length), over their positions below the length; other blocks keep what
  * they have.  A NaN key makes its bound NaN; a value of an e4m3 cache that
- * `dtype` cannot hold is rounded to nearest.  A page in two sequences' lines
- * gets the bounds of one of them.  cache->v is not used.
+ * `dtype` cannot hold is rounded to nearest.  A page that stands in several
+ * sequences' lines (a shared prefix) must be filled to the same position in
+ * each of them whose newest positions touch it, as a page is copied before one
+ * of its sequences goes on in it; else its bounds are unspecified, a mixture of
+ * theirs.  cache->v is not used.
  */
 int fat_kv_block_bounds(const fat_kv_cache* cache, const fat_page_table* table, int new_tokens,
                         void* bounds, int dtype, cudaStream_t stream);

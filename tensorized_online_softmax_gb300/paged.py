@@ -360,7 +360,9 @@ def kv_block_bounds(k_cache, page_table, seq_lens, bounds, new_tokens: int | Non
     fp16 for an e4m3 cache), the elementwise minimum and maximum of each
     block's keys.  The blocks with any of the last ``new_tokens`` positions of
     a sequence are computed anew (all of them if None); the others keep what
-    they have.  Returns ``bounds``.
+    they have.  A page that several sequences share must be filled to the same
+    position in each of those (copy it before one of them goes on in it); else
+    its bounds are unspecified.  Returns ``bounds``.
     """
     cache, device, kind, (pages, heads, _, d) = _cache(k_cache, None, k_scale, None)
     table = _table(page_table, seq_lens, device)[0]
