@@ -78,6 +78,7 @@ def declare(lib) -> None:
 _WIDE = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
 _CACHE = {**_WIDE, torch.float8_e4m3fn: DTYPES["e4m3"]}
 _E4M3 = DTYPES["e4m3"]
+_MOST = 1 << 30  # of counts that the C interface takes (and ctypes would cut to 32 bits)
 _DIRECT = 512  # FAT_DECODE_DIRECT: positions of a table that need no workspace
 
 # The checks below run for every call of a serving loop, where a few microseconds count: each
@@ -257,6 +258,8 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
         _gradient()
     if not shape[0]:
         return
+    if shape[0] > 0x7fffffff:
+        raise ValueError("more than 2^31 - 1 tokens in one call")
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
     _call("fat_kv_write", device, cache, k.data_ptr(), v.data_ptr(), _WIDE[k.dtype], *k_strides,
@@ -277,8 +280,8 @@ def kv_cache_read(k_cache, v_cache, page_table, seq_lens, max_len: int, *, dtype
     if dtype not in _WIDE or (kind != _E4M3 and dtype != k_cache.dtype):
         raise ValueError(f"a {k_cache.dtype} cache is not read as {dtype}")
     shape = (batch, heads, int(max_len), d)
-    if shape[2] < 1:
-        raise ValueError("max_len must be at least 1")
+    if not 1 <= shape[2] <= _MOST:
+        raise ValueError("max_len must be 1 to 2^30")
     stream = _given(stream, device)
     if out is None:
         k, v = (_empty(shape, dtype, device, stream) for _ in range(2))
@@ -396,6 +399,8 @@ def kv_block_scores(q, bounds, page_table, seq_lens, page_size: int, *, out=None
     query = _query(q, batch, heads, d, device)
     if q.dtype is not bounds.dtype:
         raise ValueError("q and bounds must have the same type")
+    if not 1 <= page_size <= _MOST:
+        raise ValueError("page_size must be a power of two, 16 to 1024")
     if bounds.requires_grad:
         _gradient()
     stream = _given(stream, device)
@@ -427,9 +432,9 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
     args, device, (_, heads, _, d), batch, width, o, lse, stream = _decode_arguments(
         q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out, stream)
     num_blocks = int(num_blocks)
-    if num_blocks < 1 or first_blocks < 0 or last_blocks < 0 or \
+    if not 1 <= num_blocks <= _MOST or first_blocks < 0 or last_blocks < 0 or \
             first_blocks + last_blocks > num_blocks:
-        raise ValueError("num_blocks must be at least 1 and at least first_blocks + last_blocks")
+        raise ValueError("num_blocks must be 1 to 2^30 and at least first_blocks + last_blocks")
     _output("scores", scores, (batch, heads, width), torch.float32, device)
     shape = (batch, heads, num_blocks)
     if out is None:
