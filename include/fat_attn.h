@@ -381,6 +381,15 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
  * memory, 16-byte aligned, any contents; calls sharing it must not overlap on
  * the device.  It may be NULL if width * page_size <= FAT_DECODE_DIRECT: no
  * sequence is split then.
+ *
+ * The weights of the values of an fp16 cache reach down to 2^-36 of a head's
+ * largest, those of an e4m3 cache to 2^-36 of its largest product of weight and
+ * row scale (rows of zeros left aside, whatever their scale byte): what is
+ * below adds nothing, and each weight is off by no more than that besides its
+ * own rounding.  With scales as fat_kv_write sets them that is far below an
+ * output's rounding, unless a column is (nearly) zero in the rows that dominate.
+ * An infinite value of an fp16 cache gives NaN where its weight is below 2^-34
+ * of the largest.
  */
 #define FAT_DECODE_DIRECT 512
 int fat_attn_decode_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
@@ -414,7 +423,10 @@ int fat_kv_block_bounds(const fat_kv_cache* cache, const fat_page_table* table, 
  * [batch, kv_heads, width], is the largest over the query heads h of group g of
  *     sum_c max(q[b,h,c], 0) hi_c + min(q[b,h,c], 0) lo_c,
  * an upper bound of q . k over the block's keys, with lo and hi the bounds of
- * the page at pages[b, i]; -inf behind the sequence's last block.  q as in
+ * the page at pages[b, i]; -inf behind the sequence's last block.  (Up to the
+ * rounding of its fp32 sum; and where fp16 bounds of an e4m3 cache were rounded,
+ * beyond fp16's range or among its subnormals, a key may lie outside them.  An
+ * infinite bound times a zero of q+ or q- is NaN, which counts as the highest.)  q as in
  * fat_attn_decode_paged, of the bounds' type.
  */
 int fat_kv_block_scores(const void* q, int dtype, long long q_batch_stride,

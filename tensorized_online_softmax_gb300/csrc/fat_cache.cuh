@@ -134,8 +134,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
         : (B ? __VA_ARGS__(64, false, true) : __VA_ARGS__(64, false, false));    \
   } while (0)
 
-// ---- launchers (fat_cache_kernels.cu, fat_decode.cu, fat_block_select.cu):
-// 0, or -4 for a CUDA error ----
+// ---- launchers (fat_cache_kernels.cu, fat_decode_d128.cu, fat_decode_d64.cu,
+// fat_block_select.cu): 0, or -4 for a CUDA error ----
 struct WriteParams {
   CacheView c;
   const uint8_t* k;
@@ -184,7 +184,6 @@ struct DecodeParams {
   CacheView c;
   TableView t;
   int per_head;
-  int batch;
   const uint8_t* q;
   uint32_t q_batch, q_head;  // bytes
   int group;                  // query heads per cached head

@@ -171,7 +171,6 @@ static int decode_common(const fat_kv_cache* cache, const fat_page_table* table,
   if (cache->dtype != FAT_DTYPE_E4M3 && cache->dtype != dtype) return FAT_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || !o || !lse) return FAT_ERR_INVALID_ARG;
   if (!aligned(o, 16) || !aligned(lse, 4)) return FAT_ERR_ALIGNMENT;
-  p->batch = table->batch;
   p->least_tiles = 2;
   p->q = static_cast<const uint8_t*>(q);
   p->group = q_heads / cache->heads;

@@ -5,7 +5,7 @@
 //
 // Work: fat_decode_plan.h.  Each of a block's four warps takes 16 positions of
 // every 64-position tile through a ring of its own in shared memory, filled by
-// 16-byte asynchronous copies several tiles ahead (a ring per warp needs no
+// 16-byte asynchronous copies one to three tiles ahead, by layout (a ring per warp needs no
 // barrier between warps; 16 positions never straddle two pages).  Rows behind
 // the length are filled with zeros, not read.
 //
@@ -15,9 +15,9 @@
 //     p = 2^(z - r),  l += p,   O^T[d, heads] += V^T P^T
 // r is a running reference for each head, raised to the running maximum only
 // when a score exceeds it by more than 8 binades (fp16 weights: 4), so the usual
-// tile needs one vote and no reduction over lanes.  P enters the MMA as a 16-bit value plus
-// the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and the only
-// rounding that counts is that of the output.  fp16 weights are 2^11 at
+// tile needs one vote and no reduction over lanes.  P enters the MMA as a 16-bit
+// value plus the 16-bit remainder (two MMAs): its rounding stays below 2^-16 and
+// the only rounding that counts is that of the output.  fp16 weights are 2^11 at
 // the maximum, up to 2^15 where it was let pass: a weight is off by at most 2^-25,
 // 2^-36 of the largest, besides its relative rounding.
 //
