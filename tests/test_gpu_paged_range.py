@@ -256,3 +256,59 @@ def test_e4m3_weights_keep_more_bits_than_the_output(cuda_device, d, group):
     off = (o.cpu().double() - want[0]).abs()
     assert want[0].abs().min() < 1e-3  # (where the output's own rounding is far below the rest)
     assert (off <= 2.0 ** -8 * want[0].abs() + 2.0 ** -14 * want[2]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_infinite_queries(cuda_device, kind):
+    """Scores of -inf alone leave nothing to weigh, as for an empty sequence, whatever finite
+    elements stand beside the infinite one; +inf and NaN have no softmax."""
+    g = torch.Generator().manual_seed(4)
+    k = torch.randn((50, 1, 64), generator=g)
+    k[:, 0, 0], k[:, 0, 1] = -1.0, 1.0
+    q = torch.randn((1, 4, 64), generator=g)
+    q[0, 0, :2] = torch.tensor([math.inf, 3e38])
+    q[0, 1, 0] = -math.inf
+    q[0, 2, 5] = math.nan
+    v = torch.randn((50, 1, 64), generator=g)
+    cache, table = filled([50], 1, 16, 64, kind, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    q = q.to(torch.bfloat16)
+    o, lse = fat.attn_decode_paged(q.cuda(), cache.k, cache.v, table.cuda(),
+                                   torch.tensor([50], dtype=torch.int32).cuda(),
+                                   **cache.scale_args)
+    assert (o[0, 0] == 0).all() and lse[0, 0] == -math.inf
+    assert torch.isnan(o[0, 1:3]).all() and not torch.isfinite(lse[0, 1:3]).any()
+    want = ref.decode(q.double(), *cache.held(), table, [50], 16, 0.125)
+    check_attention(o[0, 3], lse[0, 3], *(x[0, 3] for x in want), kind=kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_short_sequences_in_a_wide_table(cuda_device, kind):
+    """A table as wide as a model's longest context, as a captured graph needs it: lengths from none
+    to a few pages, then one that grew; entries behind a sequence are never used."""
+    ps, H, G, d, width = 16, 2, 4, 128, 131072 // 16
+    for lens in ([1, 0, 15, 16, 17, 200, 511], [513, 3, 0, 5000]):
+        pages = pages_for(lens, ps)
+        cache = Cache(pages, H, ps, d, kind, seed=len(lens))
+        table = make_table(lens, ps, pages, seed=1, width=width)
+        g = torch.Generator().manual_seed(len(lens))
+        q = torch.randn((len(lens), H * G, d), generator=g).to(torch.bfloat16)
+        check(cache, table, lens, q)
+        args = (table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+        bounds = torch.zeros((pages, H, 2, d), dtype=torch.bfloat16, device="cuda")
+        fat.kv_block_bounds(cache.k, *args, bounds, k_scale=cache.scales[0])
+        scores = fat.kv_block_scores(q.cuda(), bounds, *args, ps).cpu()
+        narrow = -(-max(lens) // ps)
+        want, size = ref.scores_of(q.double(), bounds.cpu().double(), table[:, :narrow], lens, ps)
+        assert (scores[..., narrow:] == -math.inf).all()
+        got = scores[..., :narrow].double()
+        fine = torch.isfinite(want)
+        assert torch.equal(torch.isfinite(got), fine)
+        # 2 d products in fp32
+        assert ((got - want).abs()[fine] <= 2 * d * 2.0 ** -24 * size[fine]).all()
+        o, lse, blocks = fat.attn_decode_sparse(q.cuda(), cache.k, cache.v, *args, scores.cuda(),
+                                                9, **cache.scale_args)
+        *att, chosen = ref.sparse(q.double(), *cache.held(), table, lens, ps, scores.double(), 9,
+                                  float(np.float32(d ** -0.5)))
+        assert torch.equal(blocks.cpu(), chosen)
+        check_attention(o, lse, *att, kind=kind)
+        assert fat.check_device_error() == fat.FAT_OK

@@ -96,3 +96,33 @@ def test_a_workspace_is_free_for_its_own_stream_only(cuda_device):
     overwrite(want + want)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("name", ["read", "decode", "scores", "sparse"])
+def test_a_side_stream_inside_a_captured_graph(cuda_device, name):
+    """The given stream forks from the capturing one and joins it again."""
+    call = calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        first = call(side)
+        second = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in first + second:
+            t.view(torch.uint8).fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for got in (first, second) for a, b in zip(got, want))
+
+
+def test_the_default_stream_by_its_number(cuda_device):
+    call = calls()["decode"]
+    want = call(None)
+    got = call(0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
