@@ -170,10 +170,10 @@ def _stream_handle(stream, device=None):
 
 def _given(stream, device):
     """A given stream as a torch stream; None stands for the current one."""
-    import torch
-
     if stream is None or hasattr(stream, "cuda_stream"):
         return stream
+    import torch
+
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 

@@ -36,11 +36,14 @@
 // on timing.
 //
 // Measured on a GB300, calls back to back on the device: 32 sequences of 1000 to
-// 8192 positions, 8 cached heads of 4 query heads, d = 128, bf16 (599 MB): 94.8 us,
-// 0.93 of the measured copy rate (the stream itself 0.985; the rest is the plan,
-// 2.5 us to the first rows, and 4 us of end and join); one sequence of 131072
-// (537 MB): 85.2 us; 64 sequences of 4096 to 16384, groups of 8, e4m3 (1417 MB):
-// 220 to 223 us, 0.94; 13 of 0 to 4097, 20 heads, d = 64, fp16 (148 MB): 30 us, 0.73.
+// 8192 positions, 8 cached heads of 4 query heads, d = 128, bf16 (599 MB): 94 to
+// 95.4 us, 0.93 of the measured copy rate (the stream itself 0.985; the rest is the
+// plan, 2.5 us to the first rows, and 4 us of end and join); one sequence of 131072
+// (537 MB): 85.3 us; 64 sequences of 4096 to 16384, groups of 8, e4m3 (1417 MB):
+// 223 us, 0.94; 13 of 0 to 4097, 20 heads, d = 64, fp16 (148 MB): 30 us, 0.73.
+// The 32 sequences with groups of 16: bf16 101 us, e4m3 91 (304 MB, 45 at the copy
+// rate: 8 warps an SM do not hide the instructions' latency); of 64: 335, as every
+// 16 heads are a pass of their own.
 #pragma once
 
 #include "fat_cache.cuh"
