@@ -169,12 +169,17 @@ def _stream_handle(stream, device=None):
 
 
 def _given(stream, device):
-    """A given stream as a torch stream; None stands for the current one."""
-    if stream is None or hasattr(stream, "cuda_stream"):
-        return stream
+    """A given stream (torch's, a handle, or what has one as `cuda_stream`) as a torch stream;
+    None stands for the current one."""
+    if stream is None:
+        return None
     import torch
 
-    return torch.cuda.ExternalStream(int(stream), device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    # (1, the legacy default stream, is what 0 stands for here)
+    return torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
 
 
 def _empty(shape, dtype, device, stream):

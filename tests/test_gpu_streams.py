@@ -65,3 +65,23 @@ def test_memory_of_a_call_on_another_stream(cuda_device, name):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert fat.check_device_error() == fat.FAT_OK
+
+
+class Wrapped:
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("name", ["fwd", "splitkv", "bwd", "host"])
+def test_streams_given_in_other_ways(cuda_device, name):
+    """A handle, an object that has one, the default stream by its numbers, and the per-thread
+    default stream."""
+    call = calls()[name]
+    out = call(None)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    side = torch.cuda.Stream()
+    for stream in (side.cuda_stream, Wrapped(side), 0, 1, 2, torch.cuda.ExternalStream(side.cuda_stream)):
+        got = call(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
