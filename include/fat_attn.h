@@ -455,6 +455,113 @@ int fat_attn_decode_sparse(const fat_kv_cache* cache, const fat_page_table* tabl
 size_t fat_attn_decode_sparse_workspace_bytes(int batch, int q_heads, int kv_heads, int d,
                                               int num_blocks);
 
+/*
+ * Attention of one new query token per sequence over a sliding window: over the
+ * last `window` positions of its sequence (the newest one, its own, among them)
+ * and the first `sinks` ones (j < sinks or j >= seq_lens[b] - window); each
+ * position counts once.  window >= 1, sinks >= 0.  The pages between them are
+ * not read, nor used as addresses: they may have been given back.  Everything
+ * else as in fat_attn_decode_paged, its workspace too; it may be NULL where no
+ * sequence is split: where
+ *     min(ceil(width * page_size / 64), ceil(sinks / 64) + ceil(window / 64) + 1) * 64
+ * is at most FAT_DECODE_DIRECT.
+ */
+int fat_attn_decode_window(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                           int dtype, long long q_batch_stride, long long q_head_stride,
+                           int q_heads, int window, int sinks, float scale, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A step of drafted tokens over the paged cache
+ * ------------------------------------------------------------------------
+ * Several tokens per sequence are drafted, stored (fat_kv_append), judged by
+ * one pass of attention (fat_attn_tree_paged), and those of the accepted path
+ * are kept (fat_kv_keep).
+ */
+
+/*
+ * The rotation of rows by their tokens' positions.  The first `dim` elements of
+ * a row (a multiple of 16, at most d) form dim / 2 pairs: (i, i + dim / 2), or
+ * with `interleaved` (2 i, 2 i + 1).  Pair i at position p becomes
+ *     (x_a c - x_b s, x_b c + x_a s),  c = cos_sin[p, i],  s = cos_sin[p, dim / 2 + i],
+ * each product and sum rounded in fp32.  With one axis p is
+ * positions[token * token_stride]; with up to four, sections[a] adjacent pairs
+ * belong to axis a (their sum is dim / 2) and take
+ * positions[a * axis_stride + token * token_stride].
+ */
+#define FAT_ROTATION_AXES 4
+typedef struct fat_rotation {
+  const float* cos_sin; /* [rows, row_stride], 16-byte aligned, row_stride a multiple of 4 */
+  long long rows, row_stride;
+  const long long* positions;
+  long long axis_stride, token_stride; /* in entries, not negative */
+  int dim, axes;
+  int sections[FAT_ROTATION_AXES]; /* ignored for one axis */
+  int interleaved;
+} fat_rotation;
+
+/*
+ * Store new tokens as fat_kv_write does, the keys rotated; and rotate their
+ * queries: q [tokens, q_heads, d] of `dtype`, strides in elements, rows 16-byte
+ * aligned; q_out contiguous [tokens, q_heads, d] of the same type, 16-byte
+ * aligned (q itself is allowed, if it is contiguous).  q_heads = 0: keys and
+ * values only.  A rotated key is rounded once, to the cache's type (for e4m3
+ * straight from fp32, by the row scale of the rotated row).  slots[t] < 0: the
+ * token is not stored, its queries are rotated all the same.  A position outside
+ * [0, rows) sets FAT_ERR_INDEX; nothing is stored or given out of that token.
+ * tokens * (q_heads + 2 heads) is below 2^31 - 2^16.
+ */
+int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const void* q,
+                  long long q_token_stride, long long q_head_stride, int q_heads, const void* k,
+                  const void* v, int dtype, long long k_token_stride, long long k_head_stride,
+                  long long v_token_stride, long long v_head_stride, const long long* slots,
+                  int tokens, void* q_out, cudaStream_t stream);
+
+/*
+ * Attention of drafted tokens: the last draft_lens[b] (NULL: `tokens`) of the
+ * seq_lens[b] positions of sequence b are drafted tokens, those ahead of them its
+ * context.  Drafted token t sees the context and the drafted tokens j whose bit is
+ * set in tree[b * tree_stride + t] (its ancestors and itself, in a tree; the lower
+ * triangle in a chain; bits from draft_lens[b] on are ignored):
+ *     z_j = scale * q[b,t,h] . K_j,  o = sum_j softmax_j(z) V_j,  lse = ln sum_j exp(z_j)
+ * q: [batch, tokens, q_heads, d] of `dtype` (bf16 or fp16, the cache's own type
+ * unless it is e4m3), strides in elements, rows 16-byte aligned; o: contiguous
+ * [batch, tokens, q_heads, d] of the same type, rounded once; lse: fp32 [batch,
+ * tokens, q_heads].  A row that sees nothing, and the rows t >= draft_lens[b], give
+ * o = 0 and lse = -inf.  What a row does not see has no part in it, NaN and
+ * infinities included.
+ * 1 <= tokens <= FAT_TREE_TOKENS; tree_stride may be 0 (one tree for all).
+ * window > 0 (at least `tokens`): token t is at position P = context + (number of
+ * bits set in its mask) - 1 and sees of the context the positions j < sinks and
+ * j > P - window only; pages that no row sees are not read.  0: no window.
+ * seq_lens[b] below draft_lens[b] sets FAT_ERR_INDEX.
+ * workspace: at least fat_attn_tree_workspace_bytes(...) bytes, 16-byte aligned, any
+ * contents; calls sharing it must not overlap on the device.
+ */
+#define FAT_TREE_TOKENS 64
+int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                        int dtype, long long q_batch_stride, long long q_token_stride,
+                        long long q_head_stride, int q_heads, int tokens, const long long* tree,
+                        long long tree_stride, const int* draft_lens, int window, int sinks,
+                        float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Workspace size for fat_attn_tree_paged (0 for invalid arguments). */
+size_t fat_attn_tree_workspace_bytes(int batch, int tokens, int q_heads, int kv_heads, int d);
+
+/*
+ * Keep the accepted drafted tokens: for i < counts[b] the row at position
+ * seq_lens[b] + path[b * path_stride + i] moves to seq_lens[b] + i, in every head, K
+ * and V, scale bytes too.  Here seq_lens[b] counts the positions ahead of the drafted
+ * tokens.  A line of the path (0 <= counts[b] <= width entries) rises from entry to
+ * entry, as the path from a tree's root does; else what the rows hold afterwards is
+ * unspecified.  An entry below 0, or one that leads outside the table, sets
+ * FAT_ERR_INDEX and moves nothing.  Pages that are written to must not be shared by
+ * sequences.
+ */
+int fat_kv_keep(const fat_kv_cache* cache, const fat_page_table* table, const int* path,
+                long long path_stride, int width, const int* counts, cudaStream_t stream);
+
 /* Human-readable name of a fat_status value (static string). */
 const char* fat_status_string(int status);
 

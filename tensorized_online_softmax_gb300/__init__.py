@@ -12,8 +12,10 @@ summary, section A3 / Fig. 2) with its tensorized online softmax (section A2,
 Algorithm 1); ``variant="vec"`` is the vector-softmax ablation arm.
 
 :mod:`.paged` binds the serving operators: a paged key-value cache (bf16, fp16
-or e4m3), its writing and reading, and single-token attention over it, whole or
-over the best-scored blocks.
+or e4m3), its writing and reading, and single-token attention over it, whole,
+over the best-scored blocks or over a sliding window.  :mod:`.drafted` binds a
+step of drafted tokens over that cache: storing them with their rotation, the
+attention of a tree of them, and keeping the accepted ones.
 """
 from __future__ import annotations
 
@@ -28,6 +30,8 @@ __all__ = [
     "attn_bwd", "attn_fwd_host",
     "kv_cache_write", "kv_cache_read", "attn_decode_paged", "kv_block_bounds",
     "kv_block_scores", "attn_decode_sparse", "attn_decode_workspace_bytes",
+    "attn_decode_window", "kv_cache_append", "attn_tree_paged", "attn_tree_workspace_bytes",
+    "tree_mask", "kv_cache_keep",
     "check_device_error", "status_string", "ABI_SYMBOLS", "FAT_OK",
     "FAT_ERR_INVALID_ARG", "FAT_ERR_UNSUPPORTED", "FAT_ERR_ALIGNMENT", "FAT_ERR_LAUNCH",
     "FAT_ERR_DEVICE_TIMEOUT", "FAT_ERR_ARCH", "FAT_ERR_INDEX",
@@ -60,7 +64,8 @@ ABI_SYMBOLS = (
     "fat_attn_fwd_host", "fat_attn_fwd_host_workspace_bytes",
     "fat_kv_write", "fat_kv_read", "fat_attn_decode_paged", "fat_attn_decode_workspace_bytes",
     "fat_kv_block_bounds", "fat_kv_block_scores", "fat_attn_decode_sparse",
-    "fat_attn_decode_sparse_workspace_bytes",
+    "fat_attn_decode_sparse_workspace_bytes", "fat_attn_decode_window",
+    "fat_kv_append", "fat_attn_tree_paged", "fat_attn_tree_workspace_bytes", "fat_kv_keep",
     "fat_status_string", "fat_check_device_error",
 )
 
@@ -149,6 +154,7 @@ def load_library(build_if_missing: bool = True):
         lib.fat_check_device_error.argtypes = [P]
         lib.fat_check_device_error.restype = I
         paged.declare(lib)
+        drafted.declare(lib)
         _lib = lib
         return lib
 
@@ -432,8 +438,11 @@ def raw_call(name: str, *args):
     return getattr(lib, name)(*args)
 
 
-from . import paged  # noqa: E402  (uses the names above)
+from . import drafted, paged  # noqa: E402  (use the names above)
+from .drafted import (  # noqa: E402
+    attn_tree_paged, attn_tree_workspace_bytes, kv_cache_append, kv_cache_keep, tree_mask,
+)
 from .paged import (  # noqa: E402
-    attn_decode_paged, attn_decode_sparse, attn_decode_workspace_bytes, kv_block_bounds,
-    kv_block_scores, kv_cache_read, kv_cache_write,
+    attn_decode_paged, attn_decode_sparse, attn_decode_window, attn_decode_workspace_bytes,
+    kv_block_bounds, kv_block_scores, kv_cache_read, kv_cache_write,
 )

@@ -148,6 +148,40 @@ struct WriteParams {
 int launch_kv_write(const WriteParams& p, int d, bool e4m3, bool bf16, int sms,
                     cudaStream_t stream);
 
+// (fat_append_kernels.cu)
+struct AppendParams {
+  CacheView c;
+  const uint8_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  uint8_t* q_out;  // [tokens, q_heads, d]
+  uint32_t q_token, q_head, k_token, k_head, v_token, v_head;  // bytes
+  int q_heads;
+  const float* cos_sin;  // [rows, row_stride]: `pairs` cosines, then as many sines
+  long long rows, row_stride;
+  const long long* positions;
+  long long axis_stride, token_stride;  // entries
+  int pairs, axes;
+  int ends[3];  // where the pairs of the first three axes end
+  const long long* slots;
+  int tokens;
+  unsigned int* error_word;
+};
+int launch_kv_append(const AppendParams& p, int d, bool e4m3, bool bf16, bool interleaved, int sms,
+                     cudaStream_t stream);
+
+struct KeepParams {
+  CacheView c;
+  TableView t;  // seq_lens: the positions ahead of the drafted tokens
+  const int* path;
+  long long path_stride;
+  int width;  // of a line of the path
+  const int* counts;
+  int chunks;  // 16-byte chunks of a row
+  int scales;  // 1: there are scale bytes
+};
+int launch_kv_keep(const KeepParams& p, cudaStream_t stream);
+
 struct ReadParams {
   CacheView c;
   TableView t;
@@ -192,6 +226,7 @@ struct DecodeParams {
   float* lse;
   void* workspace;
   int direct;                 // each block has one item (set by the launch)
+  int window, sinks;          // window > 0: only the last and the first so many positions
   int least_tiles;            // tiles that a thread block takes at least
 };
 // what launch_decode needs, whatever the batch

@@ -225,13 +225,52 @@ __device__ __forceinline__ Item item_of(const DecodeParams& p, const DecodePlace
   return r;
 }
 
-__device__ __forceinline__ int enter(const DecodeParams& p, DecodePlace& at) {
-  const int len = table_length(p.t, p.c.page_shift, at.entry);
-  at.tiles = decode_tiles(len);
-  return len;
+// Tiles of an item of a sequence of `len` positions.
+template <bool kWindow>
+__device__ __forceinline__ int tiles_of(const DecodeParams& p, int len) {
+  if constexpr (kWindow)
+    return decode_span(len, p.window, p.sinks, kDecodeTile).tiles;
+  else
+    return decode_tiles(len);
 }
 
-template <int D, int kNT, bool kE4M3, bool kBf16>
+// What of a sequence is seen; without a window only the length counts.
+template <bool kWindow>
+struct Seen {
+  int len;
+  DecodeSpan span;
+  // the first position of the tile walked i-th
+  __device__ __forceinline__ int row(int i) const {
+    return (kWindow ? decode_span_tile(span, i) : i) * kDecodeTile;
+  }
+  __device__ __forceinline__ bool sees(int at) const {
+    return at < len && (!kWindow || decode_span_sees(span, at));
+  }
+  // any, or all, of a warp's rows from `at`
+  __device__ __forceinline__ bool some(int at) const {
+    return at < len && (!kWindow || at < span.sink || at + kRowsPerWarp > span.lo);
+  }
+  __device__ __forceinline__ bool all(int at) const {
+    return at + kRowsPerWarp <= len &&
+           (!kWindow || at + kRowsPerWarp <= span.sink || at >= span.lo);
+  }
+};
+
+template <bool kWindow>
+__device__ __forceinline__ void enter(const DecodeParams& p, DecodePlace& at, Seen<kWindow>& s) {
+  s.len = table_length(p.t, p.c.page_shift, at.entry);
+  if constexpr (kWindow) {
+    s.span = decode_span(s.len, p.window, p.sinks, kDecodeTile);
+    at.tiles = s.span.tiles;
+  } else {
+    at.tiles = decode_tiles(s.len);
+  }
+}
+
+// kWindow: only the last positions of a sequence and a few first ones are seen
+// (decode_span); the tiles between them are not walked, and rows of a tile that are
+// not seen are zeros in shared memory, like those behind the length.
+template <int D, int kNT, bool kE4M3, bool kBf16, bool kWindow>
 __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     decode_kernel(const DecodeParams p) {
   using L = Layout<D, kNT, kE4M3>;
@@ -262,14 +301,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
       start_s.tile = 0;
     }
     begin = 0;
-    share = total = decode_tiles(table_length(p.t, p.c.page_shift, e));
+    share = total = tiles_of<kWindow>(p, table_length(p.t, p.c.page_shift, e));
     __syncthreads();
   } else {
     const int entries = p.t.batch;
     const int each = (entries + kThreads - 1) / kThreads;
     const int lo = threadIdx.x * each, hi = min(entries, lo + each);
     long long mine = 0;
-    for (int e = lo; e < hi; ++e) mine += decode_tiles(table_length(p.t, p.c.page_shift, e));
+    for (int e = lo; e < hi; ++e)
+      mine += tiles_of<kWindow>(p, table_length(p.t, p.c.page_shift, e));
     const long long upto = block_scan(mine, warp_sums, total);
     total *= copies;
     // (a 64-bit division is a few hundred cycles)
@@ -280,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     long long before = (upto - mine) * copies;
     if (begin >= before && begin < upto * copies) {
       for (int e = lo; e < hi; ++e) {
-        const int tiles = decode_tiles(table_length(p.t, p.c.page_shift, e));
+        const int tiles = tiles_of<kWindow>(p, table_length(p.t, p.c.page_shift, e));
         const long long n = static_cast<long long>(tiles) * copies;
         if (begin < before + n) {
           start_s = decode_place(e, begin - before, tiles);
@@ -300,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   // ---- the copies, ahead of the arithmetic ----
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
   DecodePlace load = start_s;
-  int load_len = enter(p, load);
+  Seen<kWindow> load_seen;
+  enter(p, load, load_seen);
   const uint8_t *load_k, *load_v;  // the item's head in page 0
   const int* load_pages;           // the entry's line of the table
   int load_head;
@@ -317,20 +358,27 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
   int window = 0, window_page = 0;
   auto load_window = [&]() {
     window = load.tile;
-    const long long row = static_cast<long long>(load.tile + lane) * kDecodeTile + warp_row;
-    window_page = row < load_len ? load_pages[row >> p.c.page_shift] : 0;
+    if constexpr (kWindow) {
+      const int row = load_seen.row(load.tile + lane) + warp_row;
+      window_page = load_seen.some(row) ? load_pages[row >> p.c.page_shift] : 0;
+    } else {
+      const long long row = static_cast<long long>(load.tile + lane) * kDecodeTile + warp_row;
+      window_page = row < load_seen.len ? load_pages[row >> p.c.page_shift] : 0;
+    }
   };
   load_window();
   int loaded = 0;
   uint32_t stage_in = ring;  // of the next copy
   const int r0 = lane / L::kChunks, c0 = lane % L::kChunks;  // the lane's first chunk
   auto issue = [&]() {
-    const int row = load.tile * kDecodeTile + warp_row;
-    if (row < load_len) {
+    const int row = load_seen.row(load.tile) + warp_row;
+    if (load_seen.some(row)) {
       const uint32_t stage = stage_in;
       const int place = row & (p.c.page_size - 1);
       int page = __shfl_sync(0xffffffffu, window_page, load.tile - window);
-      int valid = min(kRowsPerWarp, load_len - row);
+      // rows that are there; with a window, whether all of them are seen
+      int valid = kWindow ? (load_seen.all(row) ? kRowsPerWarp : 1)
+                          : min(kRowsPerWarp, load_seen.len - row);
       if (static_cast<uint32_t>(page) >= p.c.num_pages) {
         atomicOr(p.t.error_word, kErrIndex);
         page = valid = 0;  // zeros in place of rows, and no address made of the page
@@ -365,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
         for (int i = 0; i < kPer; ++i) {
           const int r = r0 + i * kStep;
           const uint32_t to = stage + chunk_at<L::kChunks>(r, c0);
-          const uint32_t bytes = r < valid ? 16u : 0u;
-          const int from = r < valid ? r : 0;
+          const bool in = kWindow ? valid && load_seen.sees(row + r) : r < valid;
+          const uint32_t bytes = in ? 16u : 0u;
+          const int from = in ? r : 0;
           copy16(to, k + wide(from, p.c.k_token) + c0 * 16, bytes);
           copy16(to + L::kStage / 2, v + wide(from, p.c.v_token) + c0 * 16, bytes);
         }
@@ -385,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     if (++loaded < count) {
       const bool entry = decode_advance(load, copies);
       if (load.tile == 0) {
-        if (entry) load_len = enter(p, load);
+        if (entry) enter(p, load, load_seen);
         load_item();
         load_window();
       } else if (load.tile == window + 32) {
@@ -401,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
 
   // ---- the arithmetic ----
   DecodePlace cur = start_s;
-  int cur_len = enter(p, cur);
+  Seen<kWindow> cur_seen;
+  enter(p, cur, cur_seen);
   long long first_tile = begin - cur.tile;  // of the current item
   uint32_t stage_out = ring;
   uint32_t qf[D / 16][kNT][2];
@@ -487,10 +537,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
     }
     copy_wait<kLate ? L::kStages - 2 : L::kStages - 1>();
     __syncwarp();
-    const int row = cur.tile * kDecodeTile + warp_row;
+    const int row = cur_seen.row(cur.tile) + warp_row;
     const uint32_t used = stage_out - ring;  // the same in every warp
     bool issued = !kLate;
-    if (row < cur_len) {
+    if (cur_seen.some(row)) {
       const uint32_t stage = stage_out;
       const int mat = lane / 8, mr = lane % 8;
       // S = K Q^T
@@ -587,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
           z[n][j] = s * (kE4M3 ? ks[rr] * factor[n][cc] : factor[n][cc]);
           zv[n][j] = z[n][j] + vs[rr];
         }
-      if (row + kRowsPerWarp > cur_len) {
+      if (!cur_seen.all(row)) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (row + g + 8 * (j >> 1) >= cur_len) z[n][j] = zv[n][j] = -INFINITY;
+            if (!cur_seen.sees(row + g + 8 * (j >> 1))) z[n][j] = zv[n][j] = -INFINITY;
       }
       bool raise = false;
 #pragma unroll
@@ -828,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kNT, kE4M3>::kBlocks)
       fresh = true;
       first_tile = begin + i + 1;
     }
-    if (i + 1 < count && decode_advance(cur, copies)) cur_len = enter(p, cur);
+    if (i + 1 < count && decode_advance(cur, copies)) enter(p, cur, cur_seen);
   }
 }
 
@@ -959,10 +1009,10 @@ bool launch_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-template <int D, int kNT, bool kE4M3, bool kBf16>
-int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
+template <int D, int kNT, bool kE4M3, bool kBf16, bool kWindow>
+int launch_one(const DecodeParams& p, int dev, cudaStream_t stream) {
   using L = Layout<D, kNT, kE4M3>;
-  auto kernel = decode_kernel<D, kNT, kE4M3, kBf16>;
+  auto kernel = decode_kernel<D, kNT, kE4M3, kBf16, kWindow>;
   static std::once_flag once[kMaxDevices];
   static int sms[kMaxDevices];
   std::call_once(once[dev], [&] {
@@ -975,7 +1025,7 @@ int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
   if (sms[dev] < 1) return -4;
   const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
   const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
-  const long long tiles = (positions + kDecodeTile - 1) / kDecodeTile;
+  const long long tiles = decode_span_most(positions, p.window, p.sinks, kDecodeTile);
   if (tiles <= kDirectTiles) {  // (the items are at most the query heads: below 2^31)
     DecodeParams one = p;
     one.direct = 1;
@@ -998,6 +1048,12 @@ int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
                      8 * kNT))
     return -4;
   return 0;
+}
+
+template <int D, int kNT, bool kE4M3, bool kBf16>
+int launch(const DecodeParams& p, int dev, cudaStream_t stream) {
+  return p.window > 0 ? launch_one<D, kNT, kE4M3, kBf16, true>(p, dev, stream)
+                      : launch_one<D, kNT, kE4M3, kBf16, false>(p, dev, stream);
 }
 
 template <int D>

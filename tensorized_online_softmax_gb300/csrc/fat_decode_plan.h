@@ -27,6 +27,40 @@ FAT_HD int decode_tiles(int len) {
   return len > kDecodeTile ? (len - 1) / kDecodeTile + 1 : 1;
 }
 
+// The positions that are seen of a sequence of `len`: the last `window` of them and
+// the first `sinks`; window 0 stands for all.  They are walked tile by tile, the
+// tiles between the two left out.
+struct DecodeSpan {
+  int lo, sink;     // seen: [0, sink) and [lo, len)
+  int heads, skip;  // tiles ahead of the gap, and tiles in it
+  int tiles;        // tiles walked (one empty one if there is nothing to see)
+};
+
+FAT_HD DecodeSpan decode_span(int len, int window, int sinks, int tile) {
+  DecodeSpan s;
+  s.lo = window > 0 && len > window ? len - window : 0;
+  s.sink = sinks < len ? sinks : len;
+  if (s.sink >= s.lo) s.lo = s.sink = 0;  // one range
+  s.heads = s.sink > 0 ? (s.sink - 1) / tile + 1 : 0;
+  s.skip = s.lo / tile > s.heads ? s.lo / tile - s.heads : 0;
+  s.tiles = (len > tile ? (len - 1) / tile + 1 : 1) - s.skip;
+  return s;
+}
+
+// The tile of the sequence that is walked i-th.
+FAT_HD int decode_span_tile(const DecodeSpan& s, int i) { return i < s.heads ? i : i + s.skip; }
+
+FAT_HD bool decode_span_sees(const DecodeSpan& s, int at) { return at < s.sink || at >= s.lo; }
+
+// The most tiles that a sequence of at most `positions` can have.
+FAT_HD long long decode_span_most(long long positions, int window, int sinks, int tile) {
+  const long long all = positions > tile ? (positions - 1) / tile + 1 : 1;
+  if (window <= 0) return all;
+  const long long seen = (static_cast<long long>(sinks) + tile - 1) / tile +
+                         (static_cast<long long>(window) + tile - 1) / tile + 1;
+  return seen < all ? seen : all;
+}
+
 // Tiles of one block: an equal share, but at least `least` (a split costs the
 // join of its parts).
 template <typename T>

@@ -70,7 +70,9 @@ def declare(lib) -> None:
             ("fat_kv_block_scores", [*query, _P, _L, _I, _I, _I, table, _P, _P], _I),
             ("fat_attn_decode_sparse",
              [cache, table, *query, _P, _I, _I, _I, _F, _P, _P, _P, _P, _Z, _P], _I),
-            ("fat_attn_decode_sparse_workspace_bytes", [_I, _I, _I, _I, _I], _Z)):
+            ("fat_attn_decode_sparse_workspace_bytes", [_I, _I, _I, _I, _I], _Z),
+            ("fat_attn_decode_window",
+             [cache, table, *query, _I, _I, _F, _P, _P, _P, _Z, _P], _I)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, result
 
@@ -446,3 +448,30 @@ def attn_decode_sparse(q, k_cache, v_cache, page_table, seq_lens, scores, num_bl
           int(first_blocks), int(last_blocks), d ** -0.5 if scale is None else scale,
           o.data_ptr(), lse.data_ptr(), blocks.data_ptr(), *work, _handle(stream, device))
     return o, lse, blocks
+
+
+def attn_decode_window(q, k_cache, v_cache, page_table, seq_lens, window: int, sinks: int = 0,
+                       scale: float | None = None, *, k_scale=None, v_scale=None,
+                       workspace=None, out=None, stream=None):
+    """Attention of one new query token per sequence over a sliding window.
+
+    The token sees the last ``window`` positions of its sequence (its own among
+    them) and the first ``sinks`` ones; the pages between them are neither read
+    nor used (they may have been given back).  Everything else as in
+    :func:`attn_decode_paged`; the workspace is needed only where the window, the
+    sinks and the table all hold more than 512 positions, whole 64s counted.
+    """
+    args, device, (_, heads, page_size, d), batch, width, o, lse, stream = _decode_arguments(
+        q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, out, stream)
+    if not 1 <= window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
+        raise ValueError("window must be at least 1 and sinks at least 0, both below 2^31")
+    window, sinks = int(window), int(sinks)
+    seen = min(-(-width * page_size // 64), -(-sinks // 64) + -(-window // 64) + 1) * 64
+    if workspace is None and seen <= _DIRECT:
+        work = None, 0
+    else:
+        work = _workspace(workspace, (batch, q.shape[1], heads, d), device, stream)
+    _call("fat_attn_decode_window", device, *args, window, sinks,
+          d ** -0.5 if scale is None else scale, o.data_ptr(), lse.data_ptr(), *work,
+          _handle(stream, device))
+    return o, lse
