@@ -107,6 +107,16 @@ int host_device(int* dev, unsigned int** error_word) {
   if (st == FAT_OK) *error_word = g_dev[*dev].error_word;
   return st;
 }
+
+bool encode_tensor_map(CUtensorMap* tm, CUtensorMapDataType type, int rank, void* ptr,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       CUtensorMapSwizzle swizzle) {
+  auto enc = encoder();
+  if (!enc) return false;
+  const cuuint32_t each[5] = {1, 1, 1, 1, 1};
+  return enc(tm, type, rank, ptr, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace fat
 
 extern "C" {

@@ -18,6 +18,12 @@ constexpr unsigned int kErrIndex = 2;  // the error word's bit for an index out 
 // refuses it (fat_attn_api.cu).
 int host_device(int* dev, unsigned int** error_word);
 
+// A tensor map of plain boxes (strides in bytes, of the dimensions behind the first); rows out
+// of range read as zero.  False if the driver refuses it (fat_attn_api.cu).
+bool encode_tensor_map(CUtensorMap* tm, CUtensorMapDataType type, int rank, void* ptr,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       CUtensorMapSwizzle swizzle);
+
 // Returns 0 or the fat_status code FAT_ERR_LAUNCH (-4).
 template <int D, int kX, bool kLTensor, int kDt, bool kZT = false>
 int launch_fwd(const FwdParams& fp, int dev, int grid, int splits, cudaStream_t stream) {

@@ -130,8 +130,15 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
   if (!stride_ok(q_token_stride, 2, &p.q_token) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(tree, 8) || !aligned(draft_lens, 4) || !aligned(workspace, 16))
     return FAT_ERR_ALIGNMENT;
+  // a row's strides have to be told apart by the copies
+  if (p.c.k_token == 0 || p.c.v_token == 0) return FAT_ERR_UNSUPPORTED;
   int dev = 0;
   if ((st = host_device(&dev, &p.t.error_word)) != FAT_OK) return st;
+  const int sms = sm_count(dev);
+  if (sms < 1) return FAT_ERR_LAUNCH;
+  p.error_word = p.t.error_word;
+  p.timeout_ns = 4000000000ull;
+  p.workspace = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const uint8_t*>(q);
   p.tokens = tokens;
   p.group = q_heads / cache->heads;
@@ -143,8 +150,8 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
   p.scale_log2 = scale * kArgLog2e;
   p.o = static_cast<uint8_t*>(o);
   p.lse = lse;
-  return status(
-      launch_tree(p, cache->d, cache->dtype == FAT_DTYPE_E4M3, dtype == FAT_DTYPE_BF16, dev, stream));
+  return status(launch_tree(p, cache->d, cache->dtype == FAT_DTYPE_E4M3, dtype == FAT_DTYPE_BF16,
+                            dev, sms, stream));
 }
 
 }  // extern "C"

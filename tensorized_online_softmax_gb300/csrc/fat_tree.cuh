@@ -1,12 +1,17 @@
-// Attention of drafted tokens over the paged cache: what its kernels are given, and
-// what a row sees.
+// Attention of drafted tokens over the paged cache: what its kernels are given, what a
+// row sees, and how the work is cut.
 #pragma once
 
 #include "fat_cache.cuh"
+#include "fat_decode_plan.h"
 
 namespace fat {
 
-constexpr int kTreeTokens = 64;  // drafted tokens of a sequence: bits of a mask
+constexpr int kTreeTokens = 64;   // drafted tokens of a sequence: bits of a mask
+constexpr int kTreeTile = 128;    // positions of a tile
+constexpr int kTreeBlockRows = 128;
+constexpr int kTreeMaxBlocks = 160;  // what the workspace has room for
+constexpr int kTreeDirect = 4;       // tiles of an item up to which it is not split
 
 struct TreeParams {
   CacheView c;
@@ -22,6 +27,12 @@ struct TreeParams {
   float scale_log2;                   // scale * log2(e)
   uint8_t* o;                         // [batch, tokens, q_heads, d]
   float* lse;                         // [batch, tokens, q_heads]
+  uint8_t* workspace;
+  int item_rows;    // rows of an item: a block of the rows (token, head of the group)
+  int row_blocks;   // items of a (sequence, cached head)
+  int direct;       // items are not split
+  unsigned long long poll_limit, timeout_ns;
+  unsigned int* error_word;
 };
 
 // A sequence's length and how many of its last positions are drafted tokens.
@@ -40,7 +51,7 @@ __device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int b) {
   return n;
 }
 
-// What drafted token t sees: of the context the positions below `sink` and from `lo`
+// What drafted token t sees: of the context the positions below `sinks` and from `lo`
 // on, of the drafted tokens those in `mask`.  Its own position is the context's length
 // plus the drafted tokens that it sees, itself among them, less one.
 struct TreeRow {
@@ -56,7 +67,16 @@ __device__ __forceinline__ TreeRow tree_row(const TreeParams& p, const TreeLens&
   return r;
 }
 
+// The tiles that are walked for a sequence: those with a position that some row may see
+// (a row that sees no drafted token sees the window one further back than the others).
+__device__ __forceinline__ DecodeSpan tree_span(const TreeParams& p, const TreeLens& n) {
+  const int len = n.drafted > 0 ? n.len : 0;
+  const int window = p.window > 0 ? min(p.window, 1 << 30) + n.drafted : 0;
+  return decode_span(len, window, p.sinks, kTreeTile);
+}
+
 size_t tree_workspace_bytes(int tokens, int group, int d);
-int launch_tree(const TreeParams& p, int d, bool e4m3, bool bf16, int dev, cudaStream_t stream);
+int launch_tree(const TreeParams& p, int d, bool e4m3, bool bf16, int dev, int sms,
+                cudaStream_t stream);
 
 }  // namespace fat
