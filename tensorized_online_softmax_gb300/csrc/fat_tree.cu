@@ -15,7 +15,7 @@ namespace {
 
 // K or V as [page, head, token, d], in boxes of as many tokens as a tile has of a page: 64
 // columns of 16 bits, 128-byte swizzle (the layout of the MMA's operands), or whole rows of
-// codes as they are.  A dimension whose stride is 0 becomes one of size 1, and its
+// codes (swizzled alike where they have 128 bytes).  A dimension whose stride is 0 becomes one of size 1, and its
 // coordinates are multiplied by 0.
 bool cache_map(CUtensorMap* tm, void* ptr, const CacheView& c, int d, bool e4m3, uint32_t page,
                uint32_t head, uint32_t token, int* by_page, int* by_head) {
@@ -31,7 +31,7 @@ bool cache_map(CUtensorMap* tm, void* ptr, const CacheView& c, int d, bool e4m3,
   return encode_tensor_map(tm,
                            e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                            4, ptr, dims, strides, box,
-                           e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+                           e4m3 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Rows of an item: one block of 128, or two for 16-bit caches with more; the rows beyond that

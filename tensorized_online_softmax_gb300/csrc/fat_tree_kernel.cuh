@@ -69,7 +69,8 @@ struct Join {  // what the join kernel needs of the item that starts, unfinished
   int part;  // where the first block keeps its part
 };
 constexpr size_t kJoinBytes = sizeof(Join) * kTreeMaxBlocks;
-// then, for each block and part, `rows` LSEs (log2), and after all of those the rows
+// then, for each block and part, `rows` LSEs (log2), and after all of those the rows: four
+// columns of all rows, then the next four, as threads hold one row each
 __host__ __device__ inline size_t lse_at(int block, int part, int rows) {
   return kJoinBytes + sizeof(float) * (static_cast<size_t>(block) * 2 + part) * rows;
 }
@@ -94,13 +95,14 @@ struct Layout {
   static constexpr int kKStages = kE4M3 ? 2 : D == 64 ? (kNB == 1 ? 6 : 5) : kNB == 1 ? 3 : 2;
   static constexpr int kStages = kE4M3 ? 2 : D == 64 ? (kNB == 1 ? 6 : 5) : 3;
   static constexpr int kRawStages = !kE4M3 ? 0 : D == 64 ? 12 : kParts == 2 ? 2 : 4;
-  static constexpr int kRawTile = kTreeTile * D + kTreeTile;  // codes, then scale bytes
+  static constexpr int kRawTile = kTreeTile * D;  // codes
   static constexpr int kAtoms = D / 64;  // slabs of 64 columns (128 bytes)
   static constexpr int kQ = 0;
   static constexpr int kK = kNB * kParts * kTile;
   static constexpr int kV = kK + kKStages * kTile;
   static constexpr int kRaw = kV + kStages * kTile;
-  static constexpr int kBars = kRaw + kRawStages * kRawTile;
+  static constexpr int kScales = kRaw + kRawStages * kRawTile;  // of the codes' rows
+  static constexpr int kBars = kScales + kRawStages * kTreeTile;
   static constexpr int bKFull = 0;
   static constexpr int bKEmpty = bKFull + kKStages;
   static constexpr int bVFull = bKEmpty + kKStages;
@@ -117,7 +119,7 @@ struct Layout {
   static __device__ __forceinline__ int arrivals(int bar) {
     if (kE4M3 && ((bar >= bKFull && bar < bKEmpty) || (bar >= bVFull && bar < bVEmpty) ||
                   (bar >= bRawEmpty && bar < bSFull)))
-      return kConvertWarps;
+      return kConvertWarps / 2;
     return bar == bPFull || bar == bPFull + 1 ? 4 : bar == bQFull || bar == bSync ? 8 : 1;
   }
   static constexpr int kMisc = kBars + ((8 * kNumBars + 15) & ~15);
@@ -127,8 +129,9 @@ struct Layout {
   // float [2 groups][2][128]: reference and sum of each row; ahead of that the plan's sums
   static constexpr int kFin = kBad + 16;
   static constexpr int kBytes = kFin + 2 * 2 * kTreeBlockRows * 4;
+  static_assert(kRawStages % 2 == 0, "K's and V's codes in turn");
   static_assert(!kE4M3 || kNB == 1, "one block of rows where the codes need room");
-  static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kRaw % 128 == 0, "tiles on 1 KB");
+  static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kRaw % 1024 == 0, "tiles on 1 KB");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -169,17 +172,23 @@ __device__ __forceinline__ uint32_t below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// Bits 15 and 31 say which of two 16-bit values are not finite: their exponents overflow.
 template <bool kFp16>
-__device__ __forceinline__ bool finite16(uint32_t two) {
+__device__ __forceinline__ uint32_t not_finite(uint32_t two) {
   constexpr uint32_t kExp = kFp16 ? 0x7C007C00u : 0x7F807F80u;
-  const uint32_t e = two & kExp;
-  return (e & 0xFFFFu) != (kExp & 0xFFFFu) && (e >> 16) != (kExp >> 16);
+  return (two & kExp) + (kFp16 ? 0x04000400u : 0x00800080u);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // element c of the row of V at position j; what is out of range reads as 0 (the sequence's
 // results are unspecified then)
 template <int kType>
-__device__ __noinline__ float value_at(const TreeParams& p, int b, uint32_t head, int j, int c) {
+__device__ __forceinline__ float value_at(const TreeParams& p, int b, uint32_t head, int j, int c) {
   const int page = table_page(p.t, p.c.num_pages, b, j >> p.c.page_shift);
   if (page < 0) return 0.f;
   const uint32_t at = j & (p.c.page_size - 1);
@@ -192,6 +201,26 @@ __device__ __noinline__ float value_at(const TreeParams& p, int b, uint32_t head
   return unpack16<kType == kBf16>(reinterpret_cast<const uint16_t*>(row)[c]).x;
 }
 
+// Adds the non-finite values of the positions base + (bits of `left`) to columns col0 .. of a
+// row that this thread has just written: 16-bit values at `out`, or, where that is null, fp32
+// in the workspace.  (Hardly ever called.)
+template <int kType, bool kOutBf16>
+__device__ __noinline__ void add_not_finite(const TreeParams& p, int b, uint32_t head, int base,
+                                            unsigned long long left, int col0, int cols,
+                                            uint16_t* out, float* part) {
+  for (; left; left &= left - 1) {
+    const int j = base + __ffsll(static_cast<long long>(left)) - 1;
+    for (int c = col0; c < col0 + cols; ++c) {
+      const float v = value_at<kType>(p, b, head, j, c);
+      if (fabsf(v) < INFINITY) continue;
+      if (out)
+        out[c] = static_cast<uint16_t>(pack16<kOutBf16>(unpack16<kOutBf16>(out[c]).x + v, 0.f));
+      else
+        part[static_cast<size_t>(c / 4) * p.item_rows * 4 + c % 4] += v;
+    }
+  }
+}
+
 template <int D, int kType, int kNB>
 __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     tree_kernel(const __grid_constant__ KernelParams kp) {
@@ -200,6 +229,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   constexpr bool kFp16 = kType == kF16;  // the products' operands
   constexpr bool kOutBf16 = kType == kBf16 || kType == kE4M3Bf16;
   constexpr int kParts = L::kParts;
+  constexpr int kCh = L::kE4M3 ? 1 : 2;  // times 32 scores in registers at a time
   constexpr int SK = L::kKStages, SV = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = kp.p;
@@ -350,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           if constexpr (L::kE4M3) {
             const uint32_t to = ring + slot * L::kRawTile;
             tma_load_4d(to + lane * box_bytes, tm, bar(full + slot), 0, place, c2, c3);
-            bulk_load(to + kTreeTile * D + lane * rows,
+            bulk_load(sb + L::kScales + slot * kTreeTile + lane * rows,
                       (is_k ? p.c.k_scale : p.c.v_scale) + scale_offset(p.c, page, head, place),
                       rows, bar(full + slot));
           } else {
@@ -461,64 +491,112 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     __syncwarp();
   } else if (L::kE4M3 && warp >= kConvertWarp) {
     // =================== converters ===================
-    // 16 rows of a tile to a warp, 16 codes of a row to a lane at a time
-    constexpr int kC = D / 16, kPer = 16 * kC / 32;
-    int raw = 0, slot[2] = {0, 0};
-    uint32_t raw_phase = 0, phase[2] = {0, 0};
+    // Half of the warps take K's tiles, half V's: 32 rows of a tile to a warp, 16 codes to a
+    // lane at a time, four of those with their loads ahead of the arithmetic.
+    constexpr int kC = D / 16, kEach = 4;
+    const bool is_v = warp >= kConvertWarp + kConvertWarps / 2;
+    const int row0 = (warp - kConvertWarp) % (kConvertWarps / 2) * 32;
+    const int S = is_v ? SV : SK;
+    const int full = is_v ? L::bVFull : L::bKFull, empty = is_v ? L::bVEmpty : L::bKEmpty;
+    const uint32_t ring = sb + (is_v ? L::kV : L::kK);
+    // Four lanes have 64 codes of a row, eight groups of them eight rows.  128-byte rows are
+    // swizzled as they come; rows 5 apart (by xor) in neighbouring groups meet no bank twice,
+    // neither here nor in the tile that is written.
+    const int group = lane / 4;
+    const int my_row = D == 64 ? group : (group / 2) ^ (group % 2 * 5);
+    int raw = is_v ? 1 : 0, slot = 0;
+    uint32_t raw_phase = 0, phase = 0;
     bool ok = true;
 #pragma unroll 1
-    for (int i = 0; ok && i < count; ++i) {
+    for (int i = 0; i < count; ++i) {
+      const uint32_t from = sb + L::kRaw + raw * L::kRawTile;
+      const uint32_t scales = sb + L::kScales + raw * kTreeTile;
+      const uint32_t to = ring + slot * L::kTile;
+      if (!(ok = wait(L::bRawFull + raw, raw_phase))) break;
+      if (!(ok = wait(empty + slot, phase ^ 1u))) break;
+#pragma unroll 1
+      for (int x = 0; x < kC; x += kEach) {  // kC pieces of eight rows and 64 codes
+        uint32_t in[kEach][4], e[kEach];
 #pragma unroll
-      for (int turn = 0; turn < 2; ++turn) {
-        const int S = turn == 0 ? SK : SV;
-        const uint32_t from = sb + L::kRaw + raw * L::kRawTile;
-        const uint32_t to = sb + (turn == 0 ? L::kK : L::kV) + slot[turn] * L::kTile;
-        if (!(ok = wait(L::bRawFull + raw, raw_phase))) break;
-        if (!(ok = wait((turn == 0 ? L::bKEmpty : L::bVEmpty) + slot[turn], phase[turn] ^ 1u)))
-          break;
+        for (int y = 0; y < kEach; ++y) {
+          const int row = row0 + (x + y) % 4 * 8 + my_row;
+          const int c = (x + y) / 4 * 4 + lane % 4;
+          const float4 v =
+              ld_shared_v4(from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16);
+          in[y][0] = __float_as_uint(v.x), in[y][1] = __float_as_uint(v.y);
+          in[y][2] = __float_as_uint(v.z), in[y][3] = __float_as_uint(v.w);
+          asm volatile("ld.shared.u8 %0, [%1];"
+                       : "=r"(e[y])
+                       : "r"(scales + row)
+                       : "memory");
+        }
+        // A code's sign and seven other bits in the places of a bf16's sign, low exponent and
+        // high mantissa are the value times 2^-120, subnormal codes included; one
+        // multiplication by 2^(120 + e - 127) makes it right, and NaN of a row that is one.
+        // Codes that are NaN and scales that bf16 has not take the slow way.
+        uint32_t out[kEach][8];
+        bool slow = false;
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int at = (warp - kConvertWarp) * 16 * kC + x * 32 + lane;
-          const int row = at / kC, c = at % kC;
-          const float4 codes = ld_shared_v4(from + at * 16);
-          uint32_t e;
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(from + kTreeTile * D + row) : "memory");
-          const float scale = scale_value(e);
-          const uint64_t scale2 = f2_pack(scale, scale);
-          const uint32_t in[4] = {__float_as_uint(codes.x), __float_as_uint(codes.y),
-                                  __float_as_uint(codes.z), __float_as_uint(codes.w)};
-          uint32_t out[8];
+        for (int y = 0; y < kEach; ++y) {
+          uint32_t nan = 0;
+          const uint32_t s2 = e[y] == 255u ? 0x7FFF7FFFu : ((e[y] + 120u) << 7) * 0x00010001u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t h[2];
-            e4m3x4_to_f16(in[k], h[0], h[1]);
+            nan |= (in[y][k] & 0x7F7F7F7Fu) + 0x01010101u;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float2 f = unpack16<false>(h[y]);
-              float a, b;
-              f2_unpack(f2_mul(f2_pack(f.x, f.y), scale2), a, b);
-              out[2 * k + y] = pack16<true>(a, b);
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t w = __byte_perm(in[y][k], 0u, z ? 0x3424 : 0x1404);
+              out[y][2 * k + z] = mul_bf16x2(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u), s2);
             }
           }
-          const uint32_t line = to + (c / 4) * (kTreeTile * 128) + row * 128;
-          const int first = c / 4;  // (lanes of the two slabs write in turn: no bank is met twice)
+          slow |= (nan & 0x80808080u) != 0 || (e[y] >= 135u && e[y] < 255u);
+        }
+        if (slow) {
+#pragma unroll 1
+          for (int y = 0; y < kEach; ++y) {
+            const int row = row0 + (x + y) % 4 * 8 + my_row;
+            const int c = (x + y) / 4 * 4 + lane % 4;
+            const uint32_t line = to + (c / 4) * (kTreeTile * 128) + row * 128;
+            const uint32_t codes = from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16;
+            uint32_t eb;
+            asm volatile("ld.shared.u8 %0, [%1];"
+                         : "=r"(eb)
+                         : "r"(scales + row)
+                         : "memory");
+            const float scale = scale_value(eb);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {  // pairs
+              uint32_t w, lo, hi;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(codes + k / 2 * 4) : "memory");
+              e4m3x4_to_f16(w, lo, hi);
+              const float2 f = unpack16<false>(k % 2 ? hi : lo);
+              const uint32_t at = line + ((2 * c + k / 4) % 8 ^ (row & 7)) * 16 + k % 4 * 4;
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at),
+                           "r"(pack16<true>(f.x * scale, f.y * scale))
+                           : "memory");
+            }
+          }
+        } else {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int half = y ^ first;
-            const uint32_t chunk = ((2 * c + half) % 8) ^ (row & 7);
-            st_shared_v4u(line + chunk * 16, half ? out[4] : out[0], half ? out[5] : out[1],
-                          half ? out[6] : out[2], half ? out[7] : out[3]);
+          for (int y = 0; y < kEach; ++y) {
+            const int row = row0 + (x + y) % 4 * 8 + my_row;
+            const int c = (x + y) / 4 * 4 + lane % 4;
+            const uint32_t line = to + (c / 4) * (kTreeTile * 128) + row * 128;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              st_shared_v4u(line + ((2 * c + z) % 8 ^ (row & 7)) * 16, out[y][4 * z],
+                            out[y][4 * z + 1], out[y][4 * z + 2], out[y][4 * z + 3]);
           }
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar((turn == 0 ? L::bKFull : L::bVFull) + slot[turn]));
-          mbar_arrive(bar(L::bRawEmpty + raw));
-        }
-        if (++raw == L::kRawStages) raw = 0, raw_phase ^= 1u;
-        if (++slot[turn] == S) slot[turn] = 0, phase[turn] ^= 1u;
       }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(full + slot));
+        mbar_arrive(bar(L::bRawEmpty + raw));
+      }
+      if ((raw += 2) >= L::kRawStages) raw -= L::kRawStages, raw_phase ^= 1u;
+      if (++slot == S) slot = 0, phase ^= 1u;
     }
     __syncwarp();
   } else if (warp < kMmaWarp) {
@@ -614,44 +692,44 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         if (!(ok = wait(L::bSFull + g, s_phase))) break;
         tc_fence_after();
         if (warp_live) {
-          uint32_t vis[4];  // what of the tile the row sees
-          if (!whole_tile) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int base = pos0 + 32 * k;
-              uint32_t m = below(context - base);
-              if (p.window > 0) m &= below(p.sinks - base) | ~below(seen.lo - base);
-              const int shift = context - base;  // bit of the first drafted token
-              const uint32_t drafted = shift >= 32 || shift <= -64 ? 0u
-                                       : shift >= 0
-                                           ? static_cast<uint32_t>(seen.mask << shift)
-                                           : static_cast<uint32_t>(seen.mask >> -shift);
-              vis[k] = live ? m | drafted : 0u;
-            }
-          }
           float top = -INFINITY;
+#pragma unroll 1  // (little code: what an item's end runs must not be fetched anew each time)
+          for (int k = 0; k < 4; k += kCh) {
+            uint32_t s[kCh][32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t s[32];
-            tmem_ld32(s_at + 32 * k, s);
-            tmem_wait_ld(s);
-            if (!whole_tile) {
+            for (int y = 0; y < kCh; ++y) tmem_ld32(s_at + 32 * (k + y), s[y]);
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!(vis[k] >> x & 1u)) s[x] = 0xFF800000u;
+            for (int y = 0; y < kCh; ++y) tmem_wait_ld(s[y]);
+            if (!whole_tile) {  // what the row does not see becomes -inf, for the second pass too
+#pragma unroll
+              for (int y = 0; y < kCh; ++y) {
+                const int base = pos0 + 32 * (k + y);
+                uint32_t m = below(context - base);
+                if (p.window > 0) m &= below(p.sinks - base) | ~below(seen.lo - base);
+                const int shift = context - base;  // bit of the first drafted token
+                m |= shift >= 32 || shift <= -64 ? 0u
+                     : shift >= 0               ? static_cast<uint32_t>(seen.mask << shift)
+                                                : static_cast<uint32_t>(seen.mask >> -shift);
+                if (!live) m = 0;
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!(m >> x & 1u)) s[y][x] = 0xFF800000u;
+                tmem_st32(s_at + 32 * (k + y), s[y]);
+              }
+              tmem_wait_st();
             }
-            float mx[2];
+            float mx[2 * kCh];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              mx[a] = fmax3(__uint_as_float(s[16 * a]), __uint_as_float(s[16 * a + 1]),
-                            __uint_as_float(s[16 * a + 2]));
+            for (int a = 0; a < 2 * kCh; ++a) {
+              const uint32_t* v = s[a / 2] + a % 2 * 16;
+              mx[a] = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
 #pragma unroll
               for (int x = 3; x < 15; x += 2)
-                mx[a] = fmax3(mx[a], __uint_as_float(s[16 * a + x]),
-                              __uint_as_float(s[16 * a + x + 1]));
+                mx[a] = fmax3(mx[a], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+              mx[a] = fmaxf(mx[a], __uint_as_float(v[15]));
             }
-            top = fmax3(top, mx[0], mx[1]);
-            top = fmax3(top, __uint_as_float(s[15]), __uint_as_float(s[31]));
+#pragma unroll
+            for (int a = 0; a < kCh; ++a) top = fmax3(top, mx[2 * a], mx[2 * a + 1]);
           }
           const float z = top * p.scale_log2;
           const bool raise = z > limit;
@@ -668,7 +746,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
               // O refers to the old reference: once the last O += P V has landed
               if (!(ok = wait(L::bPV + g, s_phase ^ 1u))) break;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
                 tmem_ld32(o_at + 32 * k, o);
@@ -682,35 +760,37 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           }
           const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), r2 = f2_pack(-ref, -ref);
           uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll 1
+          for (int k = 0; k < 4; k += kCh) {
+            uint32_t s[kCh][32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t s[32], pk[16 * kParts];
-            tmem_ld32(s_at + 32 * k, s);
-            tmem_wait_ld(s);
-            if (!whole_tile) {
+            for (int y = 0; y < kCh; ++y) tmem_ld32(s_at + 32 * (k + y), s[y]);
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!(vis[k] >> x & 1u)) s[x] = 0xFF800000u;
-            }
+            for (int y = 0; y < kCh; ++y) tmem_wait_ld(s[y]);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const uint64_t z2 = f2_fma(
-                  f2_pack(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, r2);
-              float z0, z1;
-              f2_unpack(z2, z0, z1);
-              z0 = ex2_approx(z0);
-              z1 = ex2_approx(z1);
-              acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
-              pk[x] = pack16<!kFp16>(z0, z1);
-              if constexpr (kParts == 2) {
-                const float2 h = unpack16<true>(pk[x]);
-                pk[16 + x] = pack16<true>(z0 - h.x, z1 - h.y);
+            for (int y = 0; y < kCh; ++y) {
+              uint32_t pk[16 * kParts];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const uint64_t z2 = f2_fma(f2_pack(__uint_as_float(s[y][2 * x]),
+                                                   __uint_as_float(s[y][2 * x + 1])),
+                                           c2, r2);
+                float z0, z1;
+                f2_unpack(z2, z0, z1);
+                z0 = ex2_approx(z0);
+                z1 = ex2_approx(z1);
+                acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
+                pk[x] = pack16<!kFp16>(z0, z1);
+                if constexpr (kParts == 2) {
+                  const float2 h = unpack16<true>(pk[x]);
+                  pk[16 + x] = pack16<true>(z0 - h.x, z1 - h.y);
+                }
               }
+              if constexpr (kParts == 2)
+                tmem_st32(s_at + 32 * (k + y), pk);
+              else
+                tmem_st16(s_at + 16 * (k + y), pk);
             }
-            if constexpr (kParts == 2)
-              tmem_st32(s_at + 32 * k, pk);
-            else
-              tmem_st16(s_at + 16 * k, pk);
           }
           float a0, a1;
           f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
@@ -724,38 +804,42 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           if (!(j < context && (p.window <= 0 || j < p.sinks || j >= w.hi)) || w.n.drafted == 0) {
             const bool drafted = j >= context && j < w.n.len;
             const bool border = j < context && j >= w.lo;
-            const bool some = w.n.drafted > 0 && (drafted || border);
+            bool zero = w.n.drafted == 0 || !(drafted || border);
             const uint32_t line = sb + L::kV + v_slot * L::kTile + r * 128;
-            bool found = false;
-#pragma unroll 1
-            for (int x = 0; x < L::kAtoms; ++x)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint32_t at = line + x * (kTreeTile * 128) + c * 16;
-                if (!some) {
-                  st_shared_v4u(at, 0u, 0u, 0u, 0u);
-                  continue;
-                }
-                const float4 f = ld_shared_v4(at);
-                uint32_t v[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
-                                 __float_as_uint(f.w)};
-                bool fine = true;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (finite16<kFp16>(v[k])) continue;
-                  fine = false;
-                  if (!finite16<kFp16>(v[k] & 0xFFFFu)) v[k] &= 0xFFFF0000u;
-                  if (!finite16<kFp16>(v[k] & 0xFFFF0000u)) v[k] &= 0x0000FFFFu;
-                }
-                if (fine) continue;
-                if (!found) {
-                  // noted before it is gone: the other group may look at the same row
-                  atomicOr(&bad[drafted ? 0 : 1], 1ull << (drafted ? j - context : j - w.lo));
-                  __threadfence_block();
-                }
-                found = true;
-                st_shared_v4u(at, v[0], v[1], v[2], v[3]);
+            // (chunks in the order of the swizzle: neighbouring rows meet no bank twice)
+            auto at = [&](int c) {
+              return line + c / 8 * (kTreeTile * 128) + ((c % 8) ^ (r & 7)) * 16;
+            };
+            uint32_t odd = 0;
+            if (!zero) {
+#pragma unroll 8
+              for (int c = 0; c < 8 * L::kAtoms; ++c) {
+                const float4 f = ld_shared_v4(at(c));
+                odd |= not_finite<kFp16>(__float_as_uint(f.x)) |
+                       not_finite<kFp16>(__float_as_uint(f.y));
+                odd |= not_finite<kFp16>(__float_as_uint(f.z)) |
+                       not_finite<kFp16>(__float_as_uint(f.w));
               }
+            }
+            if (odd & 0x80008000u) {
+              // noted before they are gone: the other group may look at the same row
+              atomicOr(&bad[drafted ? 0 : 1], 1ull << (drafted ? j - context : j - w.lo));
+              __threadfence_block();
+#pragma unroll 1
+              for (int c = 0; c < 32 * L::kAtoms; ++c) {
+                const uint32_t word = at(c / 4) + c % 4 * 4;
+                uint32_t v;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(word) : "memory");
+                const uint32_t n = not_finite<kFp16>(v);
+                if (n & 0x8000u) v &= 0xFFFF0000u;
+                if (n & 0x80000000u) v &= 0x0000FFFFu;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(word), "r"(v) : "memory");
+              }
+            }
+            if (zero) {
+#pragma unroll 8
+              for (int c = 0; c < 8 * L::kAtoms; ++c) st_shared_v4u(at(c), 0u, 0u, 0u, 0u);
+            }
           }
           fence_async_shared();
         }
@@ -792,8 +876,6 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const float lse =
           sum == 0.f ? -INFINITY : (base == -INFINITY ? 0.f : base) + log2f(sum);
-      const unsigned long long bad_drafted = bad[0] & seen.mask;
-      const unsigned long long bad_border = bad[1];
       const int h = (row0 + my_row) - t * p.group;
       const long long at =
           ((static_cast<long long>(b) * p.tokens + t) * p.c.heads + head) * p.group + h;
@@ -820,24 +902,6 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           }
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = sum == 0.f ? 0.f : x[c] * inv;
-          if (live && (bad_drafted | bad_border)) {
-            // (hardly ever) non-finite values that this row sees
-            for (int which = 0; which < 2; ++which) {
-              for (unsigned long long left = which ? bad_border : bad_drafted; left;
-                   left &= left - 1) {
-                const int j = (which ? w.lo : context) + __ffsll(left) - 1;
-                if (which && j < seen.lo) continue;
-#pragma unroll 1
-                for (int c = 0; c < 32; ++c) {
-                  const float v = value_at<kType>(p, b, head, j, col0 + 32 * k + c);
-                  if (fabsf(v) < INFINITY) continue;
-#pragma unroll
-                  for (int y = 0; y < 32; ++y)
-                    if (y == c) x[y] += v;
-                }
-              }
-            }
-          }
           if (my_row < rows) {
             if (whole) {
               uint4* out = reinterpret_cast<uint4*>(p.o + (at * D + col0 + 32 * k) * 2);
@@ -849,13 +913,27 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                                     pack16<kOutBf16>(x[8 * c + 6], x[8 * c + 7]));
             } else {
               float4* out = reinterpret_cast<float4*>(
-                  p.workspace + rows_at(blockIdx.x, part, p.item_rows, D) +
-                  (static_cast<size_t>(my_row) * D + col0 + 32 * k) * 4);
+                                p.workspace + rows_at(blockIdx.x, part, p.item_rows, D)) +
+                            (col0 / 4 + 8 * k) * p.item_rows + my_row;
 #pragma unroll
               for (int c = 0; c < 8; ++c)
-                out[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                out[c * p.item_rows] =
+                    make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
             }
           }
+        }
+        // non-finite values that only some rows see, this one among them
+        if (live && (bad[0] | bad[1])) {
+          uint16_t* out = whole ? reinterpret_cast<uint16_t*>(p.o) + at * D : nullptr;
+          float* ws = reinterpret_cast<float*>(p.workspace +
+                                               rows_at(blockIdx.x, part, p.item_rows, D)) +
+                      4 * my_row;
+          add_not_finite<kType, kOutBf16>(p, b, head, context, bad[0] & seen.mask, col0, kCols, out,
+                                          ws);
+          const int behind = seen.lo - w.lo;  // of the border positions: those that it does not see
+          add_not_finite<kType, kOutBf16>(p, b, head, w.lo,
+                                          behind >= 64 ? 0ull : bad[1] >> behind << behind, col0,
+                                          kCols, out, ws);
         }
         if (my_row < rows && (kNB == 2 || g == 0)) {
           if (whole)
@@ -890,39 +968,34 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// The join of an item's parts: a warp to each row of the item that starts, unfinished, in
-// block blockIdx.x of tree_kernel.  Parts are taken in order, a batch of loads at a time.
-constexpr int kJoinWarps = 8;
+// The join of an item's parts: eight columns of a row of the item that starts, unfinished, in
+// block blockIdx.x of tree_kernel to a thread, neighbouring rows to neighbouring threads.
+// Parts are taken in order, a batch of loads at a time.
+constexpr int kJoinThreads = 128;
 template <int D, bool kOutBf16>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const TreeParams p) {
-  constexpr int kPer = D / 32, kBatch = 8;
-  const int lane = threadIdx.x % 32;
-  const int c0 = blockIdx.x, row = blockIdx.y * kJoinWarps + threadIdx.x / 32;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const TreeParams p, int rows_most) {
+  constexpr int kBatch = 4;
+  const int c0 = blockIdx.x, job = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int cols = job / rows_most, row = job - cols * rows_most;
   grid_dep_wait();
   const Join j = reinterpret_cast<const Join*>(p.workspace)[c0];
-  if (j.last < 0) return;
+  if (j.last < 0 || cols >= D / 8) return;
   const int head = j.item / p.row_blocks;
   const int row0 = (j.item - head * p.row_blocks) * p.item_rows;
-  const int rows = min(p.item_rows, p.tokens * p.group - row0);
-  if (row >= rows) return;
-  float top = -INFINITY, sum = 0.f, acc[kPer] = {};
+  if (row >= min(p.item_rows, p.tokens * p.group - row0)) return;
+  float top = -INFINITY, sum = 0.f, acc[8] = {};
 #pragma unroll 1
   for (int c = c0; c <= j.last; c += kBatch) {
-    float lse[kBatch], x[kBatch][kPer];
+    float lse[kBatch];
+    float4 x[kBatch][2];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int at = min(c + i, j.last), part = at == c0 ? j.part : 0;
       lse[i] = reinterpret_cast<const float*>(p.workspace + lse_at(at, part, p.item_rows))[row];
-      const float* o = reinterpret_cast<const float*>(
-                           p.workspace + rows_at(at, part, p.item_rows, D)) +
-                       static_cast<size_t>(row) * D + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        x[i][0] = v.x, x[i][1] = v.y;
-      }
+      const float4* o =
+          reinterpret_cast<const float4*>(p.workspace + rows_at(at, part, p.item_rows, D)) + row;
+      x[i][0] = o[2 * cols * p.item_rows];
+      x[i][1] = o[(2 * cols + 1) * p.item_rows];
     }
     float m = top;
 #pragma unroll
@@ -931,7 +1004,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const TreeParams 
       const float f = top == -INFINITY ? 1.f : ex2_approx(top - m);
       sum *= f;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] *= f;
+      for (int k = 0; k < 8; ++k) acc[k] *= f;
       top = m;
     }
 #pragma unroll
@@ -939,18 +1012,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const TreeParams 
       if (c + i > j.last || lse[i] == -INFINITY) continue;  // (an empty part: zeros)
       const float f = ex2_approx(lse[i] - (top == -INFINITY ? 0.f : top));
       sum += f;
+      const float v[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                          x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(f, x[i][k], acc[k]);
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(f, v[k], acc[k]);
     }
   }
   const int t = (row0 + row) / p.group, h = (row0 + row) - t * p.group;
   const long long at =
       ((static_cast<long long>(j.entry) * p.tokens + t) * p.c.heads + head) * p.group + h;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.o) + (at * D + lane * kPer) / 2;
-#pragma unroll
-  for (int k = 0; k < kPer / 2; ++k) out[k] = pack16<kOutBf16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if (lane == 0)
+  reinterpret_cast<uint4*>(p.o)[at * (D / 8) + cols] =
+      make_uint4(pack16<kOutBf16>(acc[0] * inv, acc[1] * inv),
+                 pack16<kOutBf16>(acc[2] * inv, acc[3] * inv),
+                 pack16<kOutBf16>(acc[4] * inv, acc[5] * inv),
+                 pack16<kOutBf16>(acc[6] * inv, acc[7] * inv));
+  if (cols == 0)
     p.lse[at] = sum == 0.f ? -INFINITY
                            : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718055994531f;
 }
@@ -1006,8 +1083,8 @@ int launch(const KernelParams& kp, int dev, int sms, cudaStream_t stream) {
                      kp))
     return -4;
   const int rows = p.tokens * p.group < p.item_rows ? p.tokens * p.group : p.item_rows;
-  const dim3 join(static_cast<unsigned>(grid), (rows + kJoinWarps - 1) / kJoinWarps);
-  return launch_kernel(join_kernel<D, kType == kBf16 || kType == kE4M3Bf16>, join, 32 * kJoinWarps, 0, stream, true, p)
+  const dim3 join(static_cast<unsigned>(grid), (rows * (D / 8) + kJoinThreads - 1) / kJoinThreads);
+  return launch_kernel(join_kernel<D, kType == kBf16 || kType == kE4M3Bf16>, join, kJoinThreads, 0, stream, true, p, rows)
              ? 0
              : -4;
 }
