@@ -130,8 +130,10 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
   if (!stride_ok(q_token_stride, 2, &p.q_token) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(tree, 8) || !aligned(draft_lens, 4) || !aligned(workspace, 16))
     return FAT_ERR_ALIGNMENT;
-  // a row's strides have to be told apart by the copies
-  if (p.c.k_token == 0 || p.c.v_token == 0) return FAT_ERR_UNSUPPORTED;
+  // (the copies take tokens of a page, and heads and tokens of the queries, as they lie in memory)
+  if (p.c.k_token == 0 || p.c.v_token == 0 || (p.q_head == 0 && q_heads > 1) ||
+      (p.q_token == 0 && tokens > 1))
+    return FAT_ERR_UNSUPPORTED;
   int dev = 0;
   if ((st = host_device(&dev, &p.t.error_word)) != FAT_OK) return st;
   const int sms = sm_count(dev);

@@ -34,13 +34,31 @@ bool cache_map(CUtensorMap* tm, void* ptr, const CacheView& c, int d, bool e4m3,
                            e4m3 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Rows of an item: one block of 128, or two for 16-bit caches with more; the rows beyond that
-// are shared out evenly, in whole warps.
-int item_rows_of(int rows, int blocks) {
-  const int most = blocks * kTreeBlockRows;
-  const int items = (rows + most - 1) / most;
-  const int each = ((rows + items - 1) / items + 31) / 32 * 32;
-  return each < most ? each : most;
+// The queries as [sequence, token, head, d], in boxes of a block of rows.
+bool query_map(CUtensorMap* tm, const TreeParams& p, int d, int* by_batch) {
+  *by_batch = p.q_batch != 0 && p.t.batch > 1;
+  const int heads = p.group * p.c.heads;
+  const uint32_t row = static_cast<uint32_t>(d) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(p.tokens),
+                              static_cast<cuuint64_t>(*by_batch ? p.t.batch : 1)};
+  const cuuint64_t strides[3] = {heads > 1 ? p.q_head : row, p.tokens > 1 ? p.q_token : row,
+                                 *by_batch ? p.q_batch : row};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.block_heads),
+                             static_cast<cuuint32_t>(p.block_tokens), 1};
+  return encode_tensor_map(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<uint8_t*>(p.q), dims,
+                           strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The cut of a cached head's rows into items of one block of at most 128 rows or of two: as few
+// blocks as hold them, shared out evenly.
+void cut_rows(int tokens, int group, int blocks, TreeParams* p) {
+  p->head_items = (group + kTreeBlockRows - 1) / kTreeBlockRows;
+  p->block_heads = (group + p->head_items - 1) / p->head_items;
+  const int most = kTreeBlockRows / p->block_heads;
+  p->token_items = (tokens + most * blocks - 1) / (most * blocks);
+  p->block_tokens = (tokens + p->token_items * blocks - 1) / (p->token_items * blocks);
+  p->item_rows = blocks * p->block_tokens * p->block_heads;
 }
 
 }  // namespace
@@ -48,24 +66,26 @@ int item_rows_of(int rows, int blocks) {
 }  // namespace tree
 
 size_t tree_workspace_bytes(int tokens, int group, int d) {
-  const int rows = tokens * group;
-  const int one = tree::item_rows_of(rows, 1), two = tree::item_rows_of(rows, 2);
-  return tree::rows_at(kTreeMaxBlocks, 0, one > two ? one : two, d);
+  TreeParams one, two;
+  tree::cut_rows(tokens, group, 1, &one);
+  tree::cut_rows(tokens, group, 2, &two);
+  return tree::rows_at(kTreeMaxBlocks, 0,
+                       one.item_rows > two.item_rows ? one.item_rows : two.item_rows, d);
 }
 
 int launch_tree(const TreeParams& params, int d, bool e4m3, bool bf16, int dev, int sms,
                 cudaStream_t stream) {
-  tree::KernelParams kp;
+  tree::KernelParams kp = {};
   kp.p = params;
   TreeParams& p = kp.p;
   const CacheView& c = p.c;
-  const int rows = p.tokens * p.group;
   // Two blocks of rows read the cache once for both; an e4m3 cache's conversion leaves room
   // for one.
-  const int blocks = !e4m3 && rows > kTreeBlockRows ? 2 : 1;
-  p.item_rows = tree::item_rows_of(rows, blocks);
-  p.row_blocks = (rows + p.item_rows - 1) / p.item_rows;
+  tree::cut_rows(p.tokens, p.group, 1, &p);
+  const int blocks = !e4m3 && p.token_items > 1 ? 2 : 1;
+  tree::cut_rows(p.tokens, p.group, blocks, &p);
   p.direct = 0;
+  if (!e4m3 && !tree::query_map(&kp.tm_q, p, d, &kp.q_batch)) return -4;
   if (!tree::cache_map(&kp.tm_k, c.k, c, d, e4m3, c.k_page, c.k_head, c.k_token, &kp.k_page,
                        &kp.k_head) ||
       !tree::cache_map(&kp.tm_v, c.v, c, d, e4m3, c.v_page, c.v_head, c.v_token, &kp.v_page,

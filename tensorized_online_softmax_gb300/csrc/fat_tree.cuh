@@ -28,8 +28,11 @@ struct TreeParams {
   uint8_t* o;                         // [batch, tokens, q_heads, d]
   float* lse;                         // [batch, tokens, q_heads]
   uint8_t* workspace;
-  int item_rows;    // rows of an item: a block of the rows (token, head of the group)
-  int row_blocks;   // items of a (sequence, cached head)
+  // Rows of a cached head: blocks of `block_tokens` tokens by `block_heads` of the group's
+  // heads (row = token * block_heads + head), one or two blocks along the tokens to an item.
+  int block_tokens, block_heads;
+  int token_items, head_items;  // items along the tokens and along the group's heads
+  int item_rows;                // rows of an item
   int direct;       // items are not split
   unsigned long long poll_limit, timeout_ns;
   unsigned int* error_word;

@@ -6,31 +6,39 @@
 // tensor pipe a quarter (128 rows) to a half (256) of that time, so all else has to
 // hide behind the copies.
 //
-// Work: an item is a block of 128 or 256 rows of one (sequence, cached head); its
-// positions are walked in tiles of 128 (tree_span: with a window only those that a
-// row may see).  The tiles of all items form one line, of which every thread block
-// takes an equal share (fat_decode_plan.h); items that blocks share leave normalised
-// parts in the workspace for the join kernel, in a fixed order.
+// Work: an item is a block of up to 128 rows of one (sequence, cached head), or two such
+// blocks where a 16-bit cache has more; its positions are walked in tiles of 128
+// (tree_span: with a window only those that a row may see).  The tiles of all items form
+// one line, of which every thread block takes an equal share (fat_decode_plan.h); items
+// that blocks share leave normalised parts in the workspace for the join kernel, in a
+// fixed order.
 //
-//   warps 0-7   softmax in two groups of four, one row to a thread.  Of 256 rows each
-//               group takes its half at every tile; of up to 128 both have the same rows
-//               and take alternate tiles, with an O and statistics of their own that
-//               are joined at the item's end: no group ever waits for the other inside
-//               an item.  They load Q at an item's start, and write O at its end.
-//   warp 8      MMA issuer: S_g = Q_g K^T (tcgen05, 128 x 128), O_g += P_g V.
-//   warps 9,10  producers of K and V: one TMA box for each page of a tile.
-//   warps 12-19 (e4m3 caches) converters: warp 9 brings the codes and scale bytes to a ring
-//               of their own, and these warps make bf16 rows of them in the rings of K and
-//               V.  A code times a power of two is exact in bf16.  fp16 queries go as two bf16
-//               terms, which hold all their bits, and their weights as two as well.
+//   softmax     two groups of warps.  Of two blocks of rows each group takes one, at every
+//               tile; of one block both have the same rows and take alternate tiles, with
+//               an O and statistics of their own that are joined at the item's end: no group
+//               waits for the other inside an item.  For 16-bit caches a row has two threads,
+//               64 scores each, that share its reference (they vote at every tile whether it
+//               has to be raised).
+//   MMA issuer  S_g = Q_g K^T (tcgen05, 128 x 128), O_g += P_g V.
+//   producers   of K, V and Q: TMA boxes, one for each page of a tile.
+//   converters  (e4m3 caches) one producer brings codes and scale bytes to a ring of their
+//               own; these warps make 16-bit rows of them in the rings of K and V.
 //
 // TMEM: S_0, S_1 (P_g over S_g), O_0, O_1: 512 columns.
 //
 // Per score: z = scale log2(e) s - r with a running reference r for each row, raised to
 // the row's maximum only where a tile exceeds it by more than kRaise binades (then O is
 // rescaled in TMEM: a rare event).  The scores are read twice from TMEM, for the
-// maximum and for the weights: it has the bandwidth, and 128 scores to a thread would
-// need the registers of two.  P is rounded to 16 bits, the sum of the row is not.
+// maximum and for the weights: it has the bandwidth.  P is rounded to 16 bits, the sum of
+// the row is not.
+//
+// e4m3 caches: a code times its row's power of two is an fp16 wherever the scale is
+// within 2^-15 .. 2^7, and always a bf16.  Rows become fp16 (one conversion and one
+// multiplication to two codes), the tiles of V with a scale outside that range bf16, for
+// which the weights of that tile are rounded to bf16 too.  bf16 queries become fp16 times
+// a power of two for the item; where that would lose bits (elements more than 32 binades
+// apart), they stay bf16 and so do the item's keys.  Keys with a scale outside the range
+// stay codes, and the scale multiplies their scores.  So nothing is lost in any of them.
 //
 // What no row sees is zeroed in V's tile, and never fetched where it fills a page; what
 // only some rows see (drafted tokens, a window's border) has its non-finite values
@@ -50,18 +58,27 @@ namespace tree {
 // what a kernel is made for: a 16-bit cache's type, or an e4m3 cache and the queries' type
 constexpr int kBf16 = 0, kF16 = 1, kE4M3Bf16 = 2, kE4M3F16 = 3;
 
-constexpr int kGroupThreads = 128;
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
-constexpr int kConvertWarp = 12, kConvertWarps = 8;
 template <int kType>
-constexpr int kThreadsOf = kType >= kE4M3Bf16 ? 640 : 384;
+constexpr bool kIsE4M3 = kType >= kE4M3Bf16;
+// softmax warps, then the MMA issuer, the producers of K, V and Q (e4m3: one for K and V, the
+// softmax warps load Q), then the converters
+template <int kType>
+constexpr int kHalves = kIsE4M3<kType> ? 1 : 2;  // threads to a row
+template <int kType>
+constexpr int kSoftWarps = 8 * kHalves<kType>;
+constexpr int kConvertWarps = 8;
+template <int kType>
+constexpr int kThreadsOf =
+    32 * (kSoftWarps<kType> + 4 + (kIsE4M3<kType> ? kConvertWarps : 0));
 constexpr uint32_t kTmemCols = 512;
 // binades above the maximum at the last raise that are let pass; fp16 weights are
 // 2^kShift at that maximum (2^15 is the most fp16 holds)
-template <bool kFp16>
-constexpr float kRaise = kFp16 ? 4.f : 8.f;
-template <bool kFp16>
-constexpr float kShift = kFp16 ? 11.f : 0.f;
+template <int kType>
+constexpr float kRaise = kType == kBf16 ? 8.f : 4.f;
+template <int kType>
+constexpr float kShift = kType == kBf16 ? 0.f : 11.f;
+// scale bytes whose rows of codes are exact in fp16: 2^-9 2^-15 is its least step, 448 2^7 < 2^16
+constexpr uint32_t kScaleLow = 112, kScaleHigh = 134;
 
 struct Join {  // what the join kernel needs of the item that starts, unfinished, in a block
   int entry, item;
@@ -80,25 +97,26 @@ __host__ __device__ inline size_t rows_at(int block, int part, int rows, int d) 
 }
 
 struct KernelParams {
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_q;
   TreeParams p;
-  // 0 where all heads, or pages, are the same memory (a stride of 0)
-  int k_head, k_page, v_head, v_page;
+  // 0 where all heads, pages or sequences are the same memory (a stride of 0)
+  int k_head, k_page, v_head, v_page, q_batch;
 };
 
 template <int D, int kType, int kNB>
 struct Layout {
   static constexpr bool kE4M3 = kType >= kE4M3Bf16;
-  static constexpr int kParts = kType == kE4M3F16 ? 2 : 1;  // 16-bit terms of q and of a weight
   static constexpr int kTile = kTreeTile * D * 2;
-  // stages of K and V, and of an e4m3 cache's codes: what the shared memory has room for
-  static constexpr int kKStages = kE4M3 ? 2 : D == 64 ? (kNB == 1 ? 6 : 5) : kNB == 1 ? 3 : 2;
-  static constexpr int kStages = kE4M3 ? 2 : D == 64 ? (kNB == 1 ? 6 : 5) : 3;
-  static constexpr int kRawStages = !kE4M3 ? 0 : D == 64 ? 12 : kParts == 2 ? 2 : 4;
+  // buffers of Q, stages of K and V, and of an e4m3 cache's codes: what the shared memory has
+  // room for
+  static constexpr int kQBufs = !kE4M3 && (kNB == 1 || D == 64) ? 2 : 1;
+  static constexpr int kKStages = kE4M3 || D == 128 ? 2 : kNB == 1 ? 5 : 4;
+  static constexpr int kStages = kE4M3 ? 2 : D == 128 ? 3 : kNB == 1 ? 6 : 5;
+  static constexpr int kRawStages = !kE4M3 ? 0 : D == 64 ? 12 : 4;
   static constexpr int kRawTile = kTreeTile * D;  // codes
   static constexpr int kAtoms = D / 64;  // slabs of 64 columns (128 bytes)
   static constexpr int kQ = 0;
-  static constexpr int kK = kNB * kParts * kTile;
+  static constexpr int kK = kQBufs * kNB * kTile;
   static constexpr int kV = kK + kKStages * kTile;
   static constexpr int kRaw = kV + kStages * kTile;
   static constexpr int kScales = kRaw + kRawStages * kRawTile;  // of the codes' rows
@@ -110,24 +128,29 @@ struct Layout {
   static constexpr int bRawFull = bVEmpty + kStages;
   static constexpr int bRawEmpty = bRawFull + kRawStages;
   static constexpr int bSFull = bRawEmpty + kRawStages;  // [2]
-  static constexpr int bPFull = bSFull + 2;              // [2], 4 arrivals
+  static constexpr int bPFull = bSFull + 2;              // [2], the group's warps
   static constexpr int bPV = bPFull + 2;                 // [2]
-  static constexpr int bQFull = bPV + 2;                 // 8 arrivals
-  static constexpr int bSync = bQFull + 1;               // 8 arrivals: both groups are here
+  static constexpr int bQFull = bPV + 2;                 // [kQBufs]; e4m3: the softmax warps
+  static constexpr int bQFree = bQFull + kQBufs;         // [kQBufs]
+  static constexpr int bSync = bQFree + kQBufs;          // all softmax warps are here
   static constexpr int bDrain = bSync + 1;
   static constexpr int kNumBars = bDrain + 1;
   static __device__ __forceinline__ int arrivals(int bar) {
     if (kE4M3 && ((bar >= bKFull && bar < bKEmpty) || (bar >= bVFull && bar < bVEmpty) ||
                   (bar >= bRawEmpty && bar < bSFull)))
       return kConvertWarps / 2;
-    return bar == bPFull || bar == bPFull + 1 ? 4 : bar == bQFull || bar == bSync ? 8 : 1;
+    if (bar == bPFull || bar == bPFull + 1) return kSoftWarps<kType> / 2;
+    if (bar == bSync || (kE4M3 && bar == bQFull)) return kSoftWarps<kType>;
+    return 1;
   }
   static constexpr int kMisc = kBars + ((8 * kNumBars + 15) & ~15);
-  // u32: TMEM base, abort flag, -, -; DecodePlace; u64 bad[2]
-  static constexpr int kStart = kMisc + 16;
-  static constexpr int kBad = kStart + 16;
-  // float [2 groups][2][128]: reference and sum of each row; ahead of that the plan's sums
-  static constexpr int kFin = kBad + 16;
+  // u32: 0 TMEM base, 1 abort flag; (e4m3) 2 whether the item's queries and keys are bf16, 6 of
+  // V's stages whether they are, 8 the exponents of the item's queries, 20 of the last four tiles
+  // whether their keys are codes; u64 bad[2 parities][2] at 12
+  static constexpr int kBad = kMisc + 48;
+  // float: the references [2 groups][128] and the sums [2][128] of the rows; the threads of a row
+  // exchange their maxima in the latter.  Ahead of that the plan's sums and the first place.
+  static constexpr int kFin = kMisc + 96;
   static constexpr int kBytes = kFin + 2 * 2 * kTreeBlockRows * 4;
   static_assert(kRawStages % 2 == 0, "K's and V's codes in turn");
   static_assert(!kE4M3 || kNB == 1, "one block of rows where the codes need room");
@@ -140,10 +163,12 @@ struct Walk {
   DecodePlace at;
   TreeLens n;
   DecodeSpan span;
-  int lo;     // the first position that any row sees behind the sinks
-  int hi;     // from here on every row sees the context
+  int lo;  // the first position that any row sees behind the sinks
+  int hi;  // from here on every row sees the context
   __device__ __forceinline__ int context() const { return n.len - n.drafted; }
   __device__ __forceinline__ int row() const { return decode_span_tile(span, at.tile) * kTreeTile; }
+  // Nothing was drafted for the sequence: its rows are written, and nothing else is done.
+  __device__ __forceinline__ bool empty() const { return n.drafted == 0; }
 };
 __device__ __forceinline__ void enter(const TreeParams& p, Walk& w) {
   w.n = tree_lens(p, w.at.entry);
@@ -160,11 +185,25 @@ __device__ __forceinline__ void enter(const TreeParams& p, Walk& w) {
 }
 // Whether any row sees any position of [a, b).
 __device__ __forceinline__ bool some_seen(const TreeParams& p, const Walk& w, int a, int b) {
-  return w.n.drafted > 0 && a < w.n.len && (p.window <= 0 || a < p.sinks || b > w.lo);
+  return !w.empty() && a < w.n.len && (p.window <= 0 || a < p.sinks || b > w.lo);
 }
 // Whether all (live) rows see all positions of [a, b).
 __device__ __forceinline__ bool all_seen(const TreeParams& p, const Walk& w, int a, int b) {
   return b <= w.context() && (p.window <= 0 || b <= p.sinks || a >= w.hi);
+}
+
+// An item's rows: the cached head, and the first token and head of the group.
+struct Rows {
+  int head, t0, h0;
+};
+__device__ __forceinline__ Rows rows_of(const TreeParams& p, int item, int blocks) {
+  Rows r;
+  r.head = item / (p.token_items * p.head_items);
+  const int x = item - r.head * p.token_items * p.head_items;
+  const int th = x / p.head_items;
+  r.t0 = th * p.block_tokens * blocks;
+  r.h0 = (x - th * p.head_items) * p.block_heads;
+  return r;
 }
 
 // bits 0 .. n - 1
@@ -184,6 +223,24 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 
 // element c of the row of V at position j; what is out of range reads as 0 (the sequence's
 // results are unspecified then)
@@ -193,7 +250,7 @@ __device__ __forceinline__ float value_at(const TreeParams& p, int b, uint32_t h
   if (page < 0) return 0.f;
   const uint32_t at = j & (p.c.page_size - 1);
   const uint8_t* row = p.c.v + row_offset(page, head, at, p.c.v_page, p.c.v_head, p.c.v_token);
-  if constexpr (kType >= kE4M3Bf16) {
+  if constexpr (kIsE4M3<kType>) {
     uint32_t lo, hi;
     e4m3x4_to_f16(row[c], lo, hi);
     return unpack16<false>(lo).x * scale_value(p.c.v_scale[scale_offset(p.c, page, head, at)]);
@@ -226,10 +283,11 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     tree_kernel(const __grid_constant__ KernelParams kp) {
   using L = Layout<D, kType, kNB>;
   constexpr int kThreads = kThreadsOf<kType>, kWarps = kThreads / 32;
-  constexpr bool kFp16 = kType == kF16;  // the products' operands
+  constexpr bool kE4M3 = L::kE4M3, kFp16 = kType != kBf16;
   constexpr bool kOutBf16 = kType == kBf16 || kType == kE4M3Bf16;
-  constexpr int kParts = L::kParts;
-  constexpr int kCh = L::kE4M3 ? 1 : 2;  // times 32 scores in registers at a time
+  constexpr int kH = kHalves<kType>, kSoft = kSoftWarps<kType>;
+  constexpr int kMmaWarp = kSoft, kKWarp = kSoft + 1, kVWarp = kSoft + 2, kQWarp = kSoft + 3,
+                kConvertWarp = kSoft + 4;
   constexpr int SK = L::kKStages, SV = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = kp.p;
@@ -237,9 +295,10 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   volatile uint32_t* abort_flag = misc + 1;
-  DecodePlace* start_s = reinterpret_cast<DecodePlace*>(smem + L::kStart);
-  unsigned long long* bad = reinterpret_cast<unsigned long long*>(smem + L::kBad);
+  // what some rows see and is not finite: drafted tokens and border positions, by item parity
+  unsigned long long* bad_s = reinterpret_cast<unsigned long long*>(smem + L::kBad);
   float* fin = reinterpret_cast<float*>(smem + L::kFin);
+  DecodePlace* start_s = reinterpret_cast<DecodePlace*>(fin + 2 * kTreeBlockRows);
   auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8 * i; };
   auto wait = [&](int i, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait_bounded(bar(i), parity, p, abort_flag));
@@ -251,8 +310,22 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     return;
   }
 
-  // ---- the block's share of the line of tiles ----
-  const int copies = p.c.heads * p.row_blocks;
+  // ---- set-up, and the block's share of the line of tiles ----
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), L::arrivals(i));
+      misc[1] = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(sb + L::kMisc, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kKWarp && lane == 0) {
+    tma_prefetch_desc(&kp.tm_k);
+    tma_prefetch_desc(&kp.tm_v);
+    if (!kE4M3) tma_prefetch_desc(&kp.tm_q);
+  }
+  const int copies = p.c.heads * p.token_items * p.head_items;
   long long begin, share, total;
   if (p.direct) {
     const int e = blockIdx.x / copies;
@@ -275,7 +348,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     total = 0;
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) upto += sums[w];
       total += sums[w];
@@ -300,42 +373,33 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   }
   Join* joins = reinterpret_cast<Join*>(p.workspace);
   if (!p.direct && threadIdx.x == 0) joins[blockIdx.x].last = -1;
-  if (begin >= total) return;
-  const int count = static_cast<int>(min(total, begin + share) - begin);
-
-  // ---- set-up ----
-  if (threadIdx.x == kMmaWarp * 32) {
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), L::arrivals(i));
-    misc[1] = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tmem_alloc(sb + L::kMisc, kTmemCols);
-    tmem_relinquish();
-  }
+  // (0: more blocks than tiles)
+  const int count = begin < total ? static_cast<int>(min(total, begin + share) - begin) : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
   Walk w;
-  w.at = *start_s;
-  enter(p, w);
+  const bool works = count > 0 && (warp <= kVWarp || (warp == kQWarp && !kE4M3) ||
+                                   (kE4M3 && warp >= kConvertWarp));
+  if (works) {
+    w.at = *start_s;
+    enter(p, w);
+  }
 
-  if (warp == kKWarp || (warp == kVWarp && !L::kE4M3)) {
-    // =================== producers ===================
+  if (!works) {
+  } else if (warp == kKWarp || (warp == kVWarp && !kE4M3)) {
+    // =================== producers of K and V ===================
     // (e4m3: one for both, K and V of a tile in turn)
-    constexpr int kTurns = L::kE4M3 ? 2 : 1;
+    constexpr int kTurns = kE4M3 ? 2 : 1;
     const bool k_warp = warp == kKWarp;
-    const int S = L::kE4M3 ? L::kRawStages : k_warp ? SK : SV;
-    const int full = L::kE4M3 ? L::bRawFull : k_warp ? L::bKFull : L::bVFull;
-    const int empty = L::kE4M3 ? L::bRawEmpty : k_warp ? L::bKEmpty : L::bVEmpty;
-    const uint32_t ring = sb + (L::kE4M3 ? L::kRaw : k_warp ? L::kK : L::kV);
+    const int S = kE4M3 ? L::kRawStages : k_warp ? SK : SV;
+    const int full = kE4M3 ? L::bRawFull : k_warp ? L::bKFull : L::bVFull;
+    const int empty = kE4M3 ? L::bRawEmpty : k_warp ? L::bKEmpty : L::bVEmpty;
+    const uint32_t ring = sb + (kE4M3 ? L::kRaw : k_warp ? L::kK : L::kV);
     const int rows = min(p.c.page_size, kTreeTile);  // of a box
     const int boxes = kTreeTile / rows;              // to a tile, each of a page
-    const uint32_t box_bytes = rows * (L::kE4M3 ? D : 128u);
-    if (lane == 0 && k_warp) tma_prefetch_desc(&kp.tm_k);
-    if (lane == 0 && (L::kE4M3 || !k_warp)) tma_prefetch_desc(&kp.tm_v);
+    const uint32_t box_bytes = rows * (kE4M3 ? D : 128u);
     // Pages of 32 / boxes tiles from `window`, one box to a lane, loaded well before their use.
     const int per = 32 / boxes;
     int window = 0, window_page = 0;
@@ -354,46 +418,49 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     int issued = 0;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-      const int head = w.at.item / p.row_blocks;
-      const int page = __shfl_sync(0xffffffffu, window_page,
-                                   (w.at.tile - window) * boxes + lane % boxes);
-      const int a = w.row() + lane % boxes * rows;
-      bool mine = lane < boxes && some_seen(p, w, a, a + rows);
-      if (mine && static_cast<uint32_t>(page) >= p.c.num_pages) {
-        atomicOr(p.t.error_word, kErrIndex);
-        mine = false;  // no address is made of it
-      }
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-      const int place = a & (p.c.page_size - 1);
-#pragma unroll
-      for (int turn = 0; turn < kTurns; ++turn) {
-        const bool is_k = L::kE4M3 ? turn == 0 : k_warp;
-        const CUtensorMap* tm = is_k ? &kp.tm_k : &kp.tm_v;
-        const int c2 = head * (is_k ? kp.k_head : kp.v_head);
-        const int c3 = page * (is_k ? kp.k_page : kp.v_page);
-        if (!(ok = wait(empty + slot, phase ^ 1u))) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar(full + slot),
-                                n * (L::kE4M3 ? box_bytes + rows : box_bytes * L::kAtoms));
-        __syncwarp();
-        if (mine) {
-          if constexpr (L::kE4M3) {
-            const uint32_t to = ring + slot * L::kRawTile;
-            tma_load_4d(to + lane * box_bytes, tm, bar(full + slot), 0, place, c2, c3);
-            bulk_load(sb + L::kScales + slot * kTreeTile + lane * rows,
-                      (is_k ? p.c.k_scale : p.c.v_scale) + scale_offset(p.c, page, head, place),
-                      rows, bar(full + slot));
-          } else {
-            const uint32_t to = ring + slot * L::kTile + lane * box_bytes;
-#pragma unroll
-            for (int x = 0; x < L::kAtoms; ++x)
-              tma_load_4d(to + x * (kTreeTile * 128), tm, bar(full + slot), x * 64, place, c2, c3);
-          }
+      if (!w.empty()) {
+        const int head = w.at.item / (p.token_items * p.head_items);
+        const int page = __shfl_sync(0xffffffffu, window_page,
+                                     (w.at.tile - window) * boxes + lane % boxes);
+        const int a = w.row() + lane % boxes * rows;
+        bool mine = lane < boxes && some_seen(p, w, a, a + rows);
+        if (mine && static_cast<uint32_t>(page) >= p.c.num_pages) {
+          atomicOr(p.t.error_word, kErrIndex);
+          mine = false;  // no address is made of it
         }
-        ++issued;
-        if (++slot == S) slot = 0, phase ^= 1u;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+        const int place = a & (p.c.page_size - 1);
+#pragma unroll
+        for (int turn = 0; turn < kTurns; ++turn) {
+          const bool is_k = kE4M3 ? turn == 0 : k_warp;
+          const CUtensorMap* tm = is_k ? &kp.tm_k : &kp.tm_v;
+          const int c2 = head * (is_k ? kp.k_head : kp.v_head);
+          const int c3 = page * (is_k ? kp.k_page : kp.v_page);
+          if (!(ok = wait(empty + slot, phase ^ 1u))) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(full + slot),
+                                  n * (kE4M3 ? box_bytes + rows : box_bytes * L::kAtoms));
+          __syncwarp();
+          if (mine) {
+            if constexpr (kE4M3) {
+              tma_load_4d(ring + slot * L::kRawTile + lane * box_bytes, tm, bar(full + slot), 0,
+                          place, c2, c3);
+              bulk_load(sb + L::kScales + slot * kTreeTile + lane * rows,
+                        (is_k ? p.c.k_scale : p.c.v_scale) + scale_offset(p.c, page, head, place),
+                        rows, bar(full + slot));
+            } else {
+              const uint32_t to = ring + slot * L::kTile + lane * box_bytes;
+#pragma unroll
+              for (int x = 0; x < L::kAtoms; ++x)
+                tma_load_4d(to + x * (kTreeTile * 128), tm, bar(full + slot), x * 64, place, c2,
+                            c3);
+            }
+          }
+          ++issued;
+          if (++slot == S) slot = 0, phase ^= 1u;
+        }
+        if (!ok) break;
       }
-      if (!ok) break;
       if (i + 1 < count) {
         if (decode_advance(w.at, copies)) enter(p, w);
         if (w.at.tile == 0 || w.at.tile == window + per) load_window();
@@ -403,31 +470,65 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       for (int x = max(0, issued - S); x < issued; ++x) wait_drain(bar(full + x % S), (x / S) & 1);
     }
     __syncwarp();
+  } else if (!kE4M3 && warp == kQWarp) {
+    // =================== producer of Q ===================
+    const uint32_t block_bytes = p.block_tokens * p.block_heads * 128u;
+    bool ok = true;
+    int items = 0;
+#pragma unroll 1
+    for (int i = 0; i < count;) {
+      if (!w.empty()) {
+        const Rows r = rows_of(p, w.at.item, kNB);
+        const int buf = items % L::kQBufs;
+        if (!(ok = wait(L::bQFree + buf, (items / L::kQBufs & 1) ^ 1u))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::bQFull + buf), kNB * L::kAtoms * block_bytes);
+#pragma unroll
+          for (int x = 0; x < kNB; ++x)
+#pragma unroll
+            for (int y = 0; y < L::kAtoms; ++y)
+              tma_load_4d(sb + L::kQ + (buf * kNB + x) * L::kTile + y * (kTreeTile * 128),
+                          &kp.tm_q, bar(L::bQFull + buf), y * 64, r.head * p.group + r.h0,
+                          r.t0 + x * p.block_tokens, w.at.entry * kp.q_batch);
+        }
+        __syncwarp();
+        ++items;
+      }
+      i += w.at.tiles - w.at.tile;
+      if (i < count) {
+        w.at.tile = w.at.tiles - 1;
+        if (decode_advance(w.at, copies)) enter(p, w);
+      }
+    }
+    if (!ok) {
+      for (int x = max(0, items - L::kQBufs); x < items; ++x)
+        wait_drain(bar(L::bQFull + x % L::kQBufs), (x / L::kQBufs) & 1);
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // =================== MMA issuer ===================
-    constexpr uint32_t kFmt = kFp16 ? 0u : 1u;
-    constexpr uint32_t idesc_s = idesc_f32acc<kFmt>(kTreeBlockRows, kTreeTile, false);
-    constexpr uint32_t idesc_pv = idesc_f32acc<kFmt>(kTreeBlockRows, D, true);
+    // (A/B formats: bf16 1, fp16 0; an e4m3 cache's by the item and the tile)
+    constexpr uint32_t kFmt = kFp16 ? 0u : 1u, kFmtBits = (1u << 7) | (1u << 10);
+    constexpr uint32_t kIdescS = idesc_f32acc<kFmt>(kTreeBlockRows, kTreeTile, false);
+    constexpr uint32_t kIdescPV = idesc_f32acc<kFmt>(kTreeBlockRows, D, true);
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kV, kTreeTile * 128, 1024);
     int k_slot = 0, v_slot = 0, items = 0;
     uint32_t k_phase = 0, v_phase = 0, p_phase[2] = {0, 0};
+    uint32_t idesc_s = kIdescS;
     bool ok = true;
-    auto issue_s = [&](int g) -> bool {
+    auto issue_s = [&](int g, int buf) -> bool {
       if (kNB == 1 || g == 0) {
         if (!wait(L::bKFull + k_slot, k_phase)) return false;
       }
       tc_fence_after();
       const uint64_t kd = k_desc + static_cast<uint32_t>((k_slot * L::kTile) >> 4);
-      const uint64_t qd = q_desc + static_cast<uint32_t>((kNB == 2 ? g * L::kTile : 0) >> 4);
+      const uint64_t qd =
+          q_desc + static_cast<uint32_t>(((buf * kNB + (kNB == 2 ? g : 0)) * L::kTile) >> 4);
 #pragma unroll
-      for (int part = 0; part < kParts; ++part)
-#pragma unroll
-        for (int x = 0; x < L::kAtoms; ++x)
-          mma_ss_x4<false, 2>(tmem + g * kTreeTile,
-                              qd + static_cast<uint32_t>((part * L::kTile) >> 4) + x * 1024,
-                              kd + x * 1024, idesc_s, part + x > 0);
+      for (int x = 0; x < L::kAtoms; ++x)
+        mma_ss_x4<false, 2>(tmem + g * kTreeTile, qd + x * 1024, kd + x * 1024, idesc_s, x > 0);
       mma_commit(bar(L::bSFull + g));
       if (kNB == 1 || g == 1) {
         mma_commit(bar(L::bKEmpty + k_slot));
@@ -443,19 +544,20 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       p_phase[g] ^= 1u;
       tc_fence_after();
       const uint64_t vd = v_desc + static_cast<uint32_t>((v_slot * L::kTile) >> 4);
-      if constexpr (kParts == 1) {
+      if (kE4M3 && misc[6 + v_slot]) {  // bf16, the weights as two terms 16 columns apart
+#pragma unroll 1
+        for (int x = 0; x < kTreeTile / 16; ++x)
 #pragma unroll
-        for (int x = 0; x < kTreeTile / 64; ++x)  // 64 positions: 32 columns of P, 64 rows of V
-          mma_ts_x4<false, 8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 32,
-                                   vd + static_cast<uint32_t>(x * 512), idesc_pv, acc || x > 0);
+          for (int term = 0; term < 2; ++term)
+            mma_ts<false>(tmem + 256 + g * 128,
+                          tmem + g * kTreeTile + x / 2 * 32 + x % 2 * 8 + term * 16,
+                          vd + static_cast<uint32_t>(x * 128), kIdescPV | kFmtBits,
+                          acc || x + term > 0);
       } else {
 #pragma unroll
-        for (int x = 0; x < kTreeTile / 16; ++x)  // 16 positions: both terms, 16 columns apart
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-            mma_ts<false>(tmem + 256 + g * 128,
-                          tmem + g * kTreeTile + x / 2 * 32 + x % 2 * 8 + part * 16,
-                          vd + static_cast<uint32_t>(x * 128), idesc_pv, acc || x + part > 0);
+        for (int x = 0; x < kTreeTile / 64; ++x)  // 64 positions: 32 columns of P, 64 rows of V
+          mma_ts_x4<false, 8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 64,
+                                   vd + static_cast<uint32_t>(x * 512), kIdescPV, acc || x > 0);
       }
       mma_commit(bar(L::bPV + g));
       if (kNB == 1 || g == 1) {
@@ -464,20 +566,26 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       }
       return true;
     };
-    int i = 0;
 #pragma unroll 1
-    while (ok && i < count) {
+    for (int i = 0; ok && i < count;) {
       const int tiles = min(count - i, w.at.tiles - w.at.tile);
-      const int units = tiles * kNB;
-      if (!(ok = wait(L::bQFull, items & 1))) break;
-      ++items;
-      ok = issue_s(0);
-      if (ok && units > 1) ok = issue_s(1);
+      if (!w.empty()) {
+        const int units = tiles * kNB, buf = items % L::kQBufs;
+        if (!(ok = wait(L::bQFull + buf, items / L::kQBufs & 1))) break;
+        ++items;
+        if constexpr (kE4M3) idesc_s = kIdescS | (misc[2] ? kFmtBits : 0u);
+        ok = issue_s(0, buf);
+        if (ok && units > 1) ok = issue_s(1, buf);
+        if (ok && units <= 2) mma_commit(bar(L::bQFree + buf));
 #pragma unroll 1
-      for (int u = 0; ok && u < units; ++u) {
-        const int g = u & 1;
-        if (!(ok = issue_pv(g, u > 1))) break;
-        if (u + 2 < units) ok = issue_s(g);
+        for (int u = 0; ok && u < units; ++u) {
+          const int g = u & 1;
+          if (!(ok = issue_pv(g, u > 1))) break;
+          if (u + 2 < units) {
+            ok = issue_s(g, buf);
+            if (u + 3 == units) mma_commit(bar(L::bQFree + buf));
+          }
+        }
       }
       i += tiles;
       if (i < count) {
@@ -489,7 +597,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     mma_commit(bar(L::bDrain));
     wait_drain(bar(L::bDrain), 0);
     __syncwarp();
-  } else if (L::kE4M3 && warp >= kConvertWarp) {
+  } else if (kE4M3 && warp >= kConvertWarp) {
     // =================== converters ===================
     // Half of the warps take K's tiles, half V's: 32 rows of a tile to a warp, 16 codes to a
     // lane at a time, four of those with their loads ahead of the arithmetic.
@@ -504,79 +612,86 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     // neither here nor in the tile that is written.
     const int group = lane / 4;
     const int my_row = D == 64 ? group : (group / 2) ^ (group % 2 * 5);
-    int raw = is_v ? 1 : 0, slot = 0;
+    int raw = is_v ? 1 : 0, slot = 0, items = 0;
     uint32_t raw_phase = 0, phase = 0;
-    bool ok = true;
+    bool ok = true, wide = false;
+    int tile_count = 0;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-      const uint32_t from = sb + L::kRaw + raw * L::kRawTile;
-      const uint32_t scales = sb + L::kScales + raw * kTreeTile;
-      const uint32_t to = ring + slot * L::kTile;
-      if (!(ok = wait(L::bRawFull + raw, raw_phase))) break;
-      if (!(ok = wait(empty + slot, phase ^ 1u))) break;
-#pragma unroll 1
-      for (int x = 0; x < kC; x += kEach) {  // kC pieces of eight rows and 64 codes
-        uint32_t in[kEach][4], e[kEach];
-#pragma unroll
-        for (int y = 0; y < kEach; ++y) {
-          const int row = row0 + (x + y) % 4 * 8 + my_row;
-          const int c = (x + y) / 4 * 4 + lane % 4;
-          const float4 v =
-              ld_shared_v4(from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16);
-          in[y][0] = __float_as_uint(v.x), in[y][1] = __float_as_uint(v.y);
-          in[y][2] = __float_as_uint(v.z), in[y][3] = __float_as_uint(v.w);
-          asm volatile("ld.shared.u8 %0, [%1];"
-                       : "=r"(e[y])
-                       : "r"(scales + row)
-                       : "memory");
-        }
-        // A code's sign and seven other bits in the places of a bf16's sign, low exponent and
-        // high mantissa are the value times 2^-120, subnormal codes included; one
-        // multiplication by 2^(120 + e - 127) makes it right, and NaN of a row that is one.
-        // Codes that are NaN and scales that bf16 has not take the slow way.
-        uint32_t out[kEach][8];
-        bool slow = false;
-#pragma unroll
-        for (int y = 0; y < kEach; ++y) {
-          uint32_t nan = 0;
-          const uint32_t s2 = e[y] == 255u ? 0x7FFF7FFFu : ((e[y] + 120u) << 7) * 0x00010001u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            nan |= (in[y][k] & 0x7F7F7F7Fu) + 0x01010101u;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t w = __byte_perm(in[y][k], 0u, z ? 0x3424 : 0x1404);
-              out[y][2 * k + z] = mul_bf16x2(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u), s2);
-            }
+      if (!w.empty()) {
+        if (i == 0 || w.at.tile == 0) {  // the item's keys follow its queries' type
+          if (!is_v) {
+            if (!(ok = wait(L::bQFull, items & 1))) break;
+            wide = misc[2] != 0;
           }
-          slow |= (nan & 0x80808080u) != 0 || (e[y] >= 135u && e[y] < 255u);
+          ++items;
         }
-        if (slow) {
+        const uint32_t from = sb + L::kRaw + raw * L::kRawTile;
+        const uint32_t scales = sb + L::kScales + raw * kTreeTile;
+        const uint32_t to = ring + slot * L::kTile;
+        if (!(ok = wait(L::bRawFull + raw, raw_phase))) break;
+        if (!(ok = wait(empty + slot, phase ^ 1u))) break;
+        // whether a row that is seen has a scale that fp16 has not: the byte of a NaN row, 255, is
+        // NaN in either type
+        bool out_of_range = false;
+        {
+          const uint32_t four = ld_shared_u32(scales + 4 * lane);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t e = four >> (8 * y) & 255u;
+            const int j = w.row() + 4 * lane + y;
+            out_of_range |=
+                some_seen(p, w, j, j + 1) && e != 255u && (e < kScaleLow || e > kScaleHigh);
+          }
+          out_of_range = __any_sync(0xffffffffu, out_of_range);
+          // (of V's stage; of K's tile, four deep: the softmax of a tile is over once the scores
+          // of the next but one of its group are under way)
+          if (row0 == 0 && lane == 0)
+            misc[is_v ? 6 + slot : 20 + tile_count % 4] = out_of_range && (is_v || !wide) ? 1u : 0u;
+          ++tile_count;
+        }
+        const bool as_bf16 = is_v ? out_of_range : wide;
+        const bool as_codes = !is_v && !wide && out_of_range;
 #pragma unroll 1
+        for (int x = 0; x < kC; x += kEach) {  // kC pieces of eight rows and 64 codes
+          uint32_t in[kEach][4], e[kEach];
+#pragma unroll
           for (int y = 0; y < kEach; ++y) {
             const int row = row0 + (x + y) % 4 * 8 + my_row;
             const int c = (x + y) / 4 * 4 + lane % 4;
-            const uint32_t line = to + (c / 4) * (kTreeTile * 128) + row * 128;
-            const uint32_t codes = from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16;
-            uint32_t eb;
-            asm volatile("ld.shared.u8 %0, [%1];"
-                         : "=r"(eb)
-                         : "r"(scales + row)
-                         : "memory");
-            const float scale = scale_value(eb);
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {  // pairs
-              uint32_t w, lo, hi;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(codes + k / 2 * 4) : "memory");
-              e4m3x4_to_f16(w, lo, hi);
-              const float2 f = unpack16<false>(k % 2 ? hi : lo);
-              const uint32_t at = line + ((2 * c + k / 4) % 8 ^ (row & 7)) * 16 + k % 4 * 4;
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at),
-                           "r"(pack16<true>(f.x * scale, f.y * scale))
-                           : "memory");
+            const float4 v = ld_shared_v4(from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16);
+            in[y][0] = __float_as_uint(v.x), in[y][1] = __float_as_uint(v.y);
+            in[y][2] = __float_as_uint(v.z), in[y][3] = __float_as_uint(v.w);
+            e[y] = ld_shared_u8(scales + row);
+          }
+          uint32_t out[kEach][8];
+#pragma unroll
+          for (int y = 0; y < kEach; ++y)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(in[y][k], out[y][2 * k], out[y][2 * k + 1]);
+          if (!as_bf16) {
+            // 2^(e - 127) in fp16: down to its subnormals
+#pragma unroll
+            for (int y = 0; y < kEach; ++y) {
+              uint32_t s = as_codes            ? 0x3C00u
+                           : e[y] == 255u      ? 0x7FFFu
+                           : e[y] < 113u       ? 0x0400u >> min(113u - e[y], 31u)
+                                               : (e[y] - 112u) << 10;
+              s = (s & 0x7FFFu) * 0x00010001u;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) out[y][k] = mul_f16x2(out[y][k], s);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < kEach; ++y) {
+              const float s = scale_value(e[y]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float2 f = unpack16<false>(out[y][k]);
+                out[y][k] = pack16<true>(f.x * s, f.y * s);
+              }
             }
           }
-        } else {
 #pragma unroll
           for (int y = 0; y < kEach; ++y) {
             const int row = row0 + (x + y) % 4 * 8 + my_row;
@@ -588,34 +703,41 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                             out[y][4 * z + 1], out[y][4 * z + 2], out[y][4 * z + 3]);
           }
         }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(full + slot));
+          mbar_arrive(bar(L::bRawEmpty + raw));
+        }
+        if ((raw += 2) >= L::kRawStages) raw -= L::kRawStages, raw_phase ^= 1u;
+        if (++slot == S) slot = 0, phase ^= 1u;
       }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(full + slot));
-        mbar_arrive(bar(L::bRawEmpty + raw));
-      }
-      if ((raw += 2) >= L::kRawStages) raw -= L::kRawStages, raw_phase ^= 1u;
-      if (++slot == S) slot = 0, phase ^= 1u;
+      if (i + 1 < count && decode_advance(w.at, copies)) enter(p, w);
     }
     __syncwarp();
-  } else if (warp < kMmaWarp) {
+  } else if (warp < kSoft) {
     // =================== softmax ===================
-    const int g = warp / 4, quarter = warp % 4;
+    const int g = warp / (kSoft / 2), half = kH == 2 ? warp / 4 % 2 : 0, quarter = warp % 4;
     const int r = quarter * 32 + lane;  // TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_at = tmem + lanes + g * kTreeTile;
+    constexpr int kScores = kTreeTile / kH;  // of a thread
+    const uint32_t s_at = tmem + lanes + g * kTreeTile + half * kScores;
     const uint32_t o_at = tmem + lanes + 256 + g * 128;
-    const int all_rows = p.tokens * p.group;
-    uint32_t s_phase = 0;   // of bSFull[g] and bPV[g]: both complete once for each tile of the group
+    const uint32_t pair = 1 + g * 4 + quarter;  // named barrier of the warps that share rows
+    constexpr uint32_t kNan = 0x7FFFFFFFu;
+    float* refs = fin;                         // [2 groups][128]
+    float* sums = fin + 2 * kTreeBlockRows;    // [2 groups][128]
+    float* mine_s = sums + g * kTreeBlockRows + r;
+    uint32_t s_phase = 0;  // of bSFull[g] and bPV[g]: both complete once for each tile of the group
     uint32_t sync_phase = 0;
-    int v_slot = 0;
+    int tile_count = 0, v_slot = 0, parity = 0;
     uint32_t v_phase = 0;
-    auto step_v = [&]() {
+    auto step = [&]() {
       if (++v_slot == SV) v_slot = 0, v_phase ^= 1u;
+      ++tile_count;
     };
-    // both groups are here (and what they wrote to shared memory before is seen)
-    auto sync_groups = [&]() -> bool {
+    // all softmax warps are here (and what they wrote to shared memory before is seen)
+    auto sync_all = [&]() -> bool {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::bSync));
@@ -627,169 +749,258 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     int i = 0;
     long long first_tile = begin - w.at.tile;  // of the current item, on the line
     bool ok = true;
+    if (threadIdx.x < 4) bad_s[threadIdx.x] = 0;
+    if (kE4M3 && threadIdx.x < 4) misc[8 + threadIdx.x] = 0;
+    if (kE4M3 && threadIdx.x == 0) misc[2] = 0;
+    ok = sync_all();
 #pragma unroll 1
     while (ok && i < count) {
       const int tiles = min(count - i, w.at.tiles - w.at.tile);
-      const int head = w.at.item / p.row_blocks;
-      const int row0 = (w.at.item - head * p.row_blocks) * p.item_rows;
-      const int rows = min(p.item_rows, all_rows - row0);
+      const Rows at0 = rows_of(p, w.at.item, kNB);
       const int b = w.at.entry;
-      // ---- Q of the item: rows of 128-byte slabs, chunks of 16 bytes permuted by the row ----
-      {
-        constexpr int kChunks = D / 8;
-        for (int x = threadIdx.x; x < rows * kChunks; x += 2 * kGroupThreads) {
-          const int row = x / kChunks, c = x % kChunks;
-          const int t = (row0 + row) / p.group, h = (row0 + row) - t * p.group;
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                                    p.q + wide(b, p.q_batch) + wide(t, p.q_token) +
-                                    wide(head * p.group + h, p.q_head)) +
-                                c);
-          const int rr = row % kTreeBlockRows;
-          const uint32_t to = sb + L::kQ + (row / kTreeBlockRows) * L::kTile +
-                              (c / 8) * (kTreeTile * 128) + rr * 128 + ((c % 8) ^ (rr & 7)) * 16;
-          if constexpr (kParts == 1) {
-            st_shared_v4u(to, v.x, v.y, v.z, v.w);
-          } else {  // fp16 as a bf16 term and the rest: no bit is lost
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = unpack16<false>(in[k]);
-              hi[k] = pack16<true>(f.x, f.y);
-              const float2 h = unpack16<true>(hi[k]);
-              lo[k] = pack16<true>(f.x - h.x, f.y - h.y);
-            }
-            st_shared_v4u(to, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4u(to + L::kTile, lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        if (threadIdx.x < 2) bad[threadIdx.x] = 0;
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bQFull));
-      }
+      unsigned long long* bad = bad_s + 2 * parity;
       // ---- this thread's row ----
-      const int my_row = (kNB == 2 ? g * kTreeBlockRows : 0) + r;  // within the item
-      const int t = (row0 + my_row) / p.group;
-      const bool live = my_row < rows && t < w.n.drafted;
-      const bool warp_live = (kNB == 2 ? g * kTreeBlockRows : 0) + quarter * 32 < rows;
+      const int block_rows = p.block_tokens * p.block_heads;
+      const int t_in = r / p.block_heads, h_in = r - t_in * p.block_heads;
+      const int t = at0.t0 + (kNB == 2 ? g * p.block_tokens : 0) + t_in, h = at0.h0 + h_in;
+      const bool there = r < block_rows && t < p.tokens && h < p.group;
+      const bool live = there && t < w.n.drafted;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int my_row = (kNB == 2 ? g * block_rows : 0) + r;  // within the item
       const int context = w.context();
+      float scale = p.scale_log2;
+      if constexpr (kE4M3) {
+        // ---- Q: rows of 128-byte slabs, chunks of 16 bytes permuted by the row ----
+        if (!w.empty()) {
+          constexpr int kChunks = D / 8, kMost = kTreeBlockRows * kChunks / (32 * kSoft);
+          uint4 v[kMost];
+          uint32_t most = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+          for (int y = 0; y < kMost; ++y) {
+            const int x = threadIdx.x + y * 32 * kSoft;
+            const int row = x / kChunks, c = x % kChunks;
+            const int qt = row / p.block_heads, qh = row - qt * p.block_heads;
+            v[y] = make_uint4(0, 0, 0, 0);
+            if (row < block_rows && at0.t0 + qt < w.n.drafted && at0.h0 + qh < p.group)
+              v[y] = __ldg(reinterpret_cast<const uint4*>(
+                               p.q + wide(b, p.q_batch) + wide(at0.t0 + qt, p.q_token) +
+                               wide(at0.head * p.group + at0.h0 + qh, p.q_head)) +
+                           c);
+            if constexpr (kOutBf16) {
+              const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                // magnitudes compare as integers, two at a time: the largest, and the least but
+                // zero, less 1; infinities and NaN are what they are at any scale
+                uint32_t m = in[k] & 0x7FFF7FFFu;
+                if ((m & 0x7F80u) == 0x7F80u) m &= 0xFFFF0000u;
+                if ((m >> 16 & 0x7F80u) == 0x7F80u) m &= 0xFFFFu;
+                most = __vmaxu2(most, m);
+                least = __vminu2(least, __vsub2(m, 0x00010001u));
+              }
+            }
+          }
+          uint32_t up = 127u;  // the exponent byte of the power of two that q is multiplied by
+          bool keep = false;   // q stays bf16
+          if constexpr (kOutBf16) {
+            most = __reduce_max_sync(0xffffffffu, max(most >> 16, most & 0xFFFFu));
+            least = __reduce_min_sync(0xffffffffu, min(least >> 16, least & 0xFFFFu));
+            if (lane == 0) {
+              atomicMax(const_cast<uint32_t*>(misc + 8 + 2 * parity), most);
+              atomicMax(const_cast<uint32_t*>(misc + 9 + 2 * parity), 0xFFFFu - least);
+            }
+            if (!(ok = sync_all())) break;
+            most = misc[8 + 2 * parity] >> 7;  // exponent bytes
+            least = (0xFFFFu - misc[9 + 2 * parity] + 1u) >> 7;
+            // The largest magnitude goes into [2^14, 2^15): an element keeps all its bits down
+            // to 2^-31 of it, as bits of 2^-24 and above.
+            keep = least + 31u < most || most < 15u;
+            if (threadIdx.x == 0) misc[2] = keep ? 1u : 0u;
+            if (!keep) up = 127u + 141u - most;
+            scale = p.scale_log2 * __uint_as_float((254u - up) << 23);
+          }
+          const float f = __uint_as_float(up << 23);
+#pragma unroll
+          for (int y = 0; y < kMost; ++y) {
+            const int x = threadIdx.x + y * 32 * kSoft;
+            const int row = x / kChunks, c = x % kChunks;
+            uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+            if (kOutBf16 && !keep) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 q2 = unpack16<true>(in[k]);
+                in[k] = pack16<false>(q2.x * f, q2.y * f);
+              }
+            }
+            st_shared_v4u(sb + L::kQ + (c / 8) * (kTreeTile * 128) + row * 128 +
+                              ((c % 8) ^ (row & 7)) * 16,
+                          in[0], in[1], in[2], in[3]);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::bQFull));
+        }
+      }
       TreeRow seen;
       seen.mask = 0;
       seen.lo = 0;
       if (live) seen = tree_row(p, w.n, b, t);
       float ref = 0.f, limit = -INFINITY, sum = 0.f;
-      int mine = 0;  // tiles of this group so far in this item
-      int local = 0;
+      int mine = 0;       // tiles of this group so far in this item
+      bool dead = false;  // a wait ran out; the warps of a row leave the loop together
 #pragma unroll 1
-      for (; local < tiles; ++local, ++w.at.tile) {
+      for (int local = 0; local < tiles && !w.empty(); ++local, ++w.at.tile) {
         if (kNB == 1 && (local & 1) != g) {
-          step_v();
+          step();
           continue;
         }
         const int pos0 = w.row();
         const bool whole_tile = all_seen(p, w, pos0, pos0 + kTreeTile);
-        if (!(ok = wait(L::bSFull + g, s_phase))) break;
+        if (!wait(L::bSFull + g, s_phase)) dead = true;
         tc_fence_after();
-        if (warp_live) {
-          float top = -INFINITY;
+        float top = -INFINITY;
+        if (warp_live && !dead) {
+          const bool codes = kE4M3 && misc[20 + tile_count % 4] != 0;
 #pragma unroll 1  // (little code: what an item's end runs must not be fetched anew each time)
-          for (int k = 0; k < 4; k += kCh) {
-            uint32_t s[kCh][32];
-#pragma unroll
-            for (int y = 0; y < kCh; ++y) tmem_ld32(s_at + 32 * (k + y), s[y]);
-#pragma unroll
-            for (int y = 0; y < kCh; ++y) tmem_wait_ld(s[y]);
-            if (!whole_tile) {  // what the row does not see becomes -inf, for the second pass too
-#pragma unroll
-              for (int y = 0; y < kCh; ++y) {
-                const int base = pos0 + 32 * (k + y);
-                uint32_t m = below(context - base);
-                if (p.window > 0) m &= below(p.sinks - base) | ~below(seen.lo - base);
-                const int shift = context - base;  // bit of the first drafted token
-                m |= shift >= 32 || shift <= -64 ? 0u
-                     : shift >= 0               ? static_cast<uint32_t>(seen.mask << shift)
-                                                : static_cast<uint32_t>(seen.mask >> -shift);
-                if (!live) m = 0;
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if (!(m >> x & 1u)) s[y][x] = 0xFF800000u;
-                tmem_st32(s_at + 32 * (k + y), s[y]);
+          for (int k = 0; k < kScores / 32; ++k) {
+            uint32_t s[32];
+            tmem_ld32(s_at + 32 * k, s);
+            tmem_wait_ld(s);
+            if (kE4M3 && codes) {  // (hardly ever) keys whose scales fp16 does not hold
+              const int j = pos0 + 32 * k + lane;
+              float f = 1.f;
+              if (some_seen(p, w, j, j + 1)) {
+                const int page = table_page(p.t, p.c.num_pages, b, j >> p.c.page_shift);
+                if (page >= 0)
+                  f = scale_value(p.c.k_scale[scale_offset(p.c, page, at0.head,
+                                                           j & (p.c.page_size - 1))]);
               }
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                s[x] = __float_as_uint(__uint_as_float(s[x]) * __shfl_sync(0xffffffffu, f, x));
+            }
+            if (!whole_tile || (kE4M3 && codes)) {
+              // what the row does not see becomes -inf, for the second pass too
+              const int base = pos0 + half * kScores + 32 * k;
+              uint32_t m = below(context - base);
+              if (p.window > 0) m &= below(p.sinks - base) | ~below(seen.lo - base);
+              const int shift = context - base;  // bit of the first drafted token
+              m |= shift >= 32 || shift <= -64 ? 0u
+                   : shift >= 0               ? static_cast<uint32_t>(seen.mask << shift)
+                                              : static_cast<uint32_t>(seen.mask >> -shift);
+              if (!live) m = 0;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!(m >> x & 1u)) s[x] = 0xFF800000u;
+              tmem_st32(s_at + 32 * k, s);
               tmem_wait_st();
             }
-            float mx[2 * kCh];
+            float mx[2];
 #pragma unroll
-            for (int a = 0; a < 2 * kCh; ++a) {
-              const uint32_t* v = s[a / 2] + a % 2 * 16;
-              mx[a] = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            for (int a = 0; a < 2; ++a) {
+              mx[a] = fmax3(__uint_as_float(s[16 * a]), __uint_as_float(s[16 * a + 1]),
+                            __uint_as_float(s[16 * a + 2]));
 #pragma unroll
               for (int x = 3; x < 15; x += 2)
-                mx[a] = fmax3(mx[a], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-              mx[a] = fmaxf(mx[a], __uint_as_float(v[15]));
+                mx[a] = fmax3(mx[a], __uint_as_float(s[16 * a + x]),
+                              __uint_as_float(s[16 * a + x + 1]));
+              mx[a] = fmaxf(mx[a], __uint_as_float(s[16 * a + 15]));
             }
-#pragma unroll
-            for (int a = 0; a < kCh; ++a) top = fmax3(top, mx[2 * a], mx[2 * a + 1]);
+            top = fmax3(top, mx[0], mx[1]);
           }
-          const float z = top * p.scale_log2;
-          const bool raise = z > limit;
-          if (__any_sync(0xffffffffu, raise)) {
-            float f = 1.f;
-            if (raise) {
-              const float to = z - kShift<kFp16>;
-              if (limit != -INFINITY) f = ex2_approx(ref - to);  // (else nothing is summed yet)
-              ref = to;
-              limit = z + kRaise<kFp16>;
-              sum *= f;
+        }
+        float z = top * scale;
+        bool any;
+        if constexpr (kH == 2) {
+          any = named_bar_or(pair, 64, dead || z > limit);
+          if (any) {  // the row's maximum, by way of the first of its threads
+            if (half == 1) *mine_s = dead ? __uint_as_float(kNan) : z;
+            named_bar_sync(pair, 64);
+            if (half == 0) {
+              const float other = *mine_s;
+              z = dead || other != other ? __uint_as_float(kNan) : fmaxf(z, other);
+              *mine_s = z;
             }
-            if (mine > 0) {
-              // O refers to the old reference: once the last O += P V has landed
-              if (!(ok = wait(L::bPV + g, s_phase ^ 1u))) break;
+            named_bar_sync(pair, 64);
+            if (half == 1) z = *mine_s;
+            if (__any_sync(0xffffffffu, z != z)) dead = true;
+          }
+        } else {
+          any = __any_sync(0xffffffffu, z > limit);
+        }
+        if (dead) break;
+        if (any) {
+          const bool raise = z > limit;
+          float f = 1.f;
+          if (raise) {
+            const float to = z - kShift<kType>;
+            if (limit != -INFINITY) f = ex2_approx(ref - to);  // (else nothing is summed yet)
+            ref = to;
+            limit = z + kRaise<kType>;
+            sum *= f;
+          }
+          if (mine > 0 && warp_live) {
+            // O refers to the old reference: once the last O += P V has landed
+            if (!wait(L::bPV + g, s_phase ^ 1u)) {
+              dead = true;  // (leaves with the row's other thread, at the next tile)
+            } else {
               tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < D / 32; ++k) {
+              for (int k = 0; k < D / 32 / kH; ++k) {
                 uint32_t o[32];
-                tmem_ld32(o_at + 32 * k, o);
+                const uint32_t at = o_at + half * (D / kH) + 32 * k;
+                tmem_ld32(at, o);
                 tmem_wait_ld(o);
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                tmem_st32(o_at + 32 * k, o);
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st32(at, o);
               }
             }
           }
-          const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), r2 = f2_pack(-ref, -ref);
+        }
+        if (warp_live) {
+          bool wide = false;  // this tile's V is bf16
+          if constexpr (kE4M3) {
+            if (!wait(L::bVFull + v_slot, v_phase)) dead = true;
+            wide = misc[6 + v_slot] != 0;
+          }
+          const uint64_t c2 = f2_pack(scale, scale), r2 = f2_pack(-ref, -ref);
           uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll 1
-          for (int k = 0; k < 4; k += kCh) {
-            uint32_t s[kCh][32];
+          for (int k = 0; k < kScores / 32; ++k) {
+            uint32_t s[32], pk[16];
+            tmem_ld32(s_at + 32 * k, s);
+            tmem_wait_ld(s);
 #pragma unroll
-            for (int y = 0; y < kCh; ++y) tmem_ld32(s_at + 32 * (k + y), s[y]);
-#pragma unroll
-            for (int y = 0; y < kCh; ++y) tmem_wait_ld(s[y]);
-#pragma unroll
-            for (int y = 0; y < kCh; ++y) {
-              uint32_t pk[16 * kParts];
+            for (int x = 0; x < 16; ++x) {
+              const uint64_t z2 =
+                  f2_fma(f2_pack(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, r2);
+              float z0, z1;
+              f2_unpack(z2, z0, z1);
+              z0 = ex2_approx(z0);
+              z1 = ex2_approx(z1);
+              acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
+              pk[x] = pack16<!kFp16>(z0, z1);
+            }
+            // P of 64 scores takes the first 32 of their columns; as two bf16 terms, each 32 their
+            // own
+            if (kE4M3 && wide) {
+              // (the scores once more: hardly ever needed, and registers are scarce)
+              uint32_t lo[16];
+              tmem_ld32(s_at + 32 * k, s);
+              tmem_wait_ld(s);
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
-                const uint64_t z2 = f2_fma(f2_pack(__uint_as_float(s[y][2 * x]),
-                                                   __uint_as_float(s[y][2 * x + 1])),
-                                           c2, r2);
-                float z0, z1;
-                f2_unpack(z2, z0, z1);
-                z0 = ex2_approx(z0);
-                z1 = ex2_approx(z1);
-                acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
-                pk[x] = pack16<!kFp16>(z0, z1);
-                if constexpr (kParts == 2) {
-                  const float2 h = unpack16<true>(pk[x]);
-                  pk[16 + x] = pack16<true>(z0 - h.x, z1 - h.y);
-                }
+                const float z0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), scale, -ref));
+                const float z1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), scale, -ref));
+                pk[x] = pack16<true>(z0, z1);
+                const float2 h = unpack16<true>(pk[x]);
+                lo[x] = pack16<true>(z0 - h.x, z1 - h.y);
               }
-              if constexpr (kParts == 2)
-                tmem_st32(s_at + 32 * (k + y), pk);
-              else
-                tmem_st16(s_at + 16 * (k + y), pk);
+              tmem_st16(s_at + 32 * k, pk);
+              tmem_st16(s_at + 32 * k + 16, lo);
+            } else {
+              tmem_st16(s_at + k / 2 * 64 + k % 2 * 16, pk);
             }
           }
           float a0, a1;
@@ -797,28 +1008,30 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           sum += a0 + a1;
           tmem_wait_st();
         }
-        if (!whole_tile) {
+        if (!whole_tile && half == 0) {
           // ---- V's rows that not every row sees: thread r looks after position r ----
-          if (!(ok = wait(L::bVFull + v_slot, v_phase))) break;
+          if (!wait(L::bVFull + v_slot, v_phase)) dead = true;
           const int j = pos0 + r;
-          if (!(j < context && (p.window <= 0 || j < p.sinks || j >= w.hi)) || w.n.drafted == 0) {
+          if (!dead && !(j < context && (p.window <= 0 || j < p.sinks || j >= w.hi))) {
             const bool drafted = j >= context && j < w.n.len;
             const bool border = j < context && j >= w.lo;
-            bool zero = w.n.drafted == 0 || !(drafted || border);
+            const bool zero = !(drafted || border);
+            const bool wide = kE4M3 && misc[6 + v_slot] != 0;
             const uint32_t line = sb + L::kV + v_slot * L::kTile + r * 128;
             // (chunks in the order of the swizzle: neighbouring rows meet no bank twice)
             auto at = [&](int c) {
               return line + c / 8 * (kTreeTile * 128) + ((c % 8) ^ (r & 7)) * 16;
+            };
+            auto odd_in = [&](uint32_t v) {
+              return kFp16 && !wide ? not_finite<true>(v) : not_finite<false>(v);
             };
             uint32_t odd = 0;
             if (!zero) {
 #pragma unroll 8
               for (int c = 0; c < 8 * L::kAtoms; ++c) {
                 const float4 f = ld_shared_v4(at(c));
-                odd |= not_finite<kFp16>(__float_as_uint(f.x)) |
-                       not_finite<kFp16>(__float_as_uint(f.y));
-                odd |= not_finite<kFp16>(__float_as_uint(f.z)) |
-                       not_finite<kFp16>(__float_as_uint(f.w));
+                odd |= odd_in(__float_as_uint(f.x)) | odd_in(__float_as_uint(f.y));
+                odd |= odd_in(__float_as_uint(f.z)) | odd_in(__float_as_uint(f.w));
               }
             }
             if (odd & 0x80008000u) {
@@ -828,12 +1041,11 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
 #pragma unroll 1
               for (int c = 0; c < 32 * L::kAtoms; ++c) {
                 const uint32_t word = at(c / 4) + c % 4 * 4;
-                uint32_t v;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(word) : "memory");
-                const uint32_t n = not_finite<kFp16>(v);
+                uint32_t v = ld_shared_u32(word);
+                const uint32_t n = odd_in(v);
                 if (n & 0x8000u) v &= 0xFFFF0000u;
                 if (n & 0x80000000u) v &= 0x0000FFFFu;
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(word), "r"(v) : "memory");
+                st_shared_u32(word, v);
               }
             }
             if (zero) {
@@ -848,65 +1060,77 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         if (lane == 0) mbar_arrive(bar(L::bPFull + g));
         s_phase ^= 1u;
         ++mine;
-        step_v();
+        step();
+        if (kH == 1 && dead) break;
       }
-      if (!ok) break;
       // ---- the item's end: the block's part of O ----
-      if (mine > 0 && !(ok = wait(L::bPV + g, s_phase ^ 1u))) break;
+      if (!dead && mine > 0 && !wait(L::bPV + g, s_phase ^ 1u)) dead = true;
       tc_fence_after();
+      if (w.empty()) w.at.tile += tiles;
       const bool done = w.at.tile == w.at.tiles;
       const bool whole = done && first_tile >= begin;
       const int part = decode_part(first_tile, begin);
       float f0 = 1.f, f1 = 0.f;  // of this group's O and of the other's
       float base = limit == -INFINITY ? -INFINITY : ref;
-      if constexpr (kNB == 1) {
-        fin[(g * 2 + 0) * kTreeBlockRows + r] = base;
-        fin[(g * 2 + 1) * kTreeBlockRows + r] = sum;
-        if (!(ok = sync_groups())) break;
-        const float other = fin[((g ^ 1) * 2 + 0) * kTreeBlockRows + r];
-        const float other_sum = fin[((g ^ 1) * 2 + 1) * kTreeBlockRows + r];
-        const float m = fmaxf(base, other), to = m == -INFINITY ? 0.f : m;
-        // (a NaN in the sum of a row without a finite score stays one)
-        f0 = base == -INFINITY ? 1.f : ex2_approx(base - to);
-        f1 = other == -INFINITY ? 1.f : ex2_approx(other - to);
-        sum = sum * f0 + other_sum * f1;
-        base = m;
+      if (!w.empty()) {
+        // the row's sum: of its threads, and of both groups where they have the same rows
+        if constexpr (kH == 2) {
+          if (half == 1) *mine_s = sum;
+          named_bar_sync(pair, 64);
+          if (half == 0) *mine_s = sum += *mine_s;
+        } else {
+          *mine_s = sum;
+        }
+        if (half == 0) refs[g * kTreeBlockRows + r] = base;
+        if (dead || !(ok = sync_all())) {
+          ok = false;
+          break;
+        }
+        sum = *mine_s;
+        if constexpr (kNB == 1) {
+          const float other = refs[(g ^ 1) * kTreeBlockRows + r];
+          const float other_sum = sums[(g ^ 1) * kTreeBlockRows + r];
+          const float m = fmaxf(base, other), to = m == -INFINITY ? 0.f : m;
+          // (a NaN in the sum of a row without a finite score stays one)
+          f0 = base == -INFINITY ? 1.f : ex2_approx(base - to);
+          f1 = other == -INFINITY ? 1.f : ex2_approx(other - to);
+          sum = g == 0 ? sum * f0 + other_sum * f1 : other_sum * f1 + sum * f0;
+          base = m;
+        }
       }
       if (!live) sum = 0.f;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const float lse =
-          sum == 0.f ? -INFINITY : (base == -INFINITY ? 0.f : base) + log2f(sum);
-      const int h = (row0 + my_row) - t * p.group;
+      const float lse = sum == 0.f ? -INFINITY : (base == -INFINITY ? 0.f : base) + log2f(sum);
       const long long at =
-          ((static_cast<long long>(b) * p.tokens + t) * p.c.heads + head) * p.group + h;
-      const bool have0 = kNB == 2 || tiles > 0, have1 = kNB == 1 && tiles > 1;
-      constexpr int kCols = kNB == 1 ? D / 2 : D;  // of this thread
-      const int col0 = kNB == 1 ? g * kCols : 0;
+          ((static_cast<long long>(b) * p.tokens + t) * p.c.heads + at0.head) * p.group + h;
+      const bool have1 = kNB == 1 && tiles > 1;
+      constexpr int kCols = (kNB == 1 ? D / 2 : D) / kH;  // of this thread
+      const int col0 = kNB == 1 ? (g * kH + half) * kCols : half * kCols;
       // the O of tile 0's group and of the other one
-      const uint32_t o_first = kNB == 1 ? tmem + lanes + 256 : o_at;
+      const uint32_t o_first = (kNB == 1 ? tmem + lanes + 256 : o_at) + col0;
       const float w0 = kNB == 1 && g == 1 ? f1 : f0, w1 = g == 1 ? f0 : f1;
-      if (warp_live) {
+      if (__any_sync(0xffffffffu, there)) {
 #pragma unroll 1
-        for (int k = 0; k < kCols / 32; ++k) {
-          uint32_t o[32];
-          tmem_ld32(o_first + col0 + 32 * k, o);
+        for (int k = 0; k < kCols; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_first + k, o);
           tmem_wait_ld(o);
-          float x[32];
+          float x[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = have0 ? __uint_as_float(o[c]) * w0 : 0.f;
+          for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(o[c]) * w0;
           if (have1) {
-            tmem_ld32(o_first + 128 + col0 + 32 * k, o);
+            tmem_ld16(o_first + 128 + k, o);
             tmem_wait_ld(o);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = fmaf(__uint_as_float(o[c]), w1, x[c]);
+            for (int c = 0; c < 16; ++c) x[c] = fmaf(__uint_as_float(o[c]), w1, x[c]);
           }
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = sum == 0.f ? 0.f : x[c] * inv;
-          if (my_row < rows) {
+          for (int c = 0; c < 16; ++c) x[c] = sum == 0.f ? 0.f : x[c] * inv;
+          if (there) {
             if (whole) {
-              uint4* out = reinterpret_cast<uint4*>(p.o + (at * D + col0 + 32 * k) * 2);
+              uint4* out = reinterpret_cast<uint4*>(p.o + (at * D + col0 + k) * 2);
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 2; ++c)
                 out[c] = make_uint4(pack16<kOutBf16>(x[8 * c], x[8 * c + 1]),
                                     pack16<kOutBf16>(x[8 * c + 2], x[8 * c + 3]),
                                     pack16<kOutBf16>(x[8 * c + 4], x[8 * c + 5]),
@@ -914,9 +1138,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             } else {
               float4* out = reinterpret_cast<float4*>(
                                 p.workspace + rows_at(blockIdx.x, part, p.item_rows, D)) +
-                            (col0 / 4 + 8 * k) * p.item_rows + my_row;
+                            (col0 + k) / 4 * p.item_rows + my_row;
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
+              for (int c = 0; c < 4; ++c)
                 out[c * p.item_rows] =
                     make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
             }
@@ -928,14 +1152,14 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           float* ws = reinterpret_cast<float*>(p.workspace +
                                                rows_at(blockIdx.x, part, p.item_rows, D)) +
                       4 * my_row;
-          add_not_finite<kType, kOutBf16>(p, b, head, context, bad[0] & seen.mask, col0, kCols, out,
-                                          ws);
+          add_not_finite<kType, kOutBf16>(p, b, at0.head, context, bad[0] & seen.mask, col0, kCols,
+                                          out, ws);
           const int behind = seen.lo - w.lo;  // of the border positions: those that it does not see
-          add_not_finite<kType, kOutBf16>(p, b, head, w.lo,
+          add_not_finite<kType, kOutBf16>(p, b, at0.head, w.lo,
                                           behind >= 64 ? 0ull : bad[1] >> behind << behind, col0,
                                           kCols, out, ws);
         }
-        if (my_row < rows && (kNB == 2 || g == 0)) {
+        if (there && half == 0 && (kNB == 2 || g == 0)) {
           if (whole)
             p.lse[at] = lse * 0.69314718055994531f;
           else
@@ -954,8 +1178,13 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       i += tiles;
       first_tile = begin + i;
       if (i < count) {
-        // O and Q are free, and nobody looks at `bad` or `fin` any more
-        if (!(ok = sync_groups())) break;
+        if (!w.empty()) {
+          // (what the item before this one used; this one's may still be looked at)
+          parity ^= 1;
+          if (threadIdx.x < 2) bad_s[2 * parity + threadIdx.x] = 0;
+          if (kE4M3 && threadIdx.x < 2) misc[8 + 2 * parity + threadIdx.x] = 0;
+          if (!(ok = sync_all())) break;  // O is free, and nobody looks at `fin` any more
+        }
         w.at.tile = w.at.tiles - 1;
         if (decode_advance(w.at, copies)) enter(p, w);
       }
@@ -980,9 +1209,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const TreeParams p, 
   grid_dep_wait();
   const Join j = reinterpret_cast<const Join*>(p.workspace)[c0];
   if (j.last < 0 || cols >= D / 8) return;
-  const int head = j.item / p.row_blocks;
-  const int row0 = (j.item - head * p.row_blocks) * p.item_rows;
-  if (row >= min(p.item_rows, p.tokens * p.group - row0)) return;
+  const int block_rows = p.block_tokens * p.block_heads;
+  const Rows r = rows_of(p, j.item, p.item_rows / block_rows);
+  const int t = r.t0 + row / p.block_heads, h = r.h0 + row % p.block_heads;
+  if (t >= p.tokens || h >= p.group) return;
   float top = -INFINITY, sum = 0.f, acc[8] = {};
 #pragma unroll 1
   for (int c = c0; c <= j.last; c += kBatch) {
@@ -1018,9 +1248,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const TreeParams p, 
       for (int k = 0; k < 8; ++k) acc[k] = fmaf(f, v[k], acc[k]);
     }
   }
-  const int t = (row0 + row) / p.group, h = (row0 + row) - t * p.group;
   const long long at =
-      ((static_cast<long long>(j.entry) * p.tokens + t) * p.c.heads + head) * p.group + h;
+      ((static_cast<long long>(j.entry) * p.tokens + t) * p.c.heads + r.head) * p.group + h;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   reinterpret_cast<uint4*>(p.o)[at * (D / 8) + cols] =
       make_uint4(pack16<kOutBf16>(acc[0] * inv, acc[1] * inv),
@@ -1064,7 +1293,7 @@ int launch(const KernelParams& kp, int dev, int sms, cudaStream_t stream) {
   if (!ready[dev]) return -4;
   const TreeParams& p = kp.p;
   const long long items =
-      static_cast<long long>(p.t.batch) * p.c.heads * p.row_blocks;
+      static_cast<long long>(p.t.batch) * p.c.heads * p.token_items * p.head_items;
   const long long tiles =
       decode_span_most(static_cast<long long>(p.t.width) << p.c.page_shift,
                        p.window > 0 ? (p.window < (1 << 30) ? p.window : 1 << 30) + p.tokens : 0,
@@ -1082,7 +1311,7 @@ int launch(const KernelParams& kp, int dev, int sms, cudaStream_t stream) {
   if (!launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), kThreads, L::kBytes, stream, false,
                      kp))
     return -4;
-  const int rows = p.tokens * p.group < p.item_rows ? p.tokens * p.group : p.item_rows;
+  const int rows = p.item_rows;
   const dim3 join(static_cast<unsigned>(grid), (rows * (D / 8) + kJoinThreads - 1) / kJoinThreads);
   return launch_kernel(join_kernel<D, kType == kBf16 || kType == kE4M3Bf16>, join, kJoinThreads, 0, stream, true, p, rows)
              ? 0
