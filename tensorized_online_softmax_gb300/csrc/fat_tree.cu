@@ -59,6 +59,7 @@ void cut_rows(int tokens, int group, int blocks, TreeParams* p) {
   p->token_items = (tokens + most * blocks - 1) / (most * blocks);
   p->block_tokens = (tokens + p->token_items * blocks - 1) / (p->token_items * blocks);
   p->item_rows = blocks * p->block_tokens * p->block_heads;
+  p->copies = p->item_rows <= kTreeBlockRows / 2 ? 2 : 1;
 }
 
 }  // namespace

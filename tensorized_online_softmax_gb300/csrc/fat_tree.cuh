@@ -33,8 +33,9 @@ struct TreeParams {
   int block_tokens, block_heads;
   int token_items, head_items;  // items along the tokens and along the group's heads
   int item_rows;                // rows of an item
+  int copies;                   // (e4m3) of an item's rows among the 128 of a block: 2 if they fit
   int direct;       // items are not split
-  unsigned long long poll_limit, timeout_ns;
+  unsigned long long timeout_ns;  // of a wait on the device
   unsigned int* error_word;
 };
 

@@ -66,7 +66,12 @@ template <int kType>
 constexpr int kHalves = kIsE4M3<kType> ? 1 : 2;  // threads to a row
 template <int kType>
 constexpr int kSoftWarps = 8 * kHalves<kType>;
-constexpr int kConvertWarps = 8;
+constexpr int kConvertWarps = 16;  // two teams of four for K and four for V
+// Registers (e4m3): 896 threads start with 72 each; the softmax warps take what the others leave.
+constexpr int kLaunchRegs = 72, kSoftRegs = 136, kControlRegs = 72, kConvertRegs = 40;
+static_assert(256 * kSoftRegs + 128 * kControlRegs + 32 * kConvertWarps * kConvertRegs <=
+                  (384 + 32 * kConvertWarps) * kLaunchRegs,
+              "what is taken has been given");
 template <int kType>
 constexpr int kThreadsOf =
     32 * (kSoftWarps<kType> + 4 + (kIsE4M3<kType> ? kConvertWarps : 0));
@@ -120,7 +125,10 @@ struct Layout {
   static constexpr int kV = kK + kKStages * kTile;
   static constexpr int kRaw = kV + kStages * kTile;
   static constexpr int kScales = kRaw + kRawStages * kRawTile;  // of the codes' rows
-  static constexpr int kBars = kScales + kRawStages * kTreeTile;
+  // u32 [kRawStages][2]: what the converters have to know of a tile: its rows that are seen, [0, a)
+  // and [b, c), a byte each; and the items so far, its own counted, or 0 behind the last tile
+  static constexpr int kInfo = kScales + kRawStages * kTreeTile;
+  static constexpr int kBars = kInfo + kRawStages * 8;
   static constexpr int bKFull = 0;
   static constexpr int bKEmpty = bKFull + kKStages;
   static constexpr int bVFull = bKEmpty + kKStages;
@@ -133,26 +141,27 @@ struct Layout {
   static constexpr int bQFull = bPV + 2;                 // [kQBufs]; e4m3: the softmax warps
   static constexpr int bQFree = bQFull + kQBufs;         // [kQBufs]
   static constexpr int bSync = bQFree + kQBufs;          // all softmax warps are here
-  static constexpr int bDrain = bSync + 1;
+  static constexpr int bVType = bSync + 1;               // [4] (e4m3) a tile's type of V is known
+  static constexpr int bDrain = bVType + (kE4M3 ? 4 : 0);
   static constexpr int kNumBars = bDrain + 1;
   static __device__ __forceinline__ int arrivals(int bar) {
     if (kE4M3 && ((bar >= bKFull && bar < bKEmpty) || (bar >= bVFull && bar < bVEmpty) ||
                   (bar >= bRawEmpty && bar < bSFull)))
-      return kConvertWarps / 2;
+      return kConvertWarps / 4;
     if (bar == bPFull || bar == bPFull + 1) return kSoftWarps<kType> / 2;
     if (bar == bSync || (kE4M3 && bar == bQFull)) return kSoftWarps<kType>;
     return 1;
   }
   static constexpr int kMisc = kBars + ((8 * kNumBars + 15) & ~15);
-  // u32: 0 TMEM base, 1 abort flag; (e4m3) 2 whether the item's queries and keys are bf16, 6 of
-  // V's stages whether they are, 8 the exponents of the item's queries, 20 of the last four tiles
-  // whether their keys are codes; u64 bad[2 parities][2] at 12
+  // u32: 0 TMEM base, 1 abort flag; (e4m3) 2 whether the item's queries and keys are bf16, 4 of
+  // the last four tiles whether their values are, 8 the exponents of the item's queries, 20 of the
+  // last four tiles whether their keys are codes; u64 bad[2 parities][2] at 12
   static constexpr int kBad = kMisc + 48;
   // float: the references [2 groups][128] and the sums [2][128] of the rows; the threads of a row
   // exchange their maxima in the latter.  Ahead of that the plan's sums and the first place.
   static constexpr int kFin = kMisc + 96;
   static constexpr int kBytes = kFin + 2 * 2 * kTreeBlockRows * 4;
-  static_assert(kRawStages % 2 == 0, "K's and V's codes in turn");
+  static_assert(kRawStages % 4 == 0, "K's and V's codes of two teams in turn");
   static_assert(!kE4M3 || kNB == 1, "one block of rows where the codes need room");
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kRaw % 1024 == 0, "tiles on 1 KB");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -204,6 +213,24 @@ __device__ __forceinline__ Rows rows_of(const TreeParams& p, int item, int block
   r.t0 = th * p.block_tokens * blocks;
   r.h0 = (x - th * p.head_items) * p.block_heads;
   return r;
+}
+
+// Waits for a phase of a barrier, up to p.timeout_ns; false, with the abort flag set, if it does
+// not come.  Most of a block's warps wait at any time: suspended, so that their polls take no
+// issue slots.
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const TreeParams& p,
+                                               volatile uint32_t* abort_flag) {
+  constexpr uint32_t kSuspend = 50000;
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_for(bar, parity, kSuspend)) {
+    if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+      atomicOr(p.error_word, 1u);
+      *abort_flag = 1u;
+      return false;
+    }
+  }
+  return true;
 }
 
 // bits 0 .. n - 1
@@ -301,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   DecodePlace* start_s = reinterpret_cast<DecodePlace*>(fin + 2 * kTreeBlockRows);
   auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8 * i; };
   auto wait = [&](int i, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait_bounded(bar(i), parity, p, abort_flag));
+    return __all_sync(0xffffffffu, wait_suspended(bar(i), parity, p, abort_flag));
   };
 
   grid_dep_launch();
@@ -382,11 +409,19 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   Walk w;
   const bool works = count > 0 && (warp <= kVWarp || (warp == kQWarp && !kE4M3) ||
                                    (kE4M3 && warp >= kConvertWarp));
-  if (works) {
+  if (works && warp < kConvertWarp) {
     w.at = *start_s;
     enter(p, w);
   }
 
+  // (Each kind of warp to its very end: no code is shared between register budgets.)
+  auto finish = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  if (warp >= kSoft && warp < kConvertWarp) {
+  if constexpr (kE4M3) regs_dec<kControlRegs>();
   if (!works) {
   } else if (warp == kKWarp || (warp == kVWarp && !kE4M3)) {
     // =================== producers of K and V ===================
@@ -416,9 +451,11 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     uint32_t phase = 0;
     bool ok = true;
     int issued = 0;
+    uint32_t items = 0;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       if (!w.empty()) {
+        if (i == 0 || w.at.tile == 0) ++items;
         const int head = w.at.item / (p.token_items * p.head_items);
         const int page = __shfl_sync(0xffffffffu, window_page,
                                      (w.at.tile - window) * boxes + lane % boxes);
@@ -437,9 +474,19 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           const int c2 = head * (is_k ? kp.k_head : kp.v_head);
           const int c3 = page * (is_k ? kp.k_page : kp.v_page);
           if (!(ok = wait(empty + slot, phase ^ 1u))) break;
-          if (lane == 0)
+          if (lane == 0) {
+            if constexpr (kE4M3) {
+              auto byte = [&](int x) { return static_cast<uint32_t>(min(max(x, 0), kTreeTile)); };
+              const int pos0 = w.row();
+              const bool gap = p.window > 0 && p.sinks < w.lo;
+              st_shared_u32(sb + L::kInfo + slot * 8,
+                            byte(gap ? p.sinks - pos0 : w.n.len - pos0) |
+                                byte(gap ? w.lo - pos0 : 0) << 8 | byte(w.n.len - pos0) << 16);
+              st_shared_u32(sb + L::kInfo + slot * 8 + 4, items);
+            }
             mbar_arrive_expect_tx(bar(full + slot),
                                   n * (kE4M3 ? box_bytes + rows : box_bytes * L::kAtoms));
+          }
           __syncwarp();
           if (mine) {
             if constexpr (kE4M3) {
@@ -466,6 +513,19 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         if (w.at.tile == 0 || w.at.tile == window + per) load_window();
       }
     }
+    if constexpr (kE4M3) {  // to both teams' warps: there is no more
+#pragma unroll 1
+      for (int x = 0; ok && x < 4; ++x) {
+        if (!(ok = wait(empty + slot, phase ^ 1u))) break;
+        if (lane == 0) {
+          st_shared_u32(sb + L::kInfo + slot * 8 + 4, 0u);
+          mbar_arrive(bar(full + slot));
+        }
+        __syncwarp();
+        ++issued;
+        if (++slot == S) slot = 0, phase ^= 1u;
+      }
+    }
     if (!ok) {  // every copy that was issued has to land before the block may end
       for (int x = max(0, issued - S); x < issued; ++x) wait_drain(bar(full + x % S), (x / S) & 1);
     }
@@ -482,7 +542,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         const int buf = items % L::kQBufs;
         if (!(ok = wait(L::bQFree + buf, (items / L::kQBufs & 1) ^ 1u))) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(L::bQFull + buf), kNB * L::kAtoms * block_bytes);
+          mbar_arrive_expect_tx(bar(L::bQFull + buf),
+                                kNB * L::kAtoms * block_bytes);
 #pragma unroll
           for (int x = 0; x < kNB; ++x)
 #pragma unroll
@@ -514,7 +575,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kV, kTreeTile * 128, 1024);
-    int k_slot = 0, v_slot = 0, items = 0;
+    int k_slot = 0, v_slot = 0, items = 0, tile_count = 0;
     uint32_t k_phase = 0, v_phase = 0, p_phase[2] = {0, 0};
     uint32_t idesc_s = kIdescS;
     bool ok = true;
@@ -544,20 +605,18 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       p_phase[g] ^= 1u;
       tc_fence_after();
       const uint64_t vd = v_desc + static_cast<uint32_t>((v_slot * L::kTile) >> 4);
-      if (kE4M3 && misc[6 + v_slot]) {  // bf16, the weights as two terms 16 columns apart
-#pragma unroll 1
-        for (int x = 0; x < kTreeTile / 16; ++x)
+      const bool wide = kE4M3 && misc[4 + tile_count % 4];
+      ++tile_count;
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-            mma_ts<false>(tmem + 256 + g * 128,
-                          tmem + g * kTreeTile + x / 2 * 32 + x % 2 * 8 + term * 16,
-                          vd + static_cast<uint32_t>(x * 128), kIdescPV | kFmtBits,
-                          acc || x + term > 0);
-      } else {
+      for (int x = 0; x < kTreeTile / 32; ++x)  // 32 positions: 32 columns of S, P in 16 of them
+        mma_ts_x2<8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 32,
+                          vd + static_cast<uint32_t>(x * 256),
+                          wide ? kIdescPV | kFmtBits : kIdescPV, acc || x > 0);
+      if (wide) {  // the second term of the weights
 #pragma unroll
-        for (int x = 0; x < kTreeTile / 64; ++x)  // 64 positions: 32 columns of P, 64 rows of V
-          mma_ts_x4<false, 8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 64,
-                                   vd + static_cast<uint32_t>(x * 512), kIdescPV, acc || x > 0);
+        for (int x = 0; x < kTreeTile / 32; ++x)
+          mma_ts_x2<8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 32 + 16,
+                            vd + static_cast<uint32_t>(x * 256), kIdescPV | kFmtBits, 1u);
       }
       mma_commit(bar(L::bPV + g));
       if (kNB == 1 || g == 1) {
@@ -597,131 +656,141 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     mma_commit(bar(L::bDrain));
     wait_drain(bar(L::bDrain), 0);
     __syncwarp();
+  }
+  finish();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
   } else if (kE4M3 && warp >= kConvertWarp) {
+  if constexpr (kE4M3) regs_dec<kConvertRegs>();
+  if (works) {
     // =================== converters ===================
-    // Half of the warps take K's tiles, half V's: 32 rows of a tile to a warp, 16 codes to a
-    // lane at a time, four of those with their loads ahead of the arithmetic.
-    constexpr int kC = D / 16, kEach = 4;
-    const bool is_v = warp >= kConvertWarp + kConvertWarps / 2;
-    const int row0 = (warp - kConvertWarp) % (kConvertWarps / 2) * 32;
-    const int S = is_v ? SV : SK;
-    const int full = is_v ? L::bVFull : L::bKFull, empty = is_v ? L::bVEmpty : L::bKEmpty;
-    const uint32_t ring = sb + (is_v ? L::kV : L::kK);
-    // Four lanes have 64 codes of a row, eight groups of them eight rows.  128-byte rows are
-    // swizzled as they come; rows 5 apart (by xor) in neighbouring groups meet no bank twice,
-    // neither here nor in the tile that is written.
+    // Two teams take tiles in turn, a stage of K and V each; half of a team's warps take K,
+    // half V: 32 rows of a tile to a warp, in pieces of eight rows and 64 codes, 16 of them to
+    // a lane.  128-byte rows are swizzled as they come; rows 5 apart (by xor) in neighbouring
+    // groups of four lanes meet no bank twice, neither there nor in the tile that is written.
+    // A piece's eight rows are eight apart from the next one's: every address is one of three
+    // and a constant.
+    static_assert(!kE4M3 || (SK == 2 && SV == 2), "a stage to a team");
+    const int member = warp - kConvertWarp, team = member / (kConvertWarps / 2);
+    const bool is_v = member % (kConvertWarps / 2) >= kConvertWarps / 4;
     const int group = lane / 4;
-    const int my_row = D == 64 ? group : (group / 2) ^ (group % 2 * 5);
-    int raw = is_v ? 1 : 0, slot = 0, items = 0;
-    uint32_t raw_phase = 0, phase = 0;
-    bool ok = true, wide = false;
-    int tile_count = 0;
+    const int row = member % 4 * 32 + (D == 64 ? group : (group / 2) ^ (group % 2 * 5));
+    const int full = (is_v ? L::bVFull : L::bKFull) + team;
+    const int empty = (is_v ? L::bVEmpty : L::bKEmpty) + team;
+    const uint32_t from_at = sb + L::kRaw + row * D + (D == 64 ? lane % 4 : lane % 4 ^ (row & 7)) * 16;
+    const uint32_t to = sb + (is_v ? L::kV : L::kK) + team * L::kTile + row * 128 +
+                        (2 * (lane % 4) ^ (row & 7)) * 16;
+    int raw = 2 * team + (is_v ? 1 : 0), n = team;
+    uint32_t raw_phase = 0, phase = 0, items = 0;
+    bool wide = false;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      if (!w.empty()) {
-        if (i == 0 || w.at.tile == 0) {  // the item's keys follow its queries' type
-          if (!is_v) {
-            if (!(ok = wait(L::bQFull, items & 1))) break;
-            wide = misc[2] != 0;
-          }
-          ++items;
-        }
-        const uint32_t from = sb + L::kRaw + raw * L::kRawTile;
-        const uint32_t scales = sb + L::kScales + raw * kTreeTile;
-        const uint32_t to = ring + slot * L::kTile;
-        if (!(ok = wait(L::bRawFull + raw, raw_phase))) break;
-        if (!(ok = wait(empty + slot, phase ^ 1u))) break;
-        // whether a row that is seen has a scale that fp16 has not: the byte of a NaN row, 255, is
-        // NaN in either type
-        bool out_of_range = false;
-        {
-          const uint32_t four = ld_shared_u32(scales + 4 * lane);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t e = four >> (8 * y) & 255u;
-            const int j = w.row() + 4 * lane + y;
-            out_of_range |=
-                some_seen(p, w, j, j + 1) && e != 255u && (e < kScaleLow || e > kScaleHigh);
-          }
-          out_of_range = __any_sync(0xffffffffu, out_of_range);
-          // (of V's stage; of K's tile, four deep: the softmax of a tile is over once the scores
-          // of the next but one of its group are under way)
-          if (row0 == 0 && lane == 0)
-            misc[is_v ? 6 + slot : 20 + tile_count % 4] = out_of_range && (is_v || !wide) ? 1u : 0u;
-          ++tile_count;
-        }
-        const bool as_bf16 = is_v ? out_of_range : wide;
-        const bool as_codes = !is_v && !wide && out_of_range;
+    for (;; n += 2) {
+      if (!wait(L::bRawFull + raw, raw_phase)) break;
+      const uint32_t rows_seen = ld_shared_u32(sb + L::kInfo + raw * 8);
+      const uint32_t items_now = ld_shared_u32(sb + L::kInfo + raw * 8 + 4);
+      if (items_now == 0) break;
+      const uint32_t from = from_at + raw * L::kRawTile;
+      const uint32_t scales = sb + L::kScales + raw * kTreeTile;
+      // whether a row that is seen has a scale that fp16 has not (the byte of a NaN row, 255, is
+      // NaN in either type): four bytes to a lane, compared at once
+      const uint32_t four = ld_shared_u32(scales + 4 * lane);
+      uint32_t off = __vcmpgtu4(__vsub4(four, kScaleLow * 0x01010101u),
+                                (kScaleHigh - kScaleLow) * 0x01010101u) &
+                     ~__vcmpeq4(four, 0xFFFFFFFFu);
+      if (off) {
 #pragma unroll 1
-        for (int x = 0; x < kC; x += kEach) {  // kC pieces of eight rows and 64 codes
-          uint32_t in[kEach][4], e[kEach];
-#pragma unroll
-          for (int y = 0; y < kEach; ++y) {
-            const int row = row0 + (x + y) % 4 * 8 + my_row;
-            const int c = (x + y) / 4 * 4 + lane % 4;
-            const float4 v = ld_shared_v4(from + row * D + (D == 64 ? c : (c ^ (row & 7))) * 16);
-            in[y][0] = __float_as_uint(v.x), in[y][1] = __float_as_uint(v.y);
-            in[y][2] = __float_as_uint(v.z), in[y][3] = __float_as_uint(v.w);
-            e[y] = ld_shared_u8(scales + row);
-          }
-          uint32_t out[kEach][8];
-#pragma unroll
-          for (int y = 0; y < kEach; ++y)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(in[y][k], out[y][2 * k], out[y][2 * k + 1]);
-          if (!as_bf16) {
-            // 2^(e - 127) in fp16: down to its subnormals
-#pragma unroll
-            for (int y = 0; y < kEach; ++y) {
-              uint32_t s = as_codes            ? 0x3C00u
-                           : e[y] == 255u      ? 0x7FFFu
-                           : e[y] < 113u       ? 0x0400u >> min(113u - e[y], 31u)
-                                               : (e[y] - 112u) << 10;
-              s = (s & 0x7FFFu) * 0x00010001u;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) out[y][k] = mul_f16x2(out[y][k], s);
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < kEach; ++y) {
-              const float s = scale_value(e[y]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 f = unpack16<false>(out[y][k]);
-                out[y][k] = pack16<true>(f.x * s, f.y * s);
-              }
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < kEach; ++y) {
-            const int row = row0 + (x + y) % 4 * 8 + my_row;
-            const int c = (x + y) / 4 * 4 + lane % 4;
-            const uint32_t line = to + (c / 4) * (kTreeTile * 128) + row * 128;
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-              st_shared_v4u(line + ((2 * c + z) % 8 ^ (row & 7)) * 16, out[y][4 * z],
-                            out[y][4 * z + 1], out[y][4 * z + 2], out[y][4 * z + 3]);
-          }
+        for (uint32_t y = 0; y < 4; ++y) {
+          const uint32_t r = 4 * lane + y;
+          if (r >= (rows_seen & 255u) && (r < (rows_seen >> 8 & 255u) || r >= rows_seen >> 16))
+            off &= ~(255u << (8 * y));
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(full + slot));
-          mbar_arrive(bar(L::bRawEmpty + raw));
-        }
-        if ((raw += 2) >= L::kRawStages) raw -= L::kRawStages, raw_phase ^= 1u;
-        if (++slot == S) slot = 0, phase ^= 1u;
       }
-      if (i + 1 < count && decode_advance(w.at, copies)) enter(p, w);
+      const bool out_of_range = __any_sync(0xffffffffu, off != 0);
+      if (!is_v) {  // the item's keys follow its queries' type
+        bool ok = true;
+        for (; ok && items != items_now; ++items) ok = wait(L::bQFull, items & 1);
+        if (!ok) break;
+        wide = misc[2] != 0;
+      }
+      // (Four deep: a team's tile after the next has its turn once O += P V of this one is done.)
+      if (member % 4 == 0 && lane == 0) {
+        misc[(is_v ? 4 : 20) + n % 4] = out_of_range && (is_v || !wide) ? 1u : 0u;
+        if (is_v) mbar_arrive(bar(L::bVType + n % 4));
+      }
+      if (!wait(empty, phase ^ 1u)) break;
+      // (Little code, so that it stays in the nearest instruction cache beside the other warps'.)
+      if (!(is_v ? out_of_range : wide)) {
+        const bool as_codes = out_of_range && !is_v;
+#pragma unroll 1
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t e = ld_shared_u8(scales + row + 8 * y);
+          // 2^(e - 127) in fp16, down to its subnormals; 1 where the rows stay codes
+          uint32_t s = e == 255u ? 0x7FFFu : e < 113u ? 0x0400u >> min(113u - e, 31u) : (e - 112u) << 10;
+          s = as_codes ? 0x3C003C00u : (s & 0x7FFFu) * 0x00010001u;
+#pragma unroll
+          for (int x = 0; x < L::kAtoms; ++x) {
+            const float4 v = ld_shared_v4((from ^ (x * 64)) + y * 8 * D);
+            uint32_t out[8];
+            e4m3x4_to_f16(__float_as_uint(v.x), out[0], out[1]);
+            e4m3x4_to_f16(__float_as_uint(v.y), out[2], out[3]);
+            e4m3x4_to_f16(__float_as_uint(v.z), out[4], out[5]);
+            e4m3x4_to_f16(__float_as_uint(v.w), out[6], out[7]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k] = mul_f16x2(out[k], s);
+            const uint32_t at = to + x * (kTreeTile * 128) + y * 1024;
+            st_shared_v4u(at, out[0], out[1], out[2], out[3]);
+            st_shared_v4u(at ^ 16u, out[4], out[5], out[6], out[7]);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int y = 0; y < 4 * L::kAtoms; ++y) {
+          const int x = y / 4;
+          const float f = scale_value(ld_shared_u8(scales + row + 8 * (y % 4)));
+          const float4 v = ld_shared_v4((from ^ (x * 64)) + y % 4 * 8 * D);
+          const uint32_t in[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                                  __float_as_uint(v.w)};
+          uint32_t out[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16(in[k], lo, hi);
+            const float2 a = unpack16<false>(lo), b = unpack16<false>(hi);
+            out[2 * k] = pack16<true>(a.x * f, a.y * f);
+            out[2 * k + 1] = pack16<true>(b.x * f, b.y * f);
+          }
+          const uint32_t at = to + x * (kTreeTile * 128) + y % 4 * 1024;
+          st_shared_v4u(at, out[0], out[1], out[2], out[3]);
+          st_shared_v4u(at ^ 16u, out[4], out[5], out[6], out[7]);
+        }
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(full));
+        mbar_arrive(bar(L::bRawEmpty + raw));
+      }
+      if ((raw += 4) >= L::kRawStages) raw -= L::kRawStages, raw_phase ^= 1u;
+      phase ^= 1u;
     }
     __syncwarp();
-  } else if (warp < kSoft) {
+  }
+  finish();
+  } else {
+  if constexpr (kE4M3) regs_inc<kSoftRegs>();
+  if (works) {
     // =================== softmax ===================
     const int g = warp / (kSoft / 2), half = kH == 2 ? warp / 4 % 2 : 0, quarter = warp % 4;
     const int r = quarter * 32 + lane;  // TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr int kScores = kTreeTile / kH;  // of a thread
-    const uint32_t s_at = tmem + lanes + g * kTreeTile + half * kScores;
+    // (e4m3) Where a block has up to 64 rows they stand twice among the 128 of the MMA, and each
+    // copy takes half of a tile's positions (its weights for the others are 0), with statistics and
+    // an O of its own: the softmax takes half as long, and the copies are joined at the item's end.
+    // (Not for 16-bit caches: 0 times an infinite value would be NaN; e4m3 has none.)
+    const int rows_of_copy = kE4M3 && p.copies == 2 ? kTreeBlockRows / 2 : kTreeBlockRows;
+    const int copy = r / rows_of_copy, row_in = r - copy * rows_of_copy;
+    const int pieces = kTreeTile / 16 / kH / (kTreeBlockRows / rows_of_copy);  // of 16 scores
+    const int piece0 = (copy * kH + half) * pieces;
+    const uint32_t s_at = tmem + lanes + g * kTreeTile;
     const uint32_t o_at = tmem + lanes + 256 + g * 128;
     const uint32_t pair = 1 + g * 4 + quarter;  // named barrier of the warps that share rows
     constexpr uint32_t kNan = 0x7FFFFFFFu;
@@ -761,12 +830,12 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       unsigned long long* bad = bad_s + 2 * parity;
       // ---- this thread's row ----
       const int block_rows = p.block_tokens * p.block_heads;
-      const int t_in = r / p.block_heads, h_in = r - t_in * p.block_heads;
+      const int t_in = row_in / p.block_heads, h_in = row_in - t_in * p.block_heads;
       const int t = at0.t0 + (kNB == 2 ? g * p.block_tokens : 0) + t_in, h = at0.h0 + h_in;
-      const bool there = r < block_rows && t < p.tokens && h < p.group;
+      const bool there = row_in < block_rows && t < p.tokens && h < p.group;
       const bool live = there && t < w.n.drafted;
       const bool warp_live = __any_sync(0xffffffffu, live);
-      const int my_row = (kNB == 2 ? g * block_rows : 0) + r;  // within the item
+      const int my_row = (kNB == 2 ? g * block_rows : 0) + row_in;  // within the item
       const int context = w.context();
       float scale = p.scale_log2;
       if constexpr (kE4M3) {
@@ -832,9 +901,11 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                 in[k] = pack16<false>(q2.x * f, q2.y * f);
               }
             }
-            st_shared_v4u(sb + L::kQ + (c / 8) * (kTreeTile * 128) + row * 128 +
-                              ((c % 8) ^ (row & 7)) * 16,
-                          in[0], in[1], in[2], in[3]);
+            const uint32_t to =
+                sb + L::kQ + (c / 8) * (kTreeTile * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
+            if (row < rows_of_copy) st_shared_v4u(to, in[0], in[1], in[2], in[3]);
+            if (row < kTreeBlockRows - rows_of_copy)
+              st_shared_v4u(to + kTreeBlockRows / 2 * 128, in[0], in[1], in[2], in[3]);
           }
           fence_async_shared();
           __syncwarp();
@@ -861,27 +932,38 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         float top = -INFINITY;
         if (warp_live && !dead) {
           const bool codes = kE4M3 && misc[20 + tile_count % 4] != 0;
-#pragma unroll 1  // (little code: what an item's end runs must not be fetched anew each time)
-          for (int k = 0; k < kScores / 32; ++k) {
-            uint32_t s[32];
-            tmem_ld32(s_at + 32 * k, s);
-            tmem_wait_ld(s);
-            if (kE4M3 && codes) {  // (hardly ever) keys whose scales fp16 does not hold
-              const int j = pos0 + 32 * k + lane;
-              float f = 1.f;
-              if (some_seen(p, w, j, j + 1)) {
-                const int page = table_page(p.t, p.c.num_pages, b, j >> p.c.page_shift);
-                if (page >= 0)
-                  f = scale_value(p.c.k_scale[scale_offset(p.c, page, at0.head,
-                                                           j & (p.c.page_size - 1))]);
-              }
+          auto maximum = [&](const uint32_t* s) {  // of 16 scores
+            float mx[2];
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                s[x] = __float_as_uint(__uint_as_float(s[x]) * __shfl_sync(0xffffffffu, f, x));
+            for (int a = 0; a < 2; ++a) {
+              mx[a] = fmax3(__uint_as_float(s[8 * a]), __uint_as_float(s[8 * a + 1]),
+                            __uint_as_float(s[8 * a + 2]));
+#pragma unroll
+              for (int x = 3; x < 7; x += 2)
+                mx[a] = fmax3(mx[a], __uint_as_float(s[8 * a + x]),
+                              __uint_as_float(s[8 * a + x + 1]));
+              mx[a] = fmaxf(mx[a], __uint_as_float(s[8 * a + 7]));
             }
-            if (!whole_tile || (kE4M3 && codes)) {
-              // what the row does not see becomes -inf, for the second pass too
-              const int base = pos0 + half * kScores + 32 * k;
+            top = fmax3(top, mx[0], mx[1]);
+          };
+          // (Little code: what does not fit the nearest instruction cache beside the other warps'
+          // costs more than a loop.)
+          if (whole_tile && !codes) {
+#pragma unroll 1
+            for (int k = piece0; k < piece0 + pieces; k += 2) {
+              uint32_t s[32];
+              tmem_ld32(s_at + 16 * k, s);
+              tmem_wait_ld(s);
+              maximum(s);
+              maximum(s + 16);
+            }
+          } else {
+            // what the row does not see becomes -inf, for the second pass too
+#pragma unroll 1
+            for (int k = piece0; k < piece0 + pieces; ++k) {
+              uint32_t s[16];
+              tmem_ld16(s_at + 16 * k, s);
+              const int base = pos0 + 16 * k;
               uint32_t m = below(context - base);
               if (p.window > 0) m &= below(p.sinks - base) | ~below(seen.lo - base);
               const int shift = context - base;  // bit of the first drafted token
@@ -889,24 +971,27 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                    : shift >= 0               ? static_cast<uint32_t>(seen.mask << shift)
                                               : static_cast<uint32_t>(seen.mask >> -shift);
               if (!live) m = 0;
+              tmem_wait_ld(s);
+              if (kE4M3 && codes) {  // (hardly ever) keys whose scales fp16 does not hold
+                const int j = base + lane % 16;
+                float f = 1.f;
+                if (some_seen(p, w, j, j + 1)) {
+                  const int page = table_page(p.t, p.c.num_pages, b, j >> p.c.page_shift);
+                  if (page >= 0)
+                    f = scale_value(p.c.k_scale[scale_offset(p.c, page, at0.head,
+                                                             j & (p.c.page_size - 1))]);
+                }
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
+                for (int x = 0; x < 16; ++x)
+                  s[x] = __float_as_uint(__uint_as_float(s[x]) * __shfl_sync(0xffffffffu, f, x));
+              }
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
                 if (!(m >> x & 1u)) s[x] = 0xFF800000u;
-              tmem_st32(s_at + 32 * k, s);
-              tmem_wait_st();
+              tmem_st16(s_at + 16 * k, s);
+              maximum(s);
             }
-            float mx[2];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              mx[a] = fmax3(__uint_as_float(s[16 * a]), __uint_as_float(s[16 * a + 1]),
-                            __uint_as_float(s[16 * a + 2]));
-#pragma unroll
-              for (int x = 3; x < 15; x += 2)
-                mx[a] = fmax3(mx[a], __uint_as_float(s[16 * a + x]),
-                              __uint_as_float(s[16 * a + x + 1]));
-              mx[a] = fmaxf(mx[a], __uint_as_float(s[16 * a + 15]));
-            }
-            top = fmax3(top, mx[0], mx[1]);
+            tmem_wait_st();
           }
         }
         float z = top * scale;
@@ -961,46 +1046,53 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         if (warp_live) {
           bool wide = false;  // this tile's V is bf16
           if constexpr (kE4M3) {
-            if (!wait(L::bVFull + v_slot, v_phase)) dead = true;
-            wide = misc[6 + v_slot] != 0;
+            if (!wait(L::bVType + tile_count % 4, tile_count / 4 & 1)) dead = true;
+            wide = misc[4 + tile_count % 4] != 0;
+          }
+          if (kE4M3 && rows_of_copy < kTreeBlockRows) {  // the other copy's positions
+            const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k % 4 < 2 || wide) tmem_st8(s_at + (1 - copy) * 64 + 8 * k, none);
           }
           const uint64_t c2 = f2_pack(scale, scale), r2 = f2_pack(-ref, -ref);
           uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+          if (!kE4M3 || !wide) {
 #pragma unroll 1
-          for (int k = 0; k < kScores / 32; ++k) {
-            uint32_t s[32], pk[16];
-            tmem_ld32(s_at + 32 * k, s);
-            tmem_wait_ld(s);
+            for (int k = piece0; k < piece0 + pieces; k += 2) {
+              uint32_t s[32], pk[16];
+              tmem_ld32(s_at + 16 * k, s);
+              tmem_wait_ld(s);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const uint64_t z2 =
-                  f2_fma(f2_pack(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, r2);
-              float z0, z1;
-              f2_unpack(z2, z0, z1);
-              z0 = ex2_approx(z0);
-              z1 = ex2_approx(z1);
-              acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
-              pk[x] = pack16<!kFp16>(z0, z1);
+              for (int x = 0; x < 16; ++x) {
+                const uint64_t z2 = f2_fma(
+                    f2_pack(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, r2);
+                float z0, z1;
+                f2_unpack(z2, z0, z1);
+                z0 = ex2_approx(z0);
+                z1 = ex2_approx(z1);
+                acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
+                pk[x] = pack16<!kFp16>(z0, z1);
+              }
+              tmem_st16(s_at + 16 * k, pk);  // (the first half of its 32 scores' columns)
             }
-            // P of 64 scores takes the first 32 of their columns; as two bf16 terms, each 32 their
-            // own
-            if (kE4M3 && wide) {
-              // (the scores once more: hardly ever needed, and registers are scarce)
-              uint32_t lo[16];
-              tmem_ld32(s_at + 32 * k, s);
+          } else {  // as two bf16 terms
+#pragma unroll 1
+            for (int k = piece0; k < piece0 + pieces; k += 2) {
+              uint32_t s[32], hi[16], lo[16];
+              tmem_ld32(s_at + 16 * k, s);
               tmem_wait_ld(s);
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
                 const float z0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), scale, -ref));
                 const float z1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), scale, -ref));
-                pk[x] = pack16<true>(z0, z1);
-                const float2 h = unpack16<true>(pk[x]);
+                acc[x & 1] = f2_add(acc[x & 1], f2_pack(z0, z1));
+                hi[x] = pack16<true>(z0, z1);
+                const float2 h = unpack16<true>(hi[x]);
                 lo[x] = pack16<true>(z0 - h.x, z1 - h.y);
               }
-              tmem_st16(s_at + 32 * k, pk);
-              tmem_st16(s_at + 32 * k + 16, lo);
-            } else {
-              tmem_st16(s_at + k / 2 * 64 + k % 2 * 16, pk);
+              tmem_st16(s_at + 16 * k, hi);
+              tmem_st16(s_at + 16 * k + 16, lo);
             }
           }
           float a0, a1;
@@ -1016,7 +1108,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             const bool drafted = j >= context && j < w.n.len;
             const bool border = j < context && j >= w.lo;
             const bool zero = !(drafted || border);
-            const bool wide = kE4M3 && misc[6 + v_slot] != 0;
+            const bool wide = kE4M3 && misc[4 + tile_count % 4] != 0;
             const uint32_t line = sb + L::kV + v_slot * L::kTile + r * 128;
             // (chunks in the order of the swizzle: neighbouring rows meet no bank twice)
             auto at = [&](int c) {
@@ -1027,7 +1119,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             };
             uint32_t odd = 0;
             if (!zero) {
-#pragma unroll 8
+#pragma unroll 2
               for (int c = 0; c < 8 * L::kAtoms; ++c) {
                 const float4 f = ld_shared_v4(at(c));
                 odd |= odd_in(__float_as_uint(f.x)) | odd_in(__float_as_uint(f.y));
@@ -1049,7 +1141,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
               }
             }
             if (zero) {
-#pragma unroll 8
+#pragma unroll 2
               for (int c = 0; c < 8 * L::kAtoms; ++c) st_shared_v4u(at(c), 0u, 0u, 0u, 0u);
             }
           }
@@ -1088,13 +1180,21 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         }
         sum = *mine_s;
         if constexpr (kNB == 1) {
-          const float other = refs[(g ^ 1) * kTreeBlockRows + r];
-          const float other_sum = sums[(g ^ 1) * kTreeBlockRows + r];
-          const float m = fmaxf(base, other), to = m == -INFINITY ? 0.f : m;
+          // both groups and copies: the largest reference, and what theirs count relative to it
+          float m = -INFINITY;
+#pragma unroll 1
+          for (int x = row_in; x < kTreeBlockRows; x += rows_of_copy)
+            m = fmaxf(m, fmaxf(refs[x], refs[kTreeBlockRows + x]));
+          const float to = m == -INFINITY ? 0.f : m;
           // (a NaN in the sum of a row without a finite score stays one)
-          f0 = base == -INFINITY ? 1.f : ex2_approx(base - to);
-          f1 = other == -INFINITY ? 1.f : ex2_approx(other - to);
-          sum = g == 0 ? sum * f0 + other_sum * f1 : other_sum * f1 + sum * f0;
+          auto factor = [&](float ref_of) { return ref_of == -INFINITY ? 1.f : ex2_approx(ref_of - to); };
+          sum = 0.f;
+#pragma unroll 1
+          for (int x = row_in; x < kTreeBlockRows; x += rows_of_copy)
+            sum += sums[x] * factor(refs[x]) +
+                   sums[kTreeBlockRows + x] * factor(refs[kTreeBlockRows + x]);
+          f0 = factor(base);
+          f1 = factor(refs[(g ^ 1) * kTreeBlockRows + r]);
           base = m;
         }
       }
@@ -1109,7 +1209,37 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       // the O of tile 0's group and of the other one
       const uint32_t o_first = (kNB == 1 ? tmem + lanes + 256 : o_at) + col0;
       const float w0 = kNB == 1 && g == 1 ? f1 : f0, w1 = g == 1 ? f0 : f1;
-      if (__any_sync(0xffffffffu, there)) {
+      // The second copy's O goes to the first by way of Q's memory, four columns of all rows and
+      // then the next four.
+      const bool joined = kE4M3 && rows_of_copy < kTreeBlockRows && !w.empty();
+      const uint32_t stage = sb + L::kQ + row_in * 16;
+      if (joined) {
+        if (copy == 1) {
+#pragma unroll 1
+          for (int k = 0; k < kCols; k += 16) {
+            uint32_t o[16], o2[16];
+            tmem_ld16(o_first + k, o);
+            tmem_wait_ld(o);
+            if (have1) {
+              tmem_ld16(o_first + 128 + k, o2);
+              tmem_wait_ld(o2);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              float x[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                x[y] = __uint_as_float(o[c + y]) * w0;
+                if (have1) x[y] = fmaf(__uint_as_float(o2[c + y]), w1, x[y]);
+              }
+              st_shared_v4(stage + (col0 + k + c) / 4 * (kTreeBlockRows / 2 * 16), x[0], x[1], x[2],
+                           x[3]);
+            }
+          }
+        }
+        if (!(ok = sync_all())) break;
+      }
+      if (copy == 0 && __any_sync(0xffffffffu, there)) {
 #pragma unroll 1
         for (int k = 0; k < kCols; k += 16) {
           uint32_t o[16];
@@ -1123,6 +1253,13 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             tmem_wait_ld(o);
 #pragma unroll
             for (int c = 0; c < 16; ++c) x[c] = fmaf(__uint_as_float(o[c]), w1, x[c]);
+          }
+          if (joined) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              const float4 v = ld_shared_v4(stage + (col0 + k + c) / 4 * (kTreeBlockRows / 2 * 16));
+              x[c] += v.x, x[c + 1] += v.y, x[c + 2] += v.z, x[c + 3] += v.w;
+            }
           }
 #pragma unroll
           for (int c = 0; c < 16; ++c) x[c] = sum == 0.f ? 0.f : x[c] * inv;
@@ -1191,10 +1328,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     }
     __syncwarp();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  finish();
+  }
 }
 
 // The join of an item's parts: eight columns of a row of the item that starts, unfinished, in
@@ -1287,7 +1422,12 @@ int launch(const KernelParams& kp, int dev, int sms, cudaStream_t stream) {
   static std::once_flag once[kMaxDevices];
   static bool ready[kMaxDevices];
   std::call_once(once[dev], [&] {
-    ready[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    // (the split of the registers inside an e4m3 kernel assumes those that it starts with:
+    // anything else could make a warp wait for more without end)
+    cudaFuncAttributes fa;
+    ready[dev] = cudaFuncGetAttributes(&fa, kernel) == cudaSuccess &&
+                 (!L::kE4M3 || fa.numRegs == kLaunchRegs) &&
+                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       L::kBytes) == cudaSuccess;
   });
   if (!ready[dev]) return -4;
