@@ -79,6 +79,14 @@ __device__ __forceinline__ DecodeSpan tree_span(const TreeParams& p, const TreeL
   return decode_span(len, window, p.sinks, kTreeTile);
 }
 
+// An item costs as much as that many tiles besides its own: its queries, the first scores and
+// the last O += P V, which nothing overlaps, its end.  (An entry without drafted tokens costs
+// next to nothing.)
+constexpr int kTreeItemCost = 3;
+__device__ __forceinline__ int tree_cost(const TreeLens& n) {
+  return n.drafted > 0 ? kTreeItemCost : 0;
+}
+
 size_t tree_workspace_bytes(int tokens, int group, int d);
 int launch_tree(const TreeParams& p, int d, bool e4m3, bool bf16, int dev, int sms,
                 cudaStream_t stream);

@@ -353,55 +353,85 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     if (!kE4M3) tma_prefetch_desc(&kp.tm_q);
   }
   const int copies = p.c.heads * p.token_items * p.head_items;
-  long long begin, share, total;
+  long long begin = 0, share = 1;  // units of the line
+  int count;                       // tiles of this block
+  int unit = 0;                    // where its first item starts, relative to `begin`
   if (p.direct) {
     const int e = blockIdx.x / copies;
     if (threadIdx.x == 0) *start_s = {e, static_cast<int>(blockIdx.x) - e * copies, 0, 0};
-    begin = 0;
-    share = total = tree_span(p, tree_lens(p, e)).tiles;
+    count = tree_span(p, tree_lens(p, e)).tiles;
   } else {
-    long long* sums = reinterpret_cast<long long*>(fin);
+    long long* sums = reinterpret_cast<long long*>(fin);  // [warps][units, tiles]
+    long long* ends = reinterpret_cast<long long*>(start_s + 1);  // tiles up to begin, and to end
     const int each = (p.t.batch + kThreads - 1) / kThreads;
     const int lo = min(p.t.batch, static_cast<int>(threadIdx.x) * each);
     const int hi = min(p.t.batch, lo + each);
-    long long mine = 0;
-    for (int e = lo; e < hi; ++e) mine += tree_span(p, tree_lens(p, e)).tiles;
-    long long upto = mine;  // inclusive sum over the threads
+    long long units = 0, tiles = 0;
+    for (int e = lo; e < hi; ++e) {
+      const TreeLens n = tree_lens(p, e);
+      const int t = tree_span(p, n).tiles;
+      tiles += t;
+      units += t + tree_cost(n);
+    }
+    long long units_upto = units, tiles_upto = tiles;  // inclusive sums over the threads
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, s);
-      if (lane >= s) upto += y;
+      const long long x = __shfl_up_sync(0xffffffffu, units_upto, s);
+      const long long y = __shfl_up_sync(0xffffffffu, tiles_upto, s);
+      if (lane >= s) units_upto += x, tiles_upto += y;
     }
-    if (lane == 31) sums[warp] = upto;
+    if (lane == 31) sums[2 * warp] = units_upto, sums[2 * warp + 1] = tiles_upto;
     __syncthreads();
-    total = 0;
+    long long total = 0, all_tiles = 0;
 #pragma unroll 4
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) upto += sums[w];
-      total += sums[w];
+      if (w < warp) units_upto += sums[2 * w], tiles_upto += sums[2 * w + 1];
+      total += sums[2 * w];
+      all_tiles += sums[2 * w + 1];
     }
     total *= copies;
+    all_tiles *= copies;
     share = total <= 0x7fffffff - kTreeMaxBlocks
                 ? decode_share(static_cast<int>(total), gridDim.x, 1)
                 : decode_share(total, static_cast<int>(gridDim.x), 1);
     begin = blockIdx.x * share;
-    long long before = (upto - mine) * copies;
-    if (begin >= before && begin < upto * copies) {
+    const long long end = begin + share;
+    long long unit0 = (units_upto - units) * copies, tile0 = (tiles_upto - tiles) * copies;
+    if (threadIdx.x == 0) {
+      ends[0] = ends[1] = all_tiles;
+      ends[2] = 0;
+    }
+    __syncthreads();
+    if (begin < units_upto * copies && end >= unit0) {
       for (int e = lo; e < hi; ++e) {
-        const int tiles = tree_span(p, tree_lens(p, e)).tiles;
-        const long long n = static_cast<long long>(tiles) * copies;
-        if (begin < before + n) {
-          *start_s = decode_place(e, begin - before, tiles);
-          break;
+        const TreeLens n = tree_lens(p, e);
+        const int t = tree_span(p, n).tiles, cost = tree_cost(n);
+        const long long u = static_cast<long long>(t + cost) * copies;
+        // the tile that a place on the line, in this entry, is the first before or at
+        auto place = [&](long long at, DecodePlace& d, int& off) {
+          d = decode_place(e, at - unit0, t + cost);
+          off = d.tile;
+          d.tile = max(0, d.tile - cost);
+          d.tiles = t;
+          return tile0 + static_cast<long long>(d.item) * t + d.tile;
+        };
+        DecodePlace d;
+        int off;
+        if (begin >= unit0 && begin < unit0 + u) {
+          ends[0] = place(begin, d, off);
+          ends[2] = off;
+          *start_s = d;
         }
-        before += n;
+        if (end >= unit0 && end < unit0 + u) ends[1] = place(end, d, off);
+        unit0 += u;
+        tile0 += static_cast<long long>(t) * copies;
       }
     }
+    __syncthreads();
+    count = static_cast<int>(ends[1] - ends[0]);  // (0: more blocks than tiles)
+    unit = -static_cast<int>(ends[2]);
+    if (threadIdx.x == 0) reinterpret_cast<Join*>(p.workspace)[blockIdx.x].last = -1;
   }
-  Join* joins = reinterpret_cast<Join*>(p.workspace);
-  if (!p.direct && threadIdx.x == 0) joins[blockIdx.x].last = -1;
-  // (0: more blocks than tiles)
-  const int count = begin < total ? static_cast<int>(min(total, begin + share) - begin) : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -816,7 +846,6 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       return ok;
     };
     int i = 0;
-    long long first_tile = begin - w.at.tile;  // of the current item, on the line
     bool ok = true;
     if (threadIdx.x < 4) bad_s[threadIdx.x] = 0;
     if (kE4M3 && threadIdx.x < 4) misc[8 + threadIdx.x] = 0;
@@ -825,6 +854,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
 #pragma unroll 1
     while (ok && i < count) {
       const int tiles = min(count - i, w.at.tiles - w.at.tile);
+      const bool from_start = w.at.tile == 0;
       const Rows at0 = rows_of(p, w.at.item, kNB);
       const int b = w.at.entry;
       unsigned long long* bad = bad_s + 2 * parity;
@@ -1160,8 +1190,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       tc_fence_after();
       if (w.empty()) w.at.tile += tiles;
       const bool done = w.at.tile == w.at.tiles;
-      const bool whole = done && first_tile >= begin;
-      const int part = decode_part(first_tile, begin);
+      // A block leaves at most two unfinished items: its first one (part 0) and its last.
+      const bool whole = done && from_start;
+      const int part = i == 0 ? 0 : 1;
       float f0 = 1.f, f1 = 0.f;  // of this group's O and of the other's
       float base = limit == -INFINITY ? -INFINITY : ref;
       if (!w.empty()) {
@@ -1304,16 +1335,17 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                                      lse_at(blockIdx.x, part, p.item_rows))[my_row] = lse;
         }
       }
-      if (!done && first_tile >= begin && threadIdx.x == 0) {
+      const int units = w.at.tiles + tree_cost(w.n);
+      if (!done && from_start && threadIdx.x == 0) {
         Join j;
         j.entry = b;
         j.item = w.at.item;
-        j.last = static_cast<int>((first_tile + w.at.tiles - 1) / share);
+        j.last = static_cast<int>((begin + unit + units - 1) / share);
         j.part = part;
-        joins[blockIdx.x] = j;
+        reinterpret_cast<Join*>(p.workspace)[blockIdx.x] = j;
       }
+      unit += units;
       i += tiles;
-      first_tile = begin + i;
       if (i < count) {
         if (!w.empty()) {
           // (what the item before this one used; this one's may still be looked at)
