@@ -35,6 +35,7 @@ struct TreeParams {
   int item_rows;                // rows of an item
   int copies;                   // (e4m3) of an item's rows among the 128 of a block: 2 if they fit
   int direct;       // items are not split
+  int item_cost;    // what an item costs besides its tiles, in tiles
   unsigned long long timeout_ns;  // of a wait on the device
   unsigned int* error_word;
 };
@@ -79,12 +80,11 @@ __device__ __forceinline__ DecodeSpan tree_span(const TreeParams& p, const TreeL
   return decode_span(len, window, p.sinks, kTreeTile);
 }
 
-// An item costs as much as that many tiles besides its own: its queries, the first scores and
+// An item costs as much as `item_cost` tiles besides its own: its queries, the first scores and
 // the last O += P V, which nothing overlaps, its end.  (An entry without drafted tokens costs
 // next to nothing.)
-constexpr int kTreeItemCost = 3;
-__device__ __forceinline__ int tree_cost(const TreeLens& n) {
-  return n.drafted > 0 ? kTreeItemCost : 0;
+__device__ __forceinline__ int tree_cost(const TreeParams& p, const TreeLens& n) {
+  return n.drafted > 0 ? p.item_cost : 0;
 }
 
 size_t tree_workspace_bytes(int tokens, int group, int d);

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       const TreeLens n = tree_lens(p, e);
       const int t = tree_span(p, n).tiles;
       tiles += t;
-      units += t + tree_cost(n);
+      units += t + tree_cost(p, n);
     }
     long long units_upto = units, tiles_upto = tiles;  // inclusive sums over the threads
 #pragma unroll
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     if (begin < units_upto * copies && end >= unit0) {
       for (int e = lo; e < hi; ++e) {
         const TreeLens n = tree_lens(p, e);
-        const int t = tree_span(p, n).tiles, cost = tree_cost(n);
+        const int t = tree_span(p, n).tiles, cost = tree_cost(p, n);
         const long long u = static_cast<long long>(t + cost) * copies;
         // the tile that a place on the line, in this entry, is the first before or at
         auto place = [&](long long at, DecodePlace& d, int& off) {
@@ -1335,7 +1335,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                                      lse_at(blockIdx.x, part, p.item_rows))[my_row] = lse;
         }
       }
-      const int units = w.at.tiles + tree_cost(w.n);
+      const int units = w.at.tiles + tree_cost(p, w.n);
       if (!done && from_start && threadIdx.x == 0) {
         Join j;
         j.entry = b;
