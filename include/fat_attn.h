@@ -530,6 +530,13 @@ int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const
  * tokens, q_heads].  A row that sees nothing, and the rows t >= draft_lens[b], give
  * o = 0 and lse = -inf.  What a row does not see has no part in it, NaN and
  * infinities included.
+ * Weights are rounded to the operands' type for their product with the values: to bf16
+ * for a bf16 cache (2^-8 of each), else to fp16 (2^-11 of each, and 2^-36 of the row's
+ * largest); sums and the LSE take them unrounded.  Values of an e4m3 cache whose scale
+ * byte is outside 112 .. 134 take part as bf16, their weights as two terms of bf16 (2^-16);
+ * beyond 2^112 they may overflow.
+ * Tokens of a page, and heads and tokens of q, lie apart (a stride of 0 between several:
+ * FAT_ERR_UNSUPPORTED); pages, cached heads and sequences may share memory.
  * 1 <= tokens <= FAT_TREE_TOKENS; tree_stride may be 0 (one tree for all).
  * window > 0 (at least `tokens`): token t is at position P = context + (number of
  * bits set in its mask) - 1 and sees of the context the positions j < sinks and

@@ -124,7 +124,7 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
   const size_t need =
       fat_attn_tree_workspace_bytes(table->batch, tokens, q_heads, cache->heads, cache->d);
   if (need == 0 || !tree || tree_stride < 0 || sinks < 0 || (window != 0 && window < tokens) ||
-      !(scale > 0.f) || !std::isfinite(scale) || !o || !lse || !workspace ||
+      !(scale > 0.f) || !std::isfinite(scale * kArgLog2e) || !o || !lse || !workspace ||
       workspace_bytes < need)
     return FAT_ERR_INVALID_ARG;
   if (!stride_ok(q_token_stride, 2, &p.q_token) || !aligned(o, 16) || !aligned(lse, 4) ||

@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int my_row = (kNB == 2 ? g * block_rows : 0) + row_in;  // within the item
       const int context = w.context();
-      float scale = p.scale_log2;
+      float down = 1.f;  // what makes the queries of the product out of what they became
       if constexpr (kE4M3) {
         // ---- Q: rows of 128-byte slabs, chunks of 16 bytes permuted by the row ----
         if (!w.empty()) {
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             keep = least + 31u < most || most < 15u;
             if (threadIdx.x == 0) misc[2] = keep ? 1u : 0u;
             if (!keep) up = 127u + 141u - most;
-            scale = p.scale_log2 * __uint_as_float((254u - up) << 23);
+            down = __uint_as_float((254u - up) << 23);
           }
           const float f = __uint_as_float(up << 23);
 #pragma unroll
@@ -959,9 +959,12 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         const bool whole_tile = all_seen(p, w, pos0, pos0 + kTreeTile);
         if (!wait(L::bSFull + g, s_phase)) dead = true;
         tc_fence_after();
+        const bool codes = kE4M3 && misc[20 + tile_count % 4] != 0;
+        // (keys that stayed codes take `down` into their scales: either factor alone may pass what
+        // fp32 holds)
+        const float scale = kE4M3 && !codes ? p.scale_log2 * down : p.scale_log2;
         float top = -INFINITY;
         if (warp_live && !dead) {
-          const bool codes = kE4M3 && misc[20 + tile_count % 4] != 0;
           auto maximum = [&](const uint32_t* s) {  // of 16 scores
             float mx[2];
 #pragma unroll
@@ -1008,8 +1011,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                 if (some_seen(p, w, j, j + 1)) {
                   const int page = table_page(p.t, p.c.num_pages, b, j >> p.c.page_shift);
                   if (page >= 0)
-                    f = scale_value(p.c.k_scale[scale_offset(p.c, page, at0.head,
-                                                             j & (p.c.page_size - 1))]);
+                    f = down * scale_value(p.c.k_scale[scale_offset(p.c, page, at0.head,
+                                                                    j & (p.c.page_size - 1))]);
                 }
 #pragma unroll
                 for (int x = 0; x < 16; ++x)

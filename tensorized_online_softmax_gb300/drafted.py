@@ -32,8 +32,8 @@ _TREE = 64  # FAT_TREE_TOKENS
 class FatRotation(ctypes.Structure):
     """Mirror of ``fat_rotation`` in include/fat_attn.h (same field order)."""
     _fields_ = [("cos_sin", _P), ("rows", _L), ("row_stride", _L), ("positions", _P),
-                ("axis_stride", _L), ("token_stride", _L), ("dim", _I), ("axes", _I), ("sections", _I * _AXES),
-                ("interleaved", _I)]
+                ("axis_stride", _L), ("token_stride", _L), ("dim", _I), ("axes", _I),
+                ("sections", _I * _AXES), ("interleaved", _I)]
 
 
 _pack_rotation = struct.Struct("@PqqPqqii4ii4x").pack
@@ -94,7 +94,7 @@ def kv_cache_append(q, k, v, k_cache, v_cache, slots, positions, cos_sin, *, sec
     (i, i + n / 2) or with ``interleaved`` (2 i, 2 i + 1).  ``positions``: int64
     [T]; or with ``sections``, the counts of pairs that belong to each of up to
     four axes (time, height and width, say), int64 [axes, T].  A key is rounded
-    once, to the cache's type.  Tokens with a negative slot are not stored, their
+    once, to the cache's type.  The slots of one call must differ.  Tokens with a negative slot are not stored, their
     queries are rotated all the same.  A position outside the table cannot be
     refused here: nothing of that token is stored or given out, and
     :func:`check_device_error` returns ``FAT_ERR_INDEX``.
@@ -143,10 +143,10 @@ def tree_mask(parents):
     """The masks of :func:`attn_tree_paged` from the drafted tokens' parents.
 
     ``parents``: integers [..., T], T up to 64: the index of each token's parent,
-    an earlier drafted token, or -1 for a child of the context's last token (what is no earlier
-    token counts as -1).  Returns int64 [..., T]: each token's ancestors and
-    itself as bits.  Plain torch operations on the parents' device, T steps: for
-    a tree that many steps use.
+    an earlier drafted token, or -1 for a child of the context's last token (what
+    is no earlier token counts as -1).  Returns int64 [..., T]: each token's
+    ancestors and itself as bits.  Plain torch operations on the parents' device,
+    T steps: for a tree that many steps use.
     """
     tokens = parents.shape[-1] if parents.dim() else 0
     if parents.is_floating_point() or not 1 <= tokens <= _TREE:
@@ -182,8 +182,11 @@ def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: floa
     sees only the last ``window`` positions, counted along its own path, and the
     first ``sinks`` ones, as in :func:`.attn_decode_window`.
 
-    ``q``: bf16 or fp16 (the cache's own type unless it is e4m3), ``scale``
-    defaults to 1/sqrt(d).  Returns ``(o, lse)``: o contiguous of q's shape and
+    ``q``: bf16 or fp16 (the cache's own type unless it is e4m3), a view of rows
+    that lie apart (one that repeats heads or tokens is refused with
+    ``FAT_ERR_UNSUPPORTED``); ``scale`` defaults to 1/sqrt(d).  Weights are
+    rounded to bf16 for a bf16 cache and to fp16 for the others before they meet
+    the values.  Returns ``(o, lse)``: o contiguous of q's shape and
     type, lse fp32 [B, T, q_heads]; rows that see nothing and rows from
     ``draft_lens`` on are zeros and -inf.  ``workspace``: a CUDA uint8 tensor of
     :func:`attn_tree_workspace_bytes` bytes.
@@ -255,7 +258,7 @@ def kv_cache_keep(k_cache, v_cache, page_table, context_lens, path, counts, *, k
     in every head, keys, values and scales; the sequence then has
     ``context_lens + counts`` positions.  An entry that leads outside the table
     moves nothing, and :func:`check_device_error` returns ``FAT_ERR_INDEX``.
-    Block bounds are renewed by :func:`.kv_block_bounds` as after a write.
+    Pages that are written to must be the sequence's own.  Block bounds are renewed by :func:`.kv_block_bounds` as after a write.
     """
     cache, device, kind, _ = _cache(k_cache, v_cache, k_scale, v_scale, True)
     table, batch, _ = _table(page_table, context_lens, device)

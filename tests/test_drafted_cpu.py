@@ -115,6 +115,10 @@ def test_bad_queries(lib, kw, name):
     (tree, dict(masks=0xB0004), "ALIGNMENT"), (tree, dict(draft_lens=0xC0002), "ALIGNMENT"),
     (tree, dict(work=0xA0008), "ALIGNMENT"), (tree, dict(o=0x80008), "ALIGNMENT"),
     (tree, dict(lse=0x90002), "ALIGNMENT"),
+    (tree, dict(scale=3e38), "INVALID_ARG"),  # times log2(e) fp32 does not hold it
+    (tree, dict(head_stride=0), "UNSUPPORTED"), (tree, dict(token_stride=0), "UNSUPPORTED"),
+    (tree, dict(c=cache(k_token_stride=0)), "UNSUPPORTED"),
+    (tree, dict(c=cache(v_token_stride=0)), "UNSUPPORTED"),
     (keep, dict(path=None), "INVALID_ARG"), (keep, dict(counts=None), "INVALID_ARG"),
     (keep, dict(width=0), "INVALID_ARG"), (keep, dict(stride=-1), "INVALID_ARG"),
     (keep, dict(path=0xB0002), "ALIGNMENT"), (keep, dict(counts=0xC0002), "ALIGNMENT"),

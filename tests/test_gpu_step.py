@@ -92,8 +92,8 @@ def test_keep_refusals(cuda_device):
 @pytest.mark.parametrize("kind,q_type,window", [("bf16", "bf16", None), ("e4m3", "bf16", 40),
                                                 ("fp16", "fp16", 32)])
 def test_steps(cuda_device, kind, q_type, window):
-    """Prompt, two steps of drafted tokens, two single tokens, all captured calls replayed as a
-    serving loop would: against the definitions over a list of rotated keys and values."""
+    """Prompt, two steps of drafted tokens, two single tokens: against the definitions over a list
+    of rotated keys and values."""
     B, H, G, d, ps, T, sinks = 3, 2, 3, 64, 16, 6, 3 if window else 0
     g = torch.Generator().manual_seed(5)
     lens = [50, 7, 33]
