@@ -255,6 +255,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// 16 bytes to shared memory, of which the last 16 - `bytes` are zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
@@ -382,15 +390,20 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     }
     if (lane == 31) sums[2 * warp] = units_upto, sums[2 * warp + 1] = tiles_upto;
     __syncthreads();
-    long long total = 0, all_tiles = 0;
-#pragma unroll 4
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) units_upto += sums[2 * w], tiles_upto += sums[2 * w + 1];
-      total += sums[2 * w];
-      all_tiles += sums[2 * w + 1];
+    static_assert(kWarps <= 32, "a lane to a warp's sums");
+    long long total = lane < kWarps ? sums[2 * lane] : 0;
+    long long all_tiles = lane < kWarps ? sums[2 * lane + 1] : 0;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, total, s);
+      const long long y = __shfl_up_sync(0xffffffffu, all_tiles, s);
+      if (lane >= s) total += x, all_tiles += y;
     }
-    total *= copies;
-    all_tiles *= copies;
+    const long long units_ahead = __shfl_sync(0xffffffffu, total, warp - 1);
+    const long long tiles_ahead = __shfl_sync(0xffffffffu, all_tiles, warp - 1);
+    if (warp > 0) units_upto += units_ahead, tiles_upto += tiles_ahead;
+    total = __shfl_sync(0xffffffffu, total, 31) * copies;
+    all_tiles = __shfl_sync(0xffffffffu, all_tiles, 31) * copies;
     share = total <= 0x7fffffff - kTreeMaxBlocks
                 ? decode_share(static_cast<int>(total), gridDim.x, 1)
                 : decode_share(total, static_cast<int>(gridDim.x), 1);
@@ -453,15 +466,17 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   if (warp >= kSoft && warp < kConvertWarp) {
   if constexpr (kE4M3) regs_dec<kControlRegs>();
   if (!works) {
-  } else if (warp == kKWarp || (warp == kVWarp && !kE4M3)) {
+  } else if (warp == kKWarp || warp == kVWarp) {
     // =================== producers of K and V ===================
-    // (e4m3: one for both, K and V of a tile in turn)
-    constexpr int kTurns = kE4M3 ? 2 : 1;
-    const bool k_warp = warp == kKWarp;
-    const int S = kE4M3 ? L::kRawStages : k_warp ? SK : SV;
-    const int full = kE4M3 ? L::bRawFull : k_warp ? L::bKFull : L::bVFull;
-    const int empty = kE4M3 ? L::bRawEmpty : k_warp ? L::bKEmpty : L::bVEmpty;
-    const uint32_t ring = sb + (kE4M3 ? L::kRaw : k_warp ? L::kK : L::kV);
+    // (e4m3: into a common ring of codes, in turn)
+    const bool is_k = warp == kKWarp;
+    constexpr int kStep = kE4M3 ? 2 : 1;
+    const int S = kE4M3 ? L::kRawStages : is_k ? SK : SV;
+    const int full = kE4M3 ? L::bRawFull : is_k ? L::bKFull : L::bVFull;
+    const int empty = kE4M3 ? L::bRawEmpty : is_k ? L::bKEmpty : L::bVEmpty;
+    const uint32_t ring = sb + (kE4M3 ? L::kRaw : is_k ? L::kK : L::kV);
+    const CUtensorMap* tm = is_k ? &kp.tm_k : &kp.tm_v;
+    const int slot0 = kE4M3 && !is_k ? 1 : 0;
     const int rows = min(p.c.page_size, kTreeTile);  // of a box
     const int boxes = kTreeTile / rows;              // to a tile, each of a page
     const uint32_t box_bytes = rows * (kE4M3 ? D : 128u);
@@ -477,11 +492,15 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                         : 0;
     };
     load_window();
-    int slot = 0;
+    int slot = slot0;
     uint32_t phase = 0;
     bool ok = true;
     int issued = 0;
     uint32_t items = 0;
+    auto next_slot = [&]() {
+      ++issued;
+      if ((slot += kStep) >= S) slot = slot0, phase ^= 1u;
+    };
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       if (!w.empty()) {
@@ -497,46 +516,38 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         }
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
         const int place = a & (p.c.page_size - 1);
-#pragma unroll
-        for (int turn = 0; turn < kTurns; ++turn) {
-          const bool is_k = kE4M3 ? turn == 0 : k_warp;
-          const CUtensorMap* tm = is_k ? &kp.tm_k : &kp.tm_v;
-          const int c2 = head * (is_k ? kp.k_head : kp.v_head);
-          const int c3 = page * (is_k ? kp.k_page : kp.v_page);
-          if (!(ok = wait(empty + slot, phase ^ 1u))) break;
-          if (lane == 0) {
-            if constexpr (kE4M3) {
-              auto byte = [&](int x) { return static_cast<uint32_t>(min(max(x, 0), kTreeTile)); };
-              const int pos0 = w.row();
-              const bool gap = p.window > 0 && p.sinks < w.lo;
-              st_shared_u32(sb + L::kInfo + slot * 8,
-                            byte(gap ? p.sinks - pos0 : w.n.len - pos0) |
-                                byte(gap ? w.lo - pos0 : 0) << 8 | byte(w.n.len - pos0) << 16);
-              st_shared_u32(sb + L::kInfo + slot * 8 + 4, items);
-            }
-            mbar_arrive_expect_tx(bar(full + slot),
-                                  n * (kE4M3 ? box_bytes + rows : box_bytes * L::kAtoms));
+        const int c2 = head * (is_k ? kp.k_head : kp.v_head);
+        const int c3 = page * (is_k ? kp.k_page : kp.v_page);
+        if (!(ok = wait(empty + slot, phase ^ 1u))) break;
+        if (lane == 0) {
+          if constexpr (kE4M3) {
+            auto byte = [&](int x) { return static_cast<uint32_t>(min(max(x, 0), kTreeTile)); };
+            const int pos0 = w.row();
+            const bool gap = p.window > 0 && p.sinks < w.lo;
+            st_shared_u32(sb + L::kInfo + slot * 8,
+                          byte(gap ? p.sinks - pos0 : w.n.len - pos0) |
+                              byte(gap ? w.lo - pos0 : 0) << 8 | byte(w.n.len - pos0) << 16);
+            st_shared_u32(sb + L::kInfo + slot * 8 + 4, items);
           }
-          __syncwarp();
-          if (mine) {
-            if constexpr (kE4M3) {
-              tma_load_4d(ring + slot * L::kRawTile + lane * box_bytes, tm, bar(full + slot), 0,
-                          place, c2, c3);
-              bulk_load(sb + L::kScales + slot * kTreeTile + lane * rows,
-                        (is_k ? p.c.k_scale : p.c.v_scale) + scale_offset(p.c, page, head, place),
-                        rows, bar(full + slot));
-            } else {
-              const uint32_t to = ring + slot * L::kTile + lane * box_bytes;
-#pragma unroll
-              for (int x = 0; x < L::kAtoms; ++x)
-                tma_load_4d(to + x * (kTreeTile * 128), tm, bar(full + slot), x * 64, place, c2,
-                            c3);
-            }
-          }
-          ++issued;
-          if (++slot == S) slot = 0, phase ^= 1u;
+          mbar_arrive_expect_tx(bar(full + slot),
+                                n * (kE4M3 ? box_bytes + rows : box_bytes * L::kAtoms));
         }
-        if (!ok) break;
+        __syncwarp();
+        if (mine) {
+          if constexpr (kE4M3) {
+            tma_load_4d(ring + slot * L::kRawTile + lane * box_bytes, tm, bar(full + slot), 0,
+                        place, c2, c3);
+            bulk_load(sb + L::kScales + slot * kTreeTile + lane * rows,
+                      (is_k ? p.c.k_scale : p.c.v_scale) + scale_offset(p.c, page, head, place),
+                      rows, bar(full + slot));
+          } else {
+            const uint32_t to = ring + slot * L::kTile + lane * box_bytes;
+#pragma unroll
+            for (int x = 0; x < L::kAtoms; ++x)
+              tma_load_4d(to + x * (kTreeTile * 128), tm, bar(full + slot), x * 64, place, c2, c3);
+          }
+        }
+        next_slot();
       }
       if (i + 1 < count) {
         if (decode_advance(w.at, copies)) enter(p, w);
@@ -545,19 +556,20 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     }
     if constexpr (kE4M3) {  // to both teams' warps: there is no more
 #pragma unroll 1
-      for (int x = 0; ok && x < 4; ++x) {
+      for (int x = 0; ok && x < 2; ++x) {
         if (!(ok = wait(empty + slot, phase ^ 1u))) break;
         if (lane == 0) {
           st_shared_u32(sb + L::kInfo + slot * 8 + 4, 0u);
           mbar_arrive(bar(full + slot));
         }
         __syncwarp();
-        ++issued;
-        if (++slot == S) slot = 0, phase ^= 1u;
+        next_slot();
       }
     }
     if (!ok) {  // every copy that was issued has to land before the block may end
-      for (int x = max(0, issued - S); x < issued; ++x) wait_drain(bar(full + x % S), (x / S) & 1);
+      const int each = S / kStep;
+      for (int x = max(0, issued - each); x < issued; ++x)
+        wait_drain(bar(full + slot0 + x % each * kStep), (x / each) & 1);
     }
     __syncwarp();
   } else if (!kE4M3 && warp == kQWarp) {
@@ -871,37 +883,44 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       if constexpr (kE4M3) {
         // ---- Q: rows of 128-byte slabs, chunks of 16 bytes permuted by the row ----
         if (!w.empty()) {
-          constexpr int kChunks = D / 8, kMost = kTreeBlockRows * kChunks / (32 * kSoft);
-          uint4 v[kMost];
-          uint32_t most = 0, least = 0xFFFFFFFFu;
-#pragma unroll
-          for (int y = 0; y < kMost; ++y) {
-            const int x = threadIdx.x + y * 32 * kSoft;
-            const int row = x / kChunks, c = x % kChunks;
+          // 16 bytes of every kStep-th row to a thread, which come to their places as they are.
+          // (Rolled loops: straight code that runs once an item is fetched as it runs.)
+          constexpr int kChunks = D / 8, kStep = 32 * kSoft / kChunks;
+          static_assert(kStep % 8 == 0, "one place in the swizzle to a thread");
+          const int c = threadIdx.x % kChunks, row0 = threadIdx.x / kChunks;
+          const uint32_t q_at = sb + L::kQ + (c / 8) * (kTreeTile * 128) + row0 * 128 +
+                                ((c % 8) ^ (row0 & 7)) * 16;
+          const uint32_t second = (kTreeBlockRows / 2) * 128;  // the second copy's rows
+          const uint8_t* q_from = p.q + wide(b, p.q_batch) + wide(at0.t0, p.q_token) +
+                                  wide(at0.head * p.group + at0.h0, p.q_head) + c * 16;
+#pragma unroll 1
+          for (int row = row0; row < rows_of_copy; row += kStep) {
             const int qt = row / p.block_heads, qh = row - qt * p.block_heads;
-            v[y] = make_uint4(0, 0, 0, 0);
-            if (row < block_rows && at0.t0 + qt < w.n.drafted && at0.h0 + qh < p.group)
-              v[y] = __ldg(reinterpret_cast<const uint4*>(
-                               p.q + wide(b, p.q_batch) + wide(at0.t0 + qt, p.q_token) +
-                               wide(at0.head * p.group + at0.h0 + qh, p.q_head)) +
-                           c);
-            if constexpr (kOutBf16) {
-              const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+            const bool is = row < block_rows && at0.t0 + qt < w.n.drafted && at0.h0 + qh < p.group;
+            const uint8_t* from = is ? q_from + wide(qt, p.q_token) + wide(qh, p.q_head) : p.q;
+            const uint32_t to = q_at + (row - row0) * 128;
+            cp_async16(to, from, is ? 16u : 0u);  // (the others are zeros)
+            if (!kOutBf16 && rows_of_copy < kTreeBlockRows)
+              cp_async16(to + second, from, is ? 16u : 0u);
+          }
+          cp_async_wait_all();
+          if constexpr (kOutBf16) {
+            uint32_t most = 0, least = 0xFFFFFFFFu;
+#pragma unroll 1
+            for (int row = row0; row < rows_of_copy; row += kStep) {
+              const float4 v = ld_shared_v4(q_at + (row - row0) * 128);
+              const uint32_t in[4] = {__float_as_uint(v.x), __float_as_uint(v.y),
+                                      __float_as_uint(v.z), __float_as_uint(v.w)};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 // magnitudes compare as integers, two at a time: the largest, and the least but
                 // zero, less 1; infinities and NaN are what they are at any scale
                 uint32_t m = in[k] & 0x7FFF7FFFu;
-                if ((m & 0x7F80u) == 0x7F80u) m &= 0xFFFF0000u;
-                if ((m >> 16 & 0x7F80u) == 0x7F80u) m &= 0xFFFFu;
+                m &= ~__vcmpgeu2(m, 0x7F807F80u);
                 most = __vmaxu2(most, m);
                 least = __vminu2(least, __vsub2(m, 0x00010001u));
               }
             }
-          }
-          uint32_t up = 127u;  // the exponent byte of the power of two that q is multiplied by
-          bool keep = false;   // q stays bf16
-          if constexpr (kOutBf16) {
             most = __reduce_max_sync(0xffffffffu, max(most >> 16, most & 0xFFFFu));
             least = __reduce_min_sync(0xffffffffu, min(least >> 16, least & 0xFFFFu));
             if (lane == 0) {
@@ -912,30 +931,29 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             most = misc[8 + 2 * parity] >> 7;  // exponent bytes
             least = (0xFFFFu - misc[9 + 2 * parity] + 1u) >> 7;
             // The largest magnitude goes into [2^14, 2^15): an element keeps all its bits down
-            // to 2^-31 of it, as bits of 2^-24 and above.
-            keep = least + 31u < most || most < 15u;
+            // to 2^-31 of it, as bits of 2^-24 and above.  Else q stays bf16.
+            const bool keep = least + 31u < most || most < 15u;
+            const uint32_t up = 127u + 141u - most;  // the exponent byte of what q is multiplied by
             if (threadIdx.x == 0) misc[2] = keep ? 1u : 0u;
-            if (!keep) up = 127u + 141u - most;
-            down = __uint_as_float((254u - up) << 23);
-          }
-          const float f = __uint_as_float(up << 23);
+            if (!keep) down = __uint_as_float((254u - up) << 23);
+            const float f = __uint_as_float(up << 23);
+#pragma unroll 1
+            for (int row = row0; row < rows_of_copy; row += kStep) {
+              const uint32_t to = q_at + (row - row0) * 128;
+              const float4 v = ld_shared_v4(to);
+              uint32_t in[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                                __float_as_uint(v.w)};
+              if (!keep) {
 #pragma unroll
-          for (int y = 0; y < kMost; ++y) {
-            const int x = threadIdx.x + y * 32 * kSoft;
-            const int row = x / kChunks, c = x % kChunks;
-            uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-            if (kOutBf16 && !keep) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 q2 = unpack16<true>(in[k]);
-                in[k] = pack16<false>(q2.x * f, q2.y * f);
+                for (int k = 0; k < 4; ++k) {
+                  const float2 q2 = unpack16<true>(in[k]);
+                  in[k] = pack16<false>(q2.x * f, q2.y * f);
+                }
+                st_shared_v4u(to, in[0], in[1], in[2], in[3]);
               }
+              if (rows_of_copy < kTreeBlockRows)
+                st_shared_v4u(to + second, in[0], in[1], in[2], in[3]);
             }
-            const uint32_t to =
-                sb + L::kQ + (c / 8) * (kTreeTile * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
-            if (row < rows_of_copy) st_shared_v4u(to, in[0], in[1], in[2], in[3]);
-            if (row < kTreeBlockRows - rows_of_copy)
-              st_shared_v4u(to + kTreeBlockRows / 2 * 128, in[0], in[1], in[2], in[3]);
           }
           fence_async_shared();
           __syncwarp();
