@@ -649,13 +649,16 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       const uint64_t vd = v_desc + static_cast<uint32_t>((v_slot * L::kTile) >> 4);
       const bool wide = kE4M3 && misc[4 + tile_count % 4];
       ++tile_count;
-#pragma unroll
-      for (int x = 0; x < kTreeTile / 32; ++x)  // 32 positions: 32 columns of S, P in 16 of them
+      // 32 positions: 32 columns of S, P in 16 of them.  (Rolled beside the converters, whose code
+      // takes the nearest instruction cache: 32 sequences of 4096 to 16384 take 215 us unrolled, 210
+      // rolled; without converters it is the other way round, 88 and 90 us for 256 rows.)
+#pragma unroll(kE4M3 ? 1 : kTreeTile / 32)
+      for (int x = 0; x < kTreeTile / 32; ++x)
         mma_ts_x2<8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 32,
                           vd + static_cast<uint32_t>(x * 256),
                           wide ? kIdescPV | kFmtBits : kIdescPV, acc || x > 0);
       if (wide) {  // the second term of the weights
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < kTreeTile / 32; ++x)
           mma_ts_x2<8, 128>(tmem + 256 + g * 128, tmem + g * kTreeTile + x * 32 + 16,
                             vd + static_cast<uint32_t>(x * 256), kIdescPV | kFmtBits, 1u);
@@ -981,6 +984,11 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         // (keys that stayed codes take `down` into their scales: either factor alone may pass what
         // fp32 holds)
         const float scale = kE4M3 && !codes ? p.scale_log2 * down : p.scale_log2;
+        if (kE4M3 && rows_of_copy < kTreeBlockRows) {  // the other copy's positions
+          const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_st8(s_at + (1 - copy) * 64 + 8 * (k + k / 2 * 2), none);
+        }
         float top = -INFINITY;
         if (warp_live && !dead) {
           auto maximum = [&](const uint32_t* s) {  // of 16 scores
@@ -1103,8 +1111,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           if (kE4M3 && rows_of_copy < kTreeBlockRows) {  // the other copy's positions
             const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k % 4 < 2 || wide) tmem_st8(s_at + (1 - copy) * 64 + 8 * k, none);
+            for (int k = 2; k < 8; ++k)
+              if (k % 4 >= 2 && wide) tmem_st8(s_at + (1 - copy) * 64 + 8 * k, none);
           }
           const uint64_t c2 = f2_pack(scale, scale), r2 = f2_pack(-ref, -ref);
           uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
