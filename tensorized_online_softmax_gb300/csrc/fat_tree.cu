@@ -15,8 +15,8 @@ namespace {
 
 // K or V as [page, head, token, d], in boxes of as many tokens as a tile has of a page: 64
 // columns of 16 bits, 128-byte swizzle (the layout of the MMA's operands), or whole rows of
-// codes (swizzled alike where they have 128 bytes).  A dimension whose stride is 0 becomes one of size 1, and its
-// coordinates are multiplied by 0.
+// codes (swizzled alike where they have 128 bytes).  A dimension whose stride is 0 becomes one
+// of size 1, and its coordinates are multiplied by 0.
 bool cache_map(CUtensorMap* tm, void* ptr, const CacheView& c, int d, bool e4m3, uint32_t page,
                uint32_t head, uint32_t token, int* by_page, int* by_head) {
   *by_page = page != 0 && c.num_pages > 1;
@@ -31,7 +31,8 @@ bool cache_map(CUtensorMap* tm, void* ptr, const CacheView& c, int d, bool e4m3,
   return encode_tensor_map(tm,
                            e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                            4, ptr, dims, strides, box,
-                           e4m3 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+                           e4m3 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                           : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The queries as [sequence, token, head, d], in boxes of a block of rows.
@@ -80,15 +81,15 @@ int launch_tree(const TreeParams& params, int d, bool e4m3, bool bf16, int dev, 
   kp.p = params;
   TreeParams& p = kp.p;
   const CacheView& c = p.c;
-  // Two blocks of rows read the cache once for both; an e4m3 cache's conversion leaves room
-  // for one.
+  // Two blocks of rows read the cache once for both (8 sequences of 4096 to 16384, 256 rows: 88
+  // us, 120 with one); an e4m3 cache's conversion leaves room for one.
   tree::cut_rows(p.tokens, p.group, 1, &p);
   const int blocks = !e4m3 && p.token_items > 1 ? 2 : 1;
   tree::cut_rows(p.tokens, p.group, blocks, &p);
   p.direct = 0;
-  // Measured, of 1, 2, 3, 5 and 8: 16-bit 13 sequences of up to 1029 seen positions (9 tiles) 39,
-  // 31, 30, 33, 38 us; 16 of 1000 to 8192 56.5, 54.5, 54.3, 54.7, 55.3; e4m3, 32 of 4096 to 16384
-  // 275, 260, 257, 249, 247.
+  // Measured, of 1, 2, 3, 4, 6 and 8: 16-bit, 13 sequences of up to 1029 seen positions (9 tiles)
+  // 39, 31, 30, 32, 32, 37 us; 16 of 1000 to 8192 55.7, 54.3, 53.8, 53.6, 54.3, 55.2; e4m3, whose
+  // queries are converted, 32 of 4096 to 16384 231, 222, 218, 215, 210, 208.
   p.item_cost = e4m3 ? 6 : 3;
   if (!e4m3 && !tree::query_map(&kp.tm_q, p, d, &kp.q_batch)) return -4;
   if (!tree::cache_map(&kp.tm_k, c.k, c, d, e4m3, c.k_page, c.k_head, c.k_token, &kp.k_page,

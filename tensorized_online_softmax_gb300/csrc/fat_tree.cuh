@@ -11,7 +11,9 @@ constexpr int kTreeTokens = 64;   // drafted tokens of a sequence: bits of a mas
 constexpr int kTreeTile = 128;    // positions of a tile
 constexpr int kTreeBlockRows = 128;
 constexpr int kTreeMaxBlocks = 160;  // what the workspace has room for
-constexpr int kTreeDirect = 4;       // tiles of an item up to which it is not split
+// tiles of an item up to which it is not split, if a block is there for each (one sequence of 208
+// positions, two tiles: 8.7 us, 11.8 split and joined)
+constexpr int kTreeDirect = 4;
 
 struct TreeParams {
   CacheView c;

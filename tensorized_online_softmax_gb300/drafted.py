@@ -94,10 +94,10 @@ def kv_cache_append(q, k, v, k_cache, v_cache, slots, positions, cos_sin, *, sec
     (i, i + n / 2) or with ``interleaved`` (2 i, 2 i + 1).  ``positions``: int64
     [T]; or with ``sections``, the counts of pairs that belong to each of up to
     four axes (time, height and width, say), int64 [axes, T].  A key is rounded
-    once, to the cache's type.  The slots of one call must differ.  Tokens with a negative slot are not stored, their
-    queries are rotated all the same.  A position outside the table cannot be
-    refused here: nothing of that token is stored or given out, and
-    :func:`check_device_error` returns ``FAT_ERR_INDEX``.
+    once, to the cache's type.  The slots of one call must differ.  Tokens with a
+    negative slot are not stored, their queries are rotated all the same.  A
+    position outside the table cannot be refused here: nothing of that token is
+    stored or given out, and :func:`check_device_error` returns ``FAT_ERR_INDEX``.
 
     Returns the rotated queries, contiguous [T, q_heads, d] (None without q);
     ``out``: a tensor for them, which may be a contiguous q itself.
@@ -258,7 +258,8 @@ def kv_cache_keep(k_cache, v_cache, page_table, context_lens, path, counts, *, k
     in every head, keys, values and scales; the sequence then has
     ``context_lens + counts`` positions.  An entry that leads outside the table
     moves nothing, and :func:`check_device_error` returns ``FAT_ERR_INDEX``.
-    Pages that are written to must be the sequence's own.  Block bounds are renewed by :func:`.kv_block_bounds` as after a write.
+    Pages that are written to must be the sequence's own.  Block bounds are renewed
+    by :func:`.kv_block_bounds` as after a write.
     """
     cache, device, kind, _ = _cache(k_cache, v_cache, k_scale, v_scale, True)
     table, batch, _ = _table(page_table, context_lens, device)
