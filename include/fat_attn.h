@@ -564,7 +564,7 @@ size_t fat_attn_tree_workspace_bytes(int batch, int tokens, int q_heads, int kv_
  * entry, as the path from a tree's root does; else what the rows hold afterwards is
  * unspecified.  An entry below 0, or one that leads outside the table, sets
  * FAT_ERR_INDEX and moves nothing.  Pages that are written to must not be shared by
- * sequences.
+ * sequences.  batch * heads is at most 2^29.
  */
 int fat_kv_keep(const fat_kv_cache* cache, const fat_page_table* table, const int* path,
                 long long path_stride, int width, const int* counts, cudaStream_t stream);

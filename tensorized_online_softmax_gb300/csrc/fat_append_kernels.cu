@@ -215,26 +215,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 // keep
 // ---------------------------------------------------------------------------
 
-// A thread takes one 16-byte chunk of the rows of one (sequence, head), K or V,
-// in the path's order, a batch of loads and then their stores: as the path rises,
-// a row is read no later than the batch in which it is overwritten, and a chunk
-// is nobody else's.  (The scale bytes of an e4m3 cache are a chunk of their own.)
+// A block takes the rows of one (sequence, head), K or V: a wave of them is in registers before
+// any is stored.  As the path rises, a wave's rows come from its first place on or behind it, where
+// no earlier wave has written: so only a wave's own loads and stores are held apart.
 __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const KeepParams p) {
-  constexpr int kBatch = 8;
-  const int per = p.chunks + (p.scales ? 1 : 0);  // jobs to a (sequence, head) and K or V
-  const long long job = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long row_of = job / per;
-  const int chunk = static_cast<int>(job - row_of * per);
-  const long long bh = row_of >> 1;
-  const bool is_v = row_of & 1;
-  const int b = static_cast<int>(bh / p.c.heads);
-  if (b >= p.t.batch) return;
-  const uint32_t h = static_cast<uint32_t>(bh - static_cast<long long>(b) * p.c.heads);
+  constexpr int kDeep = 4;
+  const int each = kThreads / p.chunks;  // rows at a time, 16 bytes to a thread
+  const int row0 = threadIdx.x / p.chunks, chunk = threadIdx.x - row0 * p.chunks;
+  const bool is_v = blockIdx.x & 1;
+  const int b = static_cast<int>(blockIdx.x >> 1) / p.c.heads;
+  const uint32_t h = (blockIdx.x >> 1) - b * p.c.heads;
   const long long most = static_cast<long long>(p.t.width) << p.c.page_shift;
   const int base = p.t.seq_lens[b];
-  int count = p.counts[b];
+  const int count = p.counts[b];
   if (base < 0 || base > most || count < 0 || count > p.width) {
-    atomicOr(p.t.error_word, kErrIndex);
+    if (threadIdx.x == 0) atomicOr(p.t.error_word, kErrIndex);
     return;
   }
   uint8_t* data = is_v ? p.c.v : p.c.k;
@@ -251,48 +246,39 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const KeepParams p) {
     }
     return table_page(p.t, p.c.num_pages, b, static_cast<int>(at >> p.c.page_shift));
   };
-  for (int i0 = 0; i0 < count; i0 += kBatch) {
-    int from_page[kBatch], to_page[kBatch];
-    uint32_t from[kBatch], to[kBatch];
+  auto row_of = [&](int page, uint32_t at) {
+    return reinterpret_cast<uint4*>(
+               data + row_offset(page, h, at, page_stride, head_stride, token_stride)) + chunk;
+  };
+  for (int i0 = 0; i0 < count; i0 += kDeep * each) {
+    uint4 x[kDeep];
+    uint8_t e[kDeep];
+    int to_page[kDeep];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      from_page[j] = to_page[j] = -1;
-      from[j] = to[j] = 0;
-      if (i0 + j < count) {
-        const int step = __ldg(path + i0 + j);
-        if (step < 0) atomicOr(p.t.error_word, kErrIndex);
-        if (step >= 0 && step != i0 + j) {  // (else it is where it belongs)
-          const long long at = static_cast<long long>(base) + step;
-          from_page[j] = page_of(at);
-          to_page[j] = page_of(static_cast<long long>(base) + i0 + j);
-          from[j] = static_cast<uint32_t>(at) & (p.c.page_size - 1);
-          to[j] = static_cast<uint32_t>(base + i0 + j) & (p.c.page_size - 1);
-        }
-      }
+    for (int j = 0; j < kDeep; ++j) {
+      const int i = i0 + j * each + row0;
+      to_page[j] = -1;
+      if (i >= count) continue;
+      const int step = __ldg(path + i);
+      if (step < 0) atomicOr(p.t.error_word, kErrIndex);
+      if (step < 0 || step == i) continue;  // (it is where it belongs)
+      const long long at = static_cast<long long>(base) + step;
+      const int page = page_of(at);
+      const int to = page_of(static_cast<long long>(base) + i);
+      if (page < 0 || to < 0) continue;
+      const uint32_t place = static_cast<uint32_t>(at) & (p.c.page_size - 1);
+      to_page[j] = to;
+      x[j] = *row_of(page, place);
+      if (p.scales && chunk == 0) e[j] = scales[scale_offset(p.c, page, h, place)];
     }
-    if (chunk < p.chunks) {
-      uint4 x[kBatch];
+    __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (from_page[j] >= 0 && to_page[j] >= 0)
-          x[j] = reinterpret_cast<const uint4*>(
-              data + row_offset(from_page[j], h, from[j], page_stride, head_stride,
-                                token_stride))[chunk];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (from_page[j] >= 0 && to_page[j] >= 0)
-          reinterpret_cast<uint4*>(data + row_offset(to_page[j], h, to[j], page_stride,
-                                                     head_stride, token_stride))[chunk] = x[j];
-    } else {
-      uint8_t x[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (from_page[j] >= 0 && to_page[j] >= 0)
-          x[j] = scales[scale_offset(p.c, from_page[j], h, from[j])];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (from_page[j] >= 0 && to_page[j] >= 0)
-          scales[scale_offset(p.c, to_page[j], h, to[j])] = x[j];
+    for (int j = 0; j < kDeep; ++j) {
+      if (to_page[j] < 0) continue;
+      const uint32_t place =
+          static_cast<uint32_t>(base + i0 + j * each + row0) & (p.c.page_size - 1);
+      *row_of(to_page[j], place) = x[j];
+      if (p.scales && chunk == 0) scales[scale_offset(p.c, to_page[j], h, place)] = e[j];
     }
   }
 }
@@ -322,9 +308,7 @@ int launch_kv_append(const AppendParams& p, int d, bool e4m3, bool bf16, bool in
 }
 
 int launch_kv_keep(const KeepParams& p, cudaStream_t stream) {
-  const long long jobs = static_cast<long long>(p.t.batch) * p.c.heads * 2 *
-                         (p.chunks + (p.scales ? 1 : 0));
-  const unsigned grid = static_cast<unsigned>((jobs + kThreads - 1) / kThreads);
+  const unsigned grid = static_cast<unsigned>(2ll * p.t.batch * p.c.heads);
   kv_keep_kernel<<<grid, kThreads, 0, stream>>>(p);
   return launched();
 }

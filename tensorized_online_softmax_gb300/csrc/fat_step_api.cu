@@ -89,7 +89,7 @@ int fat_kv_keep(const fat_kv_cache* cache, const fat_page_table* table, const in
   const bool e4m3 = cache->dtype == FAT_DTYPE_E4M3;
   p.chunks = cache->d * (e4m3 ? 1 : 2) / 16;
   p.scales = e4m3 ? 1 : 0;
-  if (static_cast<long long>(table->batch) * cache->heads > (1ll << 33)) return FAT_ERR_INVALID_ARG;
+  if (static_cast<long long>(table->batch) * cache->heads > (1ll << 29)) return FAT_ERR_INVALID_ARG;
   int dev = 0;
   if ((st = host_device(&dev, &p.t.error_word)) != FAT_OK) return st;
   p.path = path;

@@ -18,6 +18,10 @@ CASES = [
      "phtd"),
     ([63, 15, 40], 64, [[63], list(range(0, 64, 2)), list(range(64))], 1, 64, 128, "e4m3", "kv"),
     ([500], 40, [list(range(3, 40, 3))], 5, 32, 64, "fp16", "pthd"),
+    # long paths, every row onto the one before it
+    ([70, 3, 9], 400, [list(range(1, 300)), list(range(0, 400, 2)), list(range(399))], 2, 16, 128,
+     "bf16", "phtd"),
+    ([70, 16], 700, [list(range(1, 650)), list(range(30, 700))], 1, 16, 64, "e4m3", "pthd"),
 ]
 
 
