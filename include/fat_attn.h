@@ -504,8 +504,8 @@ typedef struct fat_rotation {
  * Store new tokens as fat_kv_write does, the keys rotated; and rotate their
  * queries: q [tokens, q_heads, d] of `dtype`, strides in elements, rows 16-byte
  * aligned; q_out contiguous [tokens, q_heads, d] of the same type, 16-byte
- * aligned (q itself is allowed, if it is contiguous).  q_heads = 0: keys and
- * values only.  A rotated key is rounded once, to the cache's type (for e4m3
+ * aligned (q itself is allowed, if it is contiguous; else it shares no memory with the
+ * inputs).  q_heads = 0: keys and values only.  A rotated key is rounded once, to the cache's type (for e4m3
  * straight from fp32, by the row scale of the rotated row).  slots[t] < 0: the
  * token is not stored, its queries are rotated all the same.  A position outside
  * [0, rows) sets FAT_ERR_INDEX; nothing is stored or given out of that token.
@@ -543,7 +543,8 @@ int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const
  * j > P - window only; pages that no row sees are not read.  0: no window.
  * seq_lens[b] below draft_lens[b] sets FAT_ERR_INDEX.
  * workspace: at least fat_attn_tree_workspace_bytes(...) bytes, 16-byte aligned, any
- * contents; calls sharing it must not overlap on the device.
+ * contents; calls sharing it must not overlap on the device.  o, lse and workspace share no
+ * memory with the inputs.
  */
 #define FAT_TREE_TOKENS 64
 int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,

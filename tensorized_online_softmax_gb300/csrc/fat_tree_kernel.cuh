@@ -776,12 +776,17 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           if (!ok) break;
           wide = misc[2] != 0;
         }
-        // (Four deep: a team's tile after the next has its turn once O += P V of this one is done.)
-        if (member % 4 == 0 && lane == 0) {
-          misc[(is_v ? 4 : 20) + n % 4] = out_of_range && (is_v || !wide) ? 1u : 0u;
-          if (is_v) mbar_arrive(bar(L::bVType + n % 4));
+        // What tile n is, four deep, so once tile n - 4 has its weights.  Of V early, as the
+        // weights wait for it: this team's last tile, n - 2, took the stage of n - 4, whose
+        // O += P V was done.  Of K once the stage is free: the scores of n - 2 are, and were
+        // issued after the O += P V of n - 4.
+        const uint32_t type = out_of_range && (is_v || !wide) ? 1u : 0u;
+        if (is_v && member % 4 == 0 && lane == 0) {
+          misc[4 + n % 4] = type;
+          mbar_arrive(bar(L::bVType + n % 4));
         }
         if (!wait(empty, phase ^ 1u)) break;
+        if (!is_v && member % 4 == 0 && lane == 0) misc[20 + n % 4] = type;
         // (Little code, so that it stays in the nearest instruction cache beside the other warps'.)
         if (!(is_v ? out_of_range : wide)) {
           const bool as_codes = out_of_range && !is_v;

@@ -123,6 +123,34 @@ def test_infinite_values_of_little_weight(cuda_device, typ, lens, T, group):
     assert torch.isinf(o[..., :10]).all() and torch.isfinite(o[..., 10:]).all()
 
 
+@pytest.mark.parametrize("kind,typ", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "bf16"),
+                                      ("e4m3", "fp16")])
+@pytest.mark.parametrize("T,group", [(5, 2), (40, 4)])
+def test_queries_that_are_not_finite(cuda_device, kind, typ, T, group):
+    """NaN for their own rows, nothing for the others."""
+    g = torch.Generator().manual_seed(33)
+    lens = [T + 200, T + 40]
+    q = torch.randn((2, T, group, 64), generator=g).to(TYPES[typ])
+    k, v = torch.randn((2, sum(lens), 1, 64), generator=g).to(TYPES[typ])
+    q[0, 1, 0, 7], q[1, 2, 1, 60], q[1, 0, 0] = math.nan, math.inf, -math.inf
+    s = Drafted(lens, T, q, k, v, kind, seed=5)
+    o, lse = s.run()
+    bad = ~torch.isfinite(q).all(-1)
+    assert torch.isnan(o[bad]).all() and not torch.isfinite(lse[bad]).any()
+    check_tree(o[~bad], lse[~bad], *(x[~bad] for x in s.want()))
+
+
+def test_more_sequences_than_threads(cuda_device):
+    """The plan walks several sequences to a thread."""
+    for kind, d in (("bf16", 64), ("e4m3", 128)):
+        g = torch.Generator().manual_seed(34)
+        lens = [2 + i % 5 + (300 if i % 97 == 0 else 0) for i in range(2000)]
+        q = torch.randn((len(lens), 2, 2, d), generator=g).bfloat16()
+        k, v = torch.randn((2, sum(lens), 1, d), generator=g).bfloat16()
+        s = Drafted(lens, 2, q, k, v, kind, seed=5)
+        check_tree(*s.run(), *s.want())
+
+
 @pytest.mark.parametrize("typ", ["bf16", "fp16"])
 @pytest.mark.parametrize("lens,T,group", [([300, 40], 3, 4), ([2000, 50], 40, 4)], ids=str)
 def test_infinite_keys(cuda_device, typ, lens, T, group):
@@ -195,6 +223,41 @@ def test_scales_that_fp16_has_not(cuda_device, q_type, T, group, d):
     for x in s.cache.scales:
         x[last, 0, lens[0] % 16 or 16:] = 250
     check_tree(*s.run(), *s.want())
+
+
+@pytest.mark.parametrize("q_type", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,group,d", [(4, 2, 128), (40, 3, 64)])
+def test_many_items_with_and_without_such_scales(cuda_device, q_type, T, group, d):
+    """Blocks that go from one sequence's head to the next, whose tiles' keys and values have
+    scales that fp16 has, or has not, at random: what a tile is must not be told from another's."""
+    g = torch.Generator().manual_seed(71)
+    lens = [T + 130 * (1 + i % 9) for i in range(60)]
+    n = sum(lens)
+    q = torch.randn((len(lens), T, 3 * group, d), generator=g).to(TYPES[q_type])
+    k = torch.randn((n, 3, d), generator=g)
+    v = torch.randn((n, 3, d), generator=g)
+    at = 0
+    for m in lens:
+        for j in range(0, m, 128):
+            w = slice(at + j, at + min(j + 128, m))
+            for h in range(3):
+                if torch.rand((), generator=g) < 0.4:
+                    k[w, h] *= 2.0 ** -24
+                if torch.rand((), generator=g) < 0.4:
+                    v[w, h] *= 2.0 ** -24
+        at += m
+    s = Drafted(lens, T, q, k.bfloat16(), v.bfloat16(), "e4m3", page_size=64, seed=12)
+    kk, vv = s.cache.held()
+    for turn in range(3):
+        o, lse = s.run()
+        for b in range(turn, len(lens), 3):
+            for t in (0, T - 1):
+                at = s.positions(b, t)
+                for h in range(3):
+                    r = slice(h * group, (h + 1) * group)
+                    want = ref.attend(s.q[b, t, r].double(), kk[at[0], h, at[1]],
+                                      vv[at[0], h, at[1]], s.scale)
+                    check_tree(o[b, t, r], lse[b, t, r], *want, what=f"{b} {t} {h}")
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
