@@ -49,8 +49,8 @@
 // the other) the walk goes over the tiles of the first positions and those of the window
 // only, rows that are not seen are filled with zeros, and pages that no row needs are not
 // looked up.  32 of 8192 to 32768 positions, of which 4100 are seen, bf16 (538 MB): 88 us,
-// 0.90 of the copy rate; 48 with 1065 seen, groups of 8, e4m3, pages of 16 (107 MB): 33 us,
-// 0.48 (plan, first rows, borders inside tiles and the join: 12 us; the conversions).
+// 0.90 of the copy rate; 48 with 1065 seen, groups of 8, e4m3, pages of 16 (107 MB): 26 us,
+// 0.60 (first rows, borders inside tiles, conversions at two to three blocks an SM).
 #pragma once
 
 #include "fat_cache.cuh"
@@ -1016,6 +1016,18 @@ bool launch_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+// Under a window most sequences have as many tiles: short windows are not split where there is a
+// block for every SM at least, and the last wave of blocks is not much smaller than the others.
+// 8 heads, window 1000, 19, 24, 38, 48, 64, 96 and 128 sequences, split and not, us: bf16 20.6, 23.7,
+// 32.1, 38.3, 48.9, 67.0, 86.9 and 18.0, 20.0, 27.0, 33.2, 52.1, 61.0, 84.0; e4m3, groups of 8,
+// 19.6, 22.3, 27.7, 31.7, 39.7, 52.0, 66.0 and 19.1, 21.8, 22.1, 25.1, 40.9, 47.0, 64.6; 12
+// sequences 16.6 and 17.4, 18.4.  (A single long sequence among short ones costs up to 8 us.  Of
+// windows of 4096 some combinations gain and some lose: split.)
+inline bool whole_windows(long long tiles, long long items, int sms, long long resident) {
+  const long long waves = (items + resident - 1) / resident;
+  return tiles <= 24 && items >= sms && (waves == 1 || 10 * items >= 7 * waves * resident);
+}
+
 template <int D, int kNT, bool kE4M3, bool kBf16, bool kWindow>
 int launch_one(const DecodeParams& p, int dev, cudaStream_t stream) {
   using L = Layout<D, kNT, kE4M3>;
@@ -1033,16 +1045,17 @@ int launch_one(const DecodeParams& p, int dev, cudaStream_t stream) {
   const int copies = (p.per_head ? 1 : p.c.heads) * ((p.group + 8 * kNT - 1) / (8 * kNT));
   const long long positions = static_cast<long long>(p.t.width) << p.c.page_shift;
   const long long tiles = decode_span_most(positions, p.window, p.sinks, kDecodeTile);
-  if (tiles <= kDirectTiles) {  // (the items are at most the query heads: below 2^31)
+  // as many blocks as are resident; fewer if the table cannot hold that many tiles
+  long long grid = static_cast<long long>(L::kBlocks) * sms[dev];
+  // (the items are at most the query heads: below 2^31)
+  const unsigned items = static_cast<unsigned>(copies) * static_cast<unsigned>(p.t.batch);
+  if (tiles <= kDirectTiles || (kWindow && whole_windows(tiles, items, sms[dev], grid))) {
     DecodeParams one = p;
     one.direct = 1;
-    const unsigned items = static_cast<unsigned>(copies) * static_cast<unsigned>(p.t.batch);
     return launch_kernel(kernel, dim3(items), kThreads, L::kSmem, stream, p.per_head != 0, one)
                ? 0
                : -4;
   }
-  // as many blocks as are resident; fewer if the table cannot hold that many tiles
-  long long grid = static_cast<long long>(L::kBlocks) * sms[dev];
   if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
   const long long most =
       (tiles * copies * p.t.batch + p.least_tiles - 1) / p.least_tiles;

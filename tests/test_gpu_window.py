@@ -120,6 +120,32 @@ def test_long_sequences_split_over_the_blocks(cuda_device):
             check_attention(o[b], lse[b], *want, what=f"{lens} {b}")
 
 
+@pytest.mark.parametrize("batch,heads,group,kind,q_type", [
+    (40, 4, 2, "bf16", "bf16"), (52, 8, 8, "e4m3", "bf16"), (160, 4, 1, "fp16", "fp16"),
+    (30, 8, 16, "e4m3", "fp16"), (256, 4, 3, "bf16", "bf16")])
+def test_many_short_windows(cuda_device, batch, heads, group, kind, q_type):
+    """Enough items that each has a block of its own, in one wave of blocks or in several."""
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(0, 2200, batch)]
+    lens[:5] = [0, 1, 800, 801, 2200]
+    window, sinks = 800, 70
+    cache, table, lens, q = setup(lens, heads, group, 64, 64, q_type, kind, seed=batch)
+    o, lse = run(cache, given_back(table, lens, 64, window, sinks), lens, q, window, sinks)
+    for b in [0, 1, 2, 3, 4, *range(5, batch, 9)]:
+        n = lens[b]
+        ids = table[b, :-(-n // 64)].long()
+        at = torch.arange(n)
+        at = at[(at < sinks) | (at >= n - window)]
+        for h in range(heads):
+            k, v = (x[ids, h].reshape(-1, 64)[at] for x in (cache.k_values, cache.v_values))
+            r = slice(h * group, (h + 1) * group)
+            if not n:
+                assert (o[b, r] == 0).all() and (lse[b, r] == -math.inf).all()
+                continue
+            want = drafted_reference.ref.attend(q[b, r].double(), k, v, 0.125)
+            check_attention(o[b, r], lse[b, r], *want, what=f"{b} {h}", kind=kind)
+
+
 def test_graph_replays_with_new_lengths(cuda_device):
     cache, table, lens, q = setup([600, 40, 900], 2, 4, 16, 128, "bf16", "e4m3", seed=6)
     n = torch.tensor([100, 7, 5], dtype=torch.int32).cuda()
