@@ -14,6 +14,14 @@ constexpr int kTreeMaxBlocks = 160;  // what the workspace has room for
 // tiles of an item up to which it is not split, if a block is there for each (one sequence of 208
 // positions, two tiles: 8.7 us, 11.8 split and joined)
 constexpr int kTreeDirect = 4;
+// The same under a window, where most sequences have as many tiles, as long as blocks without an
+// item cost less than the plan and the join: tiles * (blocks - items) <= 6 * blocks.  8 heads of 32
+// rows, split and not, us: window 1000 (10 tiles), 4, 8, 12, 16, 19 sequences of 4096 to 8192, bf16
+// 16.0, 22.8, 26.8, 29.3, 31.2 and 17.7, 20.3, 19.4, 21.5, 23.4; e4m3 21.7, 27.4, 31.8, 36.6, 39.5
+// and 24.8, 25.9, 25.1, 26.1, 27.0; window 2000 (18 tiles), bf16, 8 and 19: 27.2, 41.4 and 27.0,
+// 34.2.  More items than blocks: 24, 32, 48 sequences 36.6, 42.6, 55.3 and 38.9, 40.8, 58.8 (e4m3
+// 49.7, 59.0, 80.8 and 49.2, 50.1, 73.2), and 13 sequences of 5 to 4097 29.7 and 33.3: split.
+constexpr int kTreeWhole = 24;
 
 struct TreeParams {
   CacheView c;

@@ -109,6 +109,32 @@ def test_tree_under_a_window(cuda_device, case, window, sinks):
     check_tree(o, lse, *s.want(window, sinks), what=f"{case} {window} {sinks}")
 
 
+@pytest.mark.parametrize("kind,q_type,T,group", [("bf16", "bf16", 5, 2), ("e4m3", "bf16", 7, 3),
+                                                 ("fp16", "fp16", 40, 4), ("e4m3", "fp16", 60, 2)])
+def test_short_windows_of_many_sequences(cuda_device, kind, q_type, T, group):
+    """As many items as blocks, nearly: none is split, some are short."""
+    rng = np.random.default_rng(T)
+    lens = [int(n) for n in rng.integers(T, 1500, 70)]
+    lens[:4] = [T, 1500, 0, T + 500]
+    drafted = [min(n, T) for n in lens]
+    drafted[5], drafted[6] = 0, 1
+    s = Setup(lens, drafted, T, 2, group, 64, 64, q_type, kind, seed=T)
+    window, sinks = 500, 6
+    o, lse = s.run(window=window, sinks=sinks)
+    for b in [0, 1, 2, 3, 5, 6, *range(7, 70, 8)]:
+        context = lens[b] - drafted[b]
+        assert (o[b, drafted[b]:] == 0).all() and (lse[b, drafted[b]:] == -math.inf).all()
+        for t in range(0, drafted[b], 3):
+            at = torch.tensor([j for j in range(lens[b]) if drafted_reference.sees(
+                j, context, s.masks[b][t] & (1 << drafted[b]) - 1, window, sinks)])
+            ids = s.table[b, at // 64].long()
+            for h in range(2):
+                k, v = (x[ids, h, at % 64] for x in (s.cache.k_values, s.cache.v_values))
+                r = slice(h * group, (h + 1) * group)
+                want = drafted_reference.ref.attend(s.q[b, t, r].double(), k, v, s.scale)
+                check_tree(o[b, t, r], lse[b, t, r], *want, what=f"{b} {t} {h}")
+
+
 def test_masks_that_are_no_trees(cuda_device):
     """Rows that see nothing, only others, everything; bits from draft_lens on."""
     full = (1 << 64) - 1
