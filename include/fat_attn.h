@@ -544,7 +544,8 @@ int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const
  * seq_lens[b] below draft_lens[b] sets FAT_ERR_INDEX.
  * workspace: at least fat_attn_tree_workspace_bytes(...) bytes, 16-byte aligned, any
  * contents; calls sharing it must not overlap on the device.  o, lse and workspace share no
- * memory with the inputs.
+ * memory with the inputs.  Sums are taken in an order that sizes set (the table's width among
+ * them), never timing: equal calls give equal bits.
  */
 #define FAT_TREE_TOKENS 64
 int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,

@@ -1533,8 +1533,9 @@ int launch(const KernelParams& kp, int dev, int sms, cudaStream_t stream) {
                        p.window > 0 ? (p.window < (1 << 30) ? p.window : 1 << 30) + p.tokens : 0,
                        p.sinks, kTreeTile);
   long long grid = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
-  if (items <= grid && (tiles <= kTreeDirect || (p.window > 0 && tiles <= kTreeWhole &&
-                                                 tiles * (grid - items) <= 6 * grid))) {
+  if (items <= grid &&
+      (tiles <= kTreeDirect || (tiles <= (p.window > 0 ? kTreeWholeWindow : kTreeWhole) &&
+                                tiles * (grid - items) <= 6 * grid))) {
     KernelParams one = kp;
     one.p.direct = 1;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(items)), kThreads, L::kBytes, stream,

@@ -15,6 +15,17 @@ from paged_helpers import TYPES, Cache, make_table, pages_for, ref
 pytestmark = pytest.mark.gpu
 
 
+WIDE = False
+
+
+@pytest.fixture(params=[False, True], ids=["table", "long_table"], autouse=True)
+def table_length(request):
+    """A table for the sequences, whose items are mostly not split, and one for 3400 positions more,
+    where they are."""
+    global WIDE
+    WIDE = request.param
+
+
 class Drafted:
     """Sequences whose keys and values [tokens, heads, d] kv_cache_write has stored."""
 
@@ -22,7 +33,8 @@ class Drafted:
         self.lens, self.T, self.q = lens, T, q
         heads, d = k.shape[1:]
         self.cache = Cache(pages_for(lens, page_size), heads, page_size, d, kind, seed=seed)
-        self.table = make_table(lens, page_size, self.cache.k.shape[0], seed=seed)
+        width = max(-(-n // page_size) for n in lens) + (-(-3400 // page_size) if WIDE else 0)
+        self.table = make_table(lens, page_size, self.cache.k.shape[0], seed=seed, width=width)
         slots = torch.cat([self.table[b, torch.arange(n) // page_size].long() * page_size
                            + torch.arange(n) % page_size for b, n in enumerate(lens)])
         fat.kv_cache_write(k.cuda(), v.cuda(), self.cache.k, self.cache.v, slots.cuda(),
@@ -354,7 +366,8 @@ class Step:
         B, room = 3, [n + T + 2 for n in self.context]
         self.cache = Cache(pages_for(room, ps), H, ps, d, kind, seed=seed)
         self.first = [x.clone() for x in self.tensors()]
-        table = make_table(room, ps, self.cache.k.shape[0], seed=seed)
+        width = max(-(-n // ps) for n in room) + (-(-3400 // ps) if WIDE else 0)
+        table = make_table(room, ps, self.cache.k.shape[0], seed=seed, width=width)
         slots = [int(table[b, j // ps]) * ps + j % ps for b, n in enumerate(self.context)
                  for j in range(n, n + T)]
         dev = lambda x, t=None: torch.as_tensor(x, dtype=t).cuda()

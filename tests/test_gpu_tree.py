@@ -13,6 +13,17 @@ from paged_helpers import BEHIND, TYPES, Cache, make_table, pages_for
 pytestmark = pytest.mark.gpu
 
 
+WIDE = False
+
+
+@pytest.fixture(params=[False, True], ids=["table", "long_table"], autouse=True)
+def table_length(request):
+    """A table for a little more than the sequences, whose items are mostly not split, and one for
+    3400 positions more, where they are."""
+    global WIDE
+    WIDE = request.param
+
+
 class Setup:
     def __init__(self, lens, drafted, T, heads, group, page_size, d, q_type, kind, layout="phtd",
                  seed=0, masks=None, spread=0, width=None):
@@ -21,6 +32,8 @@ class Setup:
                            seed=seed, spread=spread)
         if width is None:
             width = max(1, max(-(-n // page_size) for n in lens)) + 2
+            if WIDE:
+                width += -(-3400 // page_size)
         self.table = make_table(lens, page_size, self.cache.k.shape[0], seed=seed, width=width)
         g = torch.Generator().manual_seed(seed + 9)
         self.q = torch.randn((len(lens), T, heads * group, d), generator=g).to(TYPES[q_type])
@@ -133,6 +146,28 @@ def test_short_windows_of_many_sequences(cuda_device, kind, q_type, T, group):
                 r = slice(h * group, (h + 1) * group)
                 want = drafted_reference.ref.attend(s.q[b, t, r].double(), k, v, s.scale)
                 check_tree(o[b, t, r], lse[b, t, r], *want, what=f"{b} {t} {h}")
+
+
+@pytest.mark.parametrize("kind,q_type,T,group", [("bf16", "bf16", 5, 2), ("e4m3", "bf16", 7, 3),
+                                                 ("fp16", "fp16", 40, 4), ("e4m3", "fp16", 60, 2)])
+def test_longer_windows(cuda_device, kind, q_type, T, group):
+    """Windows of several tiles of a few sequences: items are split, at any tile."""
+    lens = [1500, 5000, T + 1290, T, 2600]
+    drafted = [T, T - 1, T, T, T]
+    s = Setup(lens, drafted, T, 2, group, 16, 64, q_type, kind, seed=T)
+    for window, sinks in ((1200, 130), (1003, 0), (2500, 300)):
+        o, lse = s.run(window=window, sinks=sinks)
+        for b, n in enumerate(lens):
+            context = n - drafted[b]
+            for t in range(0, drafted[b], 2):
+                at = torch.tensor([j for j in range(n) if drafted_reference.sees(
+                    j, context, s.masks[b][t] & (1 << drafted[b]) - 1, window, sinks)])
+                ids = s.table[b, at // 16].long()
+                for h in range(2):
+                    k, v = (x[ids, h, at % 16] for x in (s.cache.k_values, s.cache.v_values))
+                    r = slice(h * group, (h + 1) * group)
+                    want = drafted_reference.ref.attend(s.q[b, t, r].double(), k, v, s.scale)
+                    check_tree(o[b, t, r], lse[b, t, r], *want, what=f"{window} {b} {t} {h}")
 
 
 def test_masks_that_are_no_trees(cuda_device):
