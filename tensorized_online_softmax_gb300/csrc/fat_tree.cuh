@@ -4,6 +4,7 @@
 
 #include "fat_cache.cuh"
 #include "fat_decode_plan.h"
+#include "fat_tree_sync.h"
 
 namespace fat {
 

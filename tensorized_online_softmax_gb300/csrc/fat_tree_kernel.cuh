@@ -132,6 +132,7 @@ struct Layout {
   // buffers of Q, stages of K and V, and of an e4m3 cache's codes: what the shared memory has
   // room for
   static constexpr int kQBufs = !kE4M3 && (kNB == 1 || D == 64) ? 2 : 1;
+  static constexpr int kQBars = kE4M3 ? kTreeQueryBars : kQBufs;
   static constexpr int kKStages = kE4M3 || D == 128 ? 2 : kNB == 1 ? 5 : 4;
   static constexpr int kStages = kE4M3 ? 2 : D == 128 ? 3 : kNB == 1 ? 6 : 5;
   static constexpr int kRawStages = !kE4M3 ? 0 : D == 64 ? 12 : 4;
@@ -155,8 +156,8 @@ struct Layout {
   static constexpr int bSFull = bRawEmpty + kRawStages;  // [2]
   static constexpr int bPFull = bSFull + 2;              // [2], the group's warps
   static constexpr int bPV = bPFull + 2;                 // [2]
-  static constexpr int bQFull = bPV + 2;                 // [kQBufs]; e4m3: the softmax warps
-  static constexpr int bQFree = bQFull + kQBufs;         // [kQBufs]
+  static constexpr int bQFull = bPV + 2;                 // [kQBars]; e4m3: the softmax warps
+  static constexpr int bQFree = bQFull + kQBars;         // [kQBufs]
   static constexpr int bSync = bQFree + kQBufs;          // all softmax warps are here
   static constexpr int bVType = bSync + 1;               // [4] (e4m3) a tile's type of V is known
   static constexpr int bDrain = bVType + (kE4M3 ? 4 : 0);
@@ -166,7 +167,7 @@ struct Layout {
                   (bar >= bRawEmpty && bar < bSFull)))
       return kConvertWarps / 4;
     if (bar == bPFull || bar == bPFull + 1) return kSoftWarps<kType> / 2;
-    if (bar == bSync || (kE4M3 && bar == bQFull)) return kSoftWarps<kType>;
+    if (bar == bSync || (kE4M3 && bar >= bQFull && bar < bQFree)) return kSoftWarps<kType>;
     return 1;
   }
   static constexpr int kMisc = kBars + ((8 * kNumBars + 15) & ~15);
@@ -694,7 +695,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         const int tiles = min(count - i, w.at.tiles - w.at.tile);
         if (!w.empty()) {
           const int units = tiles * kNB, buf = items % L::kQBufs;
-          if (!(ok = wait(L::bQFull + buf, items / L::kQBufs & 1))) break;
+          ok = kE4M3 ? wait(L::bQFull + tree_query_bar(items), tree_query_parity(items))
+                     : wait(L::bQFull + buf, items / L::kQBufs & 1);
+          if (!ok) break;
           ++items;
           if constexpr (kE4M3) idesc_s = kIdescS | (misc[2] ? kFmtBits : 0u);
           ok = issue_s(0, buf);
@@ -770,10 +773,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           }
         }
         const bool out_of_range = __any_sync(0xffffffffu, off != 0);
-        if (!is_v) {  // the item's keys follow its queries' type
-          bool ok = true;
-          for (; ok && items != items_now; ++items) ok = wait(L::bQFull, items & 1);
-          if (!ok) break;
+        if (!is_v && items != items_now) {  // the item's keys follow its queries' type
+          items = items_now;
+          if (!wait(L::bQFull + tree_query_bar(items - 1), tree_query_parity(items - 1))) break;
           wide = misc[2] != 0;
         }
         // What tile n is, four deep, so once tile n - 4 has its weights.  Of V early, as the
@@ -872,7 +874,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       float* mine_s = sums + g * kTreeBlockRows + r;
       uint32_t s_phase = 0;  // of bSFull[g] and bPV[g]: both complete once a tile of the group
       uint32_t sync_phase = 0;
-      int tile_count = 0, v_slot = 0, parity = 0;
+      int tile_count = 0, v_slot = 0;
+      int parity = 0;  // of the items so far (tree_query_bar)
       uint32_t v_phase = 0;
       auto step = [&]() {
         if (++v_slot == SV) v_slot = 0, v_phase ^= 1u;
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             }
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::bQFull));
+            if (lane == 0) mbar_arrive(bar(L::bQFull + parity));
           }
         }
         TreeRow seen;
