@@ -176,9 +176,12 @@ struct Layout {
   // last four tiles whether their keys are codes; u64 bad[2 parities][2] at 12
   static constexpr int kBad = kMisc + 48;
   // float: the references [2 groups][128] and the sums [2][128] of the rows; the threads of a row
-  // exchange their maxima in the latter.  Ahead of that the plan's sums and the first place.
+  // exchange their maxima in the latter.  During the set-up the plan's sums are there.
   static constexpr int kFin = kMisc + 96;
-  static constexpr int kBytes = kFin + 2 * 2 * kTreeBlockRows * 4;
+  // where the block's share starts: every role reads it when it gets there, so nothing else is ever
+  // put in its place
+  static constexpr int kStart = kFin + 2 * 2 * kTreeBlockRows * 4;
+  static constexpr int kBytes = kStart + static_cast<int>(sizeof(DecodePlace));
   static_assert(kRawStages % 4 == 0, "K's and V's codes of two teams in turn");
   static_assert(!kE4M3 || kNB == 1, "one block of rows where the codes need room");
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kRaw % 1024 == 0, "tiles on 1 KB");
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
   // what some rows see and is not finite: drafted tokens and border positions, by item parity
   unsigned long long* bad_s = reinterpret_cast<unsigned long long*>(smem + L::kBad);
   float* fin = reinterpret_cast<float*>(smem + L::kFin);
-  DecodePlace* start_s = reinterpret_cast<DecodePlace*>(fin + 2 * kTreeBlockRows);
+  DecodePlace* start_s = reinterpret_cast<DecodePlace*>(smem + L::kStart);
   auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8 * i; };
   auto wait = [&](int i, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait_suspended(bar(i), parity, p, abort_flag));
@@ -388,7 +391,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     count = tree_span(p, tree_lens(p, e)).tiles;
   } else {
     long long* sums = reinterpret_cast<long long*>(fin);  // [warps][units, tiles]
-    long long* ends = reinterpret_cast<long long*>(start_s + 1);  // tiles up to begin, and to end
+    long long* ends = sums + 2 * kWarps;  // tiles up to begin, and to end
+    static_assert((2 * kWarps + 3) * 8 <= L::kStart - L::kFin, "the plan's sums");
     const int each = (p.t.batch + kThreads - 1) / kThreads;
     const int lo = min(p.t.batch, static_cast<int>(threadIdx.x) * each);
     const int hi = min(p.t.batch, lo + each);

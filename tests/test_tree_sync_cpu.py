@@ -246,3 +246,45 @@ def test_the_walk_finds_a_rule_that_stops(harness):
     with longer ones it does not."""
     assert harness(1, 12, [[1] * 12])[1] > 0
     assert harness(1, 12, [[2] * 6, [3, 2, 4]])[1:] == (0, 0)
+
+
+LAYOUTS = r"""
+#include <cstdio>
+#include "fat_tree_kernel.cuh"
+using namespace fat;
+using namespace fat::tree;
+template <int D, int kType, int kNB>
+int check() {
+  using L = Layout<D, kType, kNB>;
+  // in order, each behind the end of the one ahead of it
+  const int at[] = {L::kQ, L::kK, L::kV, L::kRaw, L::kScales, L::kInfo, L::kBars, L::kMisc, L::kFin,
+                    L::kStart, L::kBytes};
+  const int size[] = {L::kQBufs * kNB * L::kTile, L::kKStages * L::kTile, L::kStages * L::kTile,
+                      L::kRawStages * L::kRawTile, L::kRawStages * kTreeTile, L::kRawStages * 8,
+                      8 * L::kNumBars, 96, 4 * kTreeBlockRows * 4,
+                      static_cast<int>(sizeof(DecodePlace)), 0};
+  for (int i = 0; i < 10; ++i)
+    if (at[i] + size[i] > at[i + 1]) return 1;
+  return L::kBytes > 227 * 1024;
+}
+int main() {
+  int bad = check<64, kBf16, 1>() + check<64, kBf16, 2>() + check<64, kE4M3Bf16, 1>() +
+            check<128, kBf16, 1>() + check<128, kBf16, 2>() + check<128, kE4M3Bf16, 1>();
+  std::printf("%d\n", bad);
+  return 0;
+}
+"""
+
+
+def test_what_the_roles_share_lies_apart(tmp_path):
+    """The place where a block's share starts, which a late role may read when others are at work,
+    is nobody else's."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("no nvcc")
+    src, exe = tmp_path / "layouts.cu", tmp_path / "layouts"
+    src.write_text(LAYOUTS)
+    subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-I", CSRC,
+                    "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0 and out.stdout == "0\n", out.stdout + out.stderr
