@@ -555,6 +555,17 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
                         float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
                         cudaStream_t stream);
 
+/* The same with a limit of its own, in nanoseconds, for each wait inside the kernel (0: the 4 s of
+ * fat_attn_tree_paged): where one runs out the results are unspecified and
+ * fat_check_device_error returns FAT_ERR_DEVICE_TIMEOUT.  For tests. */
+int fat_attn_tree_paged_ex(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                           int dtype, long long q_batch_stride, long long q_token_stride,
+                           long long q_head_stride, int q_heads, int tokens, const long long* tree,
+                           long long tree_stride, const int* draft_lens, int window, int sinks,
+                           float scale, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, unsigned long long wait_timeout_ns,
+                           cudaStream_t stream);
+
 /* Workspace size for fat_attn_tree_paged (0 for invalid arguments). */
 size_t fat_attn_tree_workspace_bytes(int batch, int tokens, int q_heads, int kv_heads, int d);
 

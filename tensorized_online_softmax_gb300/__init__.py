@@ -65,7 +65,8 @@ ABI_SYMBOLS = (
     "fat_kv_write", "fat_kv_read", "fat_attn_decode_paged", "fat_attn_decode_workspace_bytes",
     "fat_kv_block_bounds", "fat_kv_block_scores", "fat_attn_decode_sparse",
     "fat_attn_decode_sparse_workspace_bytes", "fat_attn_decode_window",
-    "fat_kv_append", "fat_attn_tree_paged", "fat_attn_tree_workspace_bytes", "fat_kv_keep",
+    "fat_kv_append", "fat_attn_tree_paged", "fat_attn_tree_paged_ex",
+    "fat_attn_tree_workspace_bytes", "fat_kv_keep",
     "fat_status_string", "fat_check_device_error",
 )
 

@@ -113,6 +113,18 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
                         long long tree_stride, const int* draft_lens, int window, int sinks,
                         float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
                         cudaStream_t stream) {
+  return fat_attn_tree_paged_ex(cache, table, q, dtype, q_batch_stride, q_token_stride,
+                                q_head_stride, q_heads, tokens, tree, tree_stride, draft_lens,
+                                window, sinks, scale, o, lse, workspace, workspace_bytes, 0, stream);
+}
+
+int fat_attn_tree_paged_ex(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
+                           int dtype, long long q_batch_stride, long long q_token_stride,
+                           long long q_head_stride, int q_heads, int tokens, const long long* tree,
+                           long long tree_stride, const int* draft_lens, int window, int sinks,
+                           float scale, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, unsigned long long wait_timeout_ns,
+                           cudaStream_t stream) {
   TreeParams p = {};
   int st = cache_view(cache, true, &p.c);
   if (st == FAT_OK) st = table_view(table, p.c.page_shift, &p.t);
@@ -139,7 +151,7 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
   const int sms = sm_count(dev);
   if (sms < 1) return FAT_ERR_LAUNCH;
   p.error_word = p.t.error_word;
-  p.timeout_ns = 4000000000ull;
+  p.timeout_ns = wait_timeout_ns ? wait_timeout_ns : 4000000000ull;
   p.workspace = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const uint8_t*>(q);
   p.tokens = tokens;

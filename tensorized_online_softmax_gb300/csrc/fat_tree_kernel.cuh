@@ -238,13 +238,14 @@ __device__ __forceinline__ Rows rows_of(const TreeParams& p, int item, int block
 
 // Waits for a phase of a barrier, up to p.timeout_ns; false, with the abort flag set, if it does
 // not come.  Most of a block's warps wait at any time: suspended, so that their polls take no
-// issue slots.
+// issue slots (but for a limit too short for that).
 __device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const TreeParams& p,
                                                volatile uint32_t* abort_flag) {
   constexpr uint32_t kSuspend = 50000;
   if (mbar_test_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_for(bar, parity, kSuspend)) {
+  while (!(p.timeout_ns > kSuspend ? mbar_try_wait_for(bar, parity, kSuspend)
+                                   : mbar_test_wait(bar, parity))) {
     if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
       atomicOr(p.error_word, 1u);
       *abort_flag = 1u;
@@ -589,23 +590,23 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           next_slot();
         }
       }
-      if (!ok) {  // every copy that was issued has to land before the block may end
-        const int each = S / kStep;
-        for (int x = max(0, issued - each); x < issued; ++x)
-          wait_drain(bar(full + slot0 + x % each * kStep), (x / each) & 1);
-      }
+      // Every copy that was issued has to land before the block may end, also where another role
+      // gives up and does not wait for it.
+      const int each = S / kStep;
+#pragma unroll 1
+      for (int x = max(0, issued - each); x < issued; ++x)
+        wait_drain(bar(full + slot0 + x % each * kStep), (x / each) & 1);
       __syncwarp();
     } else if (!kE4M3 && warp == kQWarp) {
       // =================== producer of Q ===================
       const uint32_t block_bytes = p.block_tokens * p.block_heads * 128u;
-      bool ok = true;
       int items = 0;
 #pragma unroll 1
       for (int i = 0; i < count;) {
         if (!w.empty()) {
           const Rows r = rows_of(p, w.at.item, kNB);
           const int buf = items % L::kQBufs;
-          if (!(ok = wait(L::bQFree + buf, (items / L::kQBufs & 1) ^ 1u))) break;
+          if (!wait(L::bQFree + buf, (items / L::kQBufs & 1) ^ 1u)) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(L::bQFull + buf),
                                   kNB * L::kAtoms * block_bytes);
@@ -626,10 +627,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
           if (decode_advance(w.at, copies)) enter(p, w);
         }
       }
-      if (!ok) {
-        for (int x = max(0, items - L::kQBufs); x < items; ++x)
-          wait_drain(bar(L::bQFull + x % L::kQBufs), (x / L::kQBufs) & 1);
-      }
+#pragma unroll 1
+      for (int x = max(0, items - L::kQBufs); x < items; ++x)  // (as K's and V's copies)
+        wait_drain(bar(L::bQFull + x % L::kQBufs), (x / L::kQBufs) & 1);
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // =================== MMA issuer ===================
@@ -885,22 +885,28 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         if (++v_slot == SV) v_slot = 0, v_phase ^= 1u;
         ++tile_count;
       };
-      // all softmax warps are here (and what they wrote to shared memory before is seen)
-      auto sync_all = [&]() -> bool {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bSync));
-        const bool ok = wait(L::bSync, sync_phase);
-        sync_phase ^= 1u;
-        tc_fence_after();
-        return ok;
+      // All softmax warps are here (and what they wrote to shared memory before is seen); false
+      // where a wait has run out.  The warps that share rows go on together or leave together: one
+      // may find the flag that ends waits where the other found the barrier complete, and they meet
+      // at barriers that know no limit.
+      auto sync_all = [&](bool fine) -> bool {
+        if (fine) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::bSync));
+          fine = wait(L::bSync, sync_phase);
+          sync_phase ^= 1u;
+          tc_fence_after();
+        }
+        if constexpr (kH == 2) fine = !named_bar_or(pair, 64, !fine);
+        return fine;
       };
       int i = 0;
       bool ok = true;
       if (threadIdx.x < 4) bad_s[threadIdx.x] = 0;
       if (kE4M3 && threadIdx.x < 4) misc[8 + threadIdx.x] = 0;
       if (kE4M3 && threadIdx.x == 0) misc[2] = 0;
-      ok = sync_all();
+      ok = sync_all(true);
 #pragma unroll 1
       while (ok && i < count) {
         const int tiles = min(count - i, w.at.tiles - w.at.tile);
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                 atomicMax(const_cast<uint32_t*>(misc + 8 + 2 * parity), most);
                 atomicMax(const_cast<uint32_t*>(misc + 9 + 2 * parity), 0xFFFFu - least);
               }
-              if (!(ok = sync_all())) break;
+              if (!(ok = sync_all(true))) break;
               most = misc[8 + 2 * parity] >> 7;  // exponent bytes
               least = (0xFFFFu - misc[9 + 2 * parity] + 1u) >> 7;
               // The largest magnitude goes into [2^14, 2^15): an element keeps all its bits down
@@ -1271,10 +1277,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             *mine_s = sum;
           }
           if (half == 0) refs[g * kTreeBlockRows + r] = base;
-          if (dead || !(ok = sync_all())) {
-            ok = false;
-            break;
-          }
+          if (!(ok = sync_all(!dead))) break;
           sum = *mine_s;
           if constexpr (kNB == 1) {
             // both groups and copies: the largest reference, and what theirs count relative to it
@@ -1336,7 +1339,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
               }
             }
           }
-          if (!(ok = sync_all())) break;
+          if (!(ok = sync_all(true))) break;
         }
         if (copy == 0 && __any_sync(0xffffffffu, there)) {
 #pragma unroll 1
@@ -1421,12 +1424,13 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             parity ^= 1;
             if (threadIdx.x < 2) bad_s[2 * parity + threadIdx.x] = 0;
             if (kE4M3 && threadIdx.x < 2) misc[8 + 2 * parity + threadIdx.x] = 0;
-            if (!(ok = sync_all())) break;  // O is free, and nobody looks at `fin` any more
+            if (!(ok = sync_all(true))) break;  // O is free, and nobody looks at `fin` any more
           }
           w.at.tile = w.at.tiles - 1;
           if (decode_advance(w.at, copies)) enter(p, w);
         }
       }
+      tmem_wait_st();  // (a warp that leaves early may have stores on their way)
       __syncwarp();
     }
     finish();

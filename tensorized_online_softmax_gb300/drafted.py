@@ -41,12 +41,13 @@ _pack_rotation = struct.Struct("@PqqPqqii4ii4x").pack
 
 def declare(lib) -> None:
     """Argument and result types of the entry points used here."""
+    tree = [_P, _P, _P, _I, _L, _L, _L, _I, _I, _P, _L, _P, _I, _I, _F, _P, _P, _P, _Z]
     for name, args, result in (
             ("fat_kv_append", [_P, _P, _P, _L, _L, _I, _P, _P, _I, _L, _L, _L, _L, _P, _I, _P, _P],
              _I),
             ("fat_kv_keep", [_P, _P, _P, _L, _I, _P, _P], _I),
-            ("fat_attn_tree_paged",
-             [_P, _P, _P, _I, _L, _L, _L, _I, _I, _P, _L, _P, _I, _I, _F, _P, _P, _P, _Z, _P], _I),
+            ("fat_attn_tree_paged", [*tree, _P], _I),
+            ("fat_attn_tree_paged_ex", [*tree, ctypes.c_ulonglong, _P], _I),
             ("fat_attn_tree_workspace_bytes", [_I, _I, _I, _I, _I], _Z)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, result
@@ -169,7 +170,8 @@ def attn_tree_workspace_bytes(batch: int, tokens: int, q_heads: int, kv_heads: i
 
 def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: float | None = None, *,
                     draft_lens=None, window: int | None = None, sinks: int = 0, k_scale=None,
-                    v_scale=None, workspace=None, out=None, stream=None):
+                    v_scale=None, workspace=None, out=None, stream=None,
+                    wait_timeout_ns: int = 0):
     """Attention of up to 64 drafted tokens per sequence over its cached positions.
 
     The drafted tokens' keys and values are in the cache already, as the last
@@ -189,7 +191,9 @@ def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: floa
     the values.  Returns ``(o, lse)``: o contiguous of q's shape and
     type, lse fp32 [B, T, q_heads]; rows that see nothing and rows from
     ``draft_lens`` on are zeros and -inf.  ``workspace``: a CUDA uint8 tensor of
-    :func:`attn_tree_workspace_bytes` bytes.
+    :func:`attn_tree_workspace_bytes` bytes.  ``wait_timeout_ns``: a limit for each
+    wait inside the kernel instead of 4 s, for tests; where one runs out the results
+    are unspecified and :func:`check_device_error` returns ``FAT_ERR_DEVICE_TIMEOUT``.
     """
     cache, device, kind, (_, heads, _, d) = _cache(k_cache, v_cache, k_scale, v_scale)
     table, batch, _ = _table(page_table, seq_lens, device)
@@ -223,6 +227,8 @@ def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: floa
         raise ValueError("sinks must be at least 0, below 2^31")
     if sinks and window is None:
         raise ValueError("sinks go with a window")
+    if not 0 <= wait_timeout_ns < 1 << 63:
+        raise ValueError("wait_timeout_ns must be at least 0, below 2^63")
     stream = _given(stream, device)
     if out is None:
         o = _empty(q.shape, q.dtype, device, stream)
@@ -237,13 +243,13 @@ def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: floa
         _tensor("workspace", workspace, (torch.uint8,), 1, device)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    _call("fat_attn_tree_paged", device, cache, table, q.data_ptr(), _WIDE[q.dtype],
+    _call("fat_attn_tree_paged_ex", device, cache, table, q.data_ptr(), _WIDE[q.dtype],
           per_batch if batch > 1 else 0, per_token if tokens > 1 else 0,
           per_head if q_heads > 1 else 0, q_heads, tokens, tree.data_ptr(), tree_stride,
           None if draft_lens is None else draft_lens.data_ptr(),
           0 if window is None else int(window), int(sinks), d ** -0.5 if scale is None else scale,
           o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-          _handle(stream, device))
+          int(wait_timeout_ns), _handle(stream, device))
     return o, lse
 
 
