@@ -533,8 +533,12 @@ int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const
  * Weights are rounded to the operands' type for their product with the values: to bf16
  * for a bf16 cache (2^-8 of each), else to fp16 (2^-11 of each, and 2^-36 of the row's
  * largest); sums and the LSE take them unrounded.  Values of an e4m3 cache whose scale
- * byte is outside 112 .. 134 take part as bf16, their weights as two terms of bf16 (2^-16);
- * beyond 2^112 they may overflow.
+ * byte is outside 112 .. 134 take part as bf16 (lost below 2^-133), their weights as two
+ * terms of bf16 (2^-16).  Weighted values are summed before the sum of the weights divides
+ * them, with weights of up to 2^8 over a bf16 cache and 2^15 over the others: none
+ * overflows as long as the largest magnitude among a row's values, times the positions that it
+ * sees, is below 2^120 over a bf16 cache and 2^113 over an e4m3 cache; beyond that it may
+ * be infinite or NaN.  (An fp16 cache holds none so large.)
  * Tokens of a page, and heads and tokens of q, lie apart (a stride of 0 between several:
  * FAT_ERR_UNSUPPORTED); pages, cached heads and sequences may share memory.
  * 1 <= tokens <= FAT_TREE_TOKENS; tree_stride may be 0 (one tree for all).

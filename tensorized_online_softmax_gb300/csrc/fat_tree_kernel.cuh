@@ -37,12 +37,19 @@
 // the row is not.
 //
 // e4m3 caches: a code times its row's power of two is an fp16 wherever the scale is
-// within 2^-15 .. 2^7, and always a bf16.  Rows become fp16 (one conversion and one
+// within 2^-15 .. 2^7, and a bf16 wherever the product is from 2^-133 to below 2^128 (codes
+// from 2^-9 to 448 and scales from 2^-126 to 2^127 leave that at both ends: what is below
+// is lost, what is above infinite).  Rows become fp16 (one conversion and one
 // multiplication to two codes); the tiles of V with a scale outside that range bf16, and
 // the weights of such a tile two bf16 terms.  bf16 queries become fp16 times a power of two
 // for the item; where that would lose bits (elements more than 31 binades apart), they stay
 // bf16 and so do the item's keys.  Keys with a scale outside the range stay codes, and the
-// scale multiplies their scores.  So nothing is lost in any of them.
+// scale multiplies their scores.  So nothing is lost in any of them within that range.
+//
+// Headroom: O is summed with weights of up to 2^8 (bf16 caches) or 2^15 (2^kShift at the
+// reference, kRaise binades above it) before the row's sum divides it.  So values times
+// the positions that a row sees (as far as their weights come near its largest) have to
+// stay below 2^120 or 2^113, else O overflows where the result would not.
 //
 // Measured (GB300, device time; the rate is of the bytes that have to be read, beside 6783
 // GB/s of a plain copy), d = 128 and 8 cached heads but for the last:
@@ -864,7 +871,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
       // copy takes half of a tile's positions (its weights for the others are 0), with statistics
       // and an O of its own: the softmax takes half as long, and the copies are joined at the
       // item's end (32 sequences of 4096 to 16384, 64 rows: 210 us; a row once: 233).  Not for
-      // 16-bit caches: 0 times an infinite value would be NaN; e4m3 has none.
+      // 16-bit caches: 0 times an infinite value would be NaN; an e4m3 cache has none below the
+      // headroom's end.
       const int rows_of_copy = kE4M3 && p.copies == 2 ? kTreeBlockRows / 2 : kTreeBlockRows;
       const int copy = r / rows_of_copy, row_in = r - copy * rows_of_copy;
       const int pieces = kTreeTile / 16 / kH / (kTreeBlockRows / rows_of_copy);  // of 16 scores

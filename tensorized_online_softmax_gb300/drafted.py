@@ -188,7 +188,9 @@ def attn_tree_paged(q, k_cache, v_cache, page_table, seq_lens, tree, scale: floa
     that lie apart (one that repeats heads or tokens is refused with
     ``FAT_ERR_UNSUPPORTED``); ``scale`` defaults to 1/sqrt(d).  Weights are
     rounded to bf16 for a bf16 cache and to fp16 for the others before they meet
-    the values.  Returns ``(o, lse)``: o contiguous of q's shape and
+    the values (:func:`.attn_decode_paged` carries a second 16-bit term of them);
+    values times the positions that a row sees have to stay below 2^120 over a bf16
+    cache, 2^113 over an e4m3 one.  Returns ``(o, lse)``: o contiguous of q's shape and
     type, lse fp32 [B, T, q_heads]; rows that see nothing and rows from
     ``draft_lens`` on are zeros and -inf.  ``workspace``: a CUDA uint8 tensor of
     :func:`attn_tree_workspace_bytes` bytes.  ``wait_timeout_ns``: a limit for each
