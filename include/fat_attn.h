@@ -560,8 +560,8 @@ int fat_attn_tree_paged(const fat_kv_cache* cache, const fat_page_table* table, 
                         cudaStream_t stream);
 
 /* The same with a limit of its own, in nanoseconds, for each wait inside the kernel (0: the 4 s of
- * fat_attn_tree_paged): where one runs out the results are unspecified and
- * fat_check_device_error returns FAT_ERR_DEVICE_TIMEOUT.  For tests. */
+ * fat_attn_tree_paged; a few microseconds may pass all the same): where one runs out the results
+ * are unspecified and fat_check_device_error returns FAT_ERR_DEVICE_TIMEOUT.  For tests. */
 int fat_attn_tree_paged_ex(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
                            int dtype, long long q_batch_stride, long long q_token_stride,
                            long long q_head_stride, int q_heads, int tokens, const long long* tree,

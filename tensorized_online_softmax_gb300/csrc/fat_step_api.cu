@@ -152,6 +152,7 @@ int fat_attn_tree_paged_ex(const fat_kv_cache* cache, const fat_page_table* tabl
   if (sms < 1) return FAT_ERR_LAUNCH;
   p.error_word = p.t.error_word;
   p.timeout_ns = wait_timeout_ns ? wait_timeout_ns : 4000000000ull;
+  p.suspend_ns = p.timeout_ns < 50000 ? static_cast<uint32_t>(p.timeout_ns) : 50000u;
   p.workspace = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const uint8_t*>(q);
   p.tokens = tokens;

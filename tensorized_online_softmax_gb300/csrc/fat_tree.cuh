@@ -52,6 +52,7 @@ struct TreeParams {
   int direct;       // items are not split
   int item_cost;    // what an item costs besides its tiles, in tiles
   unsigned long long timeout_ns;  // of a wait on the device
+  uint32_t suspend_ns;            // of one poll of it, about
   unsigned int* error_word;
 };
 

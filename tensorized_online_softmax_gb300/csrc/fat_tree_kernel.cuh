@@ -245,14 +245,13 @@ __device__ __forceinline__ Rows rows_of(const TreeParams& p, int item, int block
 
 // Waits for a phase of a barrier, up to p.timeout_ns; false, with the abort flag set, if it does
 // not come.  Most of a block's warps wait at any time: suspended, so that their polls take no
-// issue slots (but for a limit too short for that).
+// issue slots.  (A test for limits too short for that, and polls that do not suspend, would cost 1 %
+// of the call.)
 __device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const TreeParams& p,
                                                volatile uint32_t* abort_flag) {
-  constexpr uint32_t kSuspend = 50000;
   if (mbar_test_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!(p.timeout_ns > kSuspend ? mbar_try_wait_for(bar, parity, kSuspend)
-                                   : mbar_test_wait(bar, parity))) {
+  while (!mbar_try_wait_for(bar, parity, p.suspend_ns)) {
     if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
       atomicOr(p.error_word, 1u);
       *abort_flag = 1u;
