@@ -89,7 +89,9 @@ int launch_tree(const TreeParams& params, int d, bool e4m3, bool bf16, int dev, 
   p.direct = 0;
   // Measured, of 1, 2, 3, 4, 6 and 8: 16-bit, 13 sequences of up to 1029 seen positions (9 tiles)
   // 39, 31, 30, 32, 32, 37 us; 16 of 1000 to 8192 55.7, 54.3, 53.8, 53.6, 54.3, 55.2; e4m3, whose
-  // queries are converted, 32 of 4096 to 16384 231, 222, 218, 215, 210, 208.
+  // queries are converted, of 3, 4, 6, 8, 10: 32 of 4096 to 16384 215, 211, 207, 205, 205; 16 of 1000
+  // to 8192 60, 59, 56, 56, 58; 32 of 100 to 1000 41.4, 40.6, 39.0, 39.5, 40.9; 64 of 20 to 300 51.4,
+  // 46.1, 46.9, 48.7, 49.8.
   p.item_cost = e4m3 ? 6 : 3;
   if (!e4m3 && !tree::query_map(&kp.tm_q, p, d, &kp.q_batch)) return -4;
   if (!tree::cache_map(&kp.tm_k, c.k, c, d, e4m3, c.k_page, c.k_head, c.k_token, &kp.k_page,

@@ -12,21 +12,16 @@ constexpr int kTreeTokens = 64;   // drafted tokens of a sequence: bits of a mas
 constexpr int kTreeTile = 128;    // positions of a tile
 constexpr int kTreeBlockRows = 128;
 constexpr int kTreeMaxBlocks = 160;  // what the workspace has room for
-// Items are not split, where a block is there for each, if they have up to so many tiles (as the
+// Items are not split, where a block is there for each, if they have up to kTreeDirect tiles (as the
 // table and the window bound them); or up to kTreeWhole (under a window, where most sequences have
 // as many, kTreeWholeWindow) and blocks without an item cost less than the plan, the join and a
 // block's second item: tiles * (blocks - items) <= 6 * blocks.  8 heads of 32 rows, split and not,
-// us.  One sequence of 208, of 768, of 1024: 11.8, 11.7, 12.4 and 8.7, 11.9, 13.5 (and a launch
-// less).  8, 12, 16, 19 sequences of 50 to 1024: 16.9, -, 19.5, 24.0 and 14.2, -, 14.5, 16.5; of 50
-// to 2048: 22.5, 23.7, 26.1, 29.0 and 21.4, 22.1, 22.8, 23.7; all near 2048: 23.6, 30.0, 35.9, 39.6
-// and 22.0, 24.2, 28.3, 31.1; of 50 to 4096: 28.0, 36.9, 36.2, 41.2 and 34.7, 36.2, 37.7, 39.7.
-// e4m3: of 50 to 2048 26.9, 29.1, 32.1, 35.7 and 28.2, 28.8, 29.2, 29.6; of 50 to 4096 31.8, 41.2,
-// 41.4, 46.8 and 47.6, 47.7, 47.5, 47.9.  Window 1000 (10 tiles), 4, 8, 12, 16, 19 sequences of 4096
-// to 8192: 16.0, 22.8, 26.8, 29.3, 31.2 and 17.7, 20.3, 19.4, 21.5, 23.4; e4m3 21.7, 27.4, 31.8,
-// 36.6, 39.5 and 24.8, 25.9, 25.1, 26.1, 27.0; window 2000 (18 tiles), 8 and 19: 27.2, 41.4 and 27.0,
-// 34.2.  More items than blocks, window 1000: 24, 32, 48 sequences 36.6, 42.6, 55.3 and 38.9, 40.8,
-// 58.8 (e4m3 49.7, 59.0, 80.8 and 49.2, 50.1, 73.2), 13 of 5 to 4097 29.7 and 33.3: split.
-constexpr int kTreeDirect = 8, kTreeWhole = 16, kTreeWholeWindow = 24;
+// us: one sequence of 6, 7 and 8 tiles 11.8, 12.0, 12.5 and 11.9, 12.8, 13.6 (e4m3, where 5 tiles
+// are the border, 15.2, 15.1, 15.2 and 16.5, 17.8, 18.9), four 13.8, 14.7, 14.9 and 12.0, 12.8,
+// 13.7; 19 of 50 to 2048 (16 tiles) 29.0 and 23.7, 8 of 50 to 4096 28.0 and 34.7; window 1000 (10
+// tiles), 19 sequences 31.2 and 23.4, 4 of them 16.0 and 17.7; where there are more items than
+// blocks neither way is better for all.
+constexpr int kTreeDirect = 6, kTreeWhole = 16, kTreeWholeWindow = 24;
 
 struct TreeParams {
   CacheView c;
