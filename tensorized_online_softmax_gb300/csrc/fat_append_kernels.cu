@@ -43,9 +43,8 @@ __device__ __forceinline__ void pack_chunks(const float (&x)[16], uint4& a, uint
   b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// One row as codes, and its scale byte (the rule of fat_kv_write: the least power
-// of two that brings the largest magnitude to at most 448).  `group` is the mask
-// of the kLanes lanes that hold the row.
+// One row as codes, and its scale byte (row_scale_byte).  `group` is the mask of the
+// kLanes lanes that hold the row.
 template <int kLanes>
 __device__ __forceinline__ void quantise(const float (&x)[16], uint32_t group, uint2& a, uint2& b,
                                          uint32_t& e) {
@@ -54,27 +53,16 @@ __device__ __forceinline__ void quantise(const float (&x)[16], uint32_t group, u
   for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int s = kLanes / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(group, top, s));
-  if (top >= 0x7F800000u) {
-    e = 255u;
-    a = b = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  e = row_scale_byte(top);
+  if (e == 255u) {
+    a = b = make_uint2(kNanCodes, kNanCodes);
     return;
   }
-  int p = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  p = top == 0 ? 127 : max(p, 1);
-  e = static_cast<uint32_t>(p);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - p) << 23);  // exact
+  const float inv = row_scale_inverse(e);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(lo)
-        : "f"(x[4 * i + 1] * inv), "f"(x[4 * i] * inv));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(hi)
-        : "f"(x[4 * i + 3] * inv), "f"(x[4 * i + 2] * inv));
-    w[i] = lo | (static_cast<uint32_t>(hi) << 16);
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = codes_of(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], inv);
   a = make_uint2(w[0], w[1]);
   b = make_uint2(w[2], w[3]);
 }

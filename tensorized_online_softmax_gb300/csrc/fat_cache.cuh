@@ -84,6 +84,28 @@ __device__ __forceinline__ float scale_value(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7FFFFFFFu : e << 23);
 }
 
+// The rule by which rows become e4m3, whoever writes them.  The scale byte, of the largest magnitude's
+// fp32 bits: that magnitude is m 2^E, 1 <= m < 2, and 448 = 1.75 2^8, so the least power of two s
+// with amax / s <= 448 is 2^(E - 8), or 2^(E - 7) if m > 1.75.  A row below 2^-118 keeps s = 2^-126
+// (its byte is 1), a row of zeros has 1, one with an inf or NaN the byte 255.
+__device__ __forceinline__ uint32_t row_scale_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return 255u;
+  const int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(top == 0 ? 127 : max(b, 1));
+}
+// What the row's elements are multiplied by (exact).
+__device__ __forceinline__ float row_scale_inverse(uint32_t e) {
+  return __uint_as_float((254u - e) << 23);
+}
+// Four elements, scaled, as codes; of a row that holds an inf or NaN all are kNanCodes.
+constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float x2, float x3, float inv) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1 * inv), "f"(x0 * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3 * inv), "f"(x2 * inv));
+  return lo | (static_cast<uint32_t>(hi) << 16);
+}
+
 // four e4m3 codes -> four fp16 (exact; a NaN code becomes NaN)
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"

@@ -25,11 +25,7 @@ constexpr int kPieces = kE4M3 ? 2 : 1;
 // ---------------------------------------------------------------------------
 
 // Two pieces of one row's lane as 16-bit values -> as codes, and the row's scale
-// byte.  kLanes lanes hold the row (a power of two, adjacent).
-//
-// The scale: the largest magnitude is m 2^E, 1 <= m < 2, and 448 = 1.75 2^8,
-// so the least power of two s with amax / s <= 448 is 2^(E - 8), or 2^(E - 7)
-// if m > 1.75.  A row below 2^-118 keeps s = 2^-126 (its byte is 1).
+// byte (row_scale_byte).  kLanes lanes hold the row (a power of two, adjacent).
 template <int kLanes, bool kBf16>
 __device__ __forceinline__ void quantise_row(const uint4 (&x)[2], uint2 (&code)[2], uint32_t& e) {
   const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -41,28 +37,17 @@ __device__ __forceinline__ void quantise_row(const uint4 (&x)[2], uint2 (&code)[
   for (int s = kLanes / 2; s > 0; s >>= 1)
     two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, s));
   const uint32_t most = max(two >> 16, two & 0xFFFFu);
-  if (most >= (kBf16 ? 0x7F80u : 0x7C00u)) {
-    e = 255u;
-    code[0] = code[1] = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  e = row_scale_byte(__float_as_uint(unpack16<kBf16>(most).x));
+  if (e == 255u) {
+    code[0] = code[1] = make_uint2(kNanCodes, kNanCodes);
     return;
   }
-  const uint32_t top = __float_as_uint(unpack16<kBf16>(most).x);
-  int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  b = top == 0 ? 127 : max(b, 1);
-  e = static_cast<uint32_t>(b);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // exact
+  const float inv = row_scale_inverse(e);
   uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint16_t c[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 f = unpack16<kBf16>(w[2 * i + j]);
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-          : "=h"(c[j])
-          : "f"(f.y * inv), "f"(f.x * inv));
-    }
-    h[i] = c[0] | (static_cast<uint32_t>(c[1]) << 16);
+    const float2 a = unpack16<kBf16>(w[2 * i]), b = unpack16<kBf16>(w[2 * i + 1]);
+    h[i] = codes_of(a.x, a.y, b.x, b.y, inv);
   }
   code[0] = make_uint2(h[0], h[1]);
   code[1] = make_uint2(h[2], h[3]);
