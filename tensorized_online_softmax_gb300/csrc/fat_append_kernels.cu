@@ -6,8 +6,11 @@
 //
 // Measured on a GB300, on the device: prompts of 1000 to 8192 tokens, 48 heads of
 // 128, bf16, positions of three axes (764 MB in and out): 122 us, 0.92 of the copy
-// rate; 16 single tokens into an e4m3 cache and back: 4.6 us for both kernels; 64
-// sequences of 64 drafted tokens stored and up to 64 of them kept: 20.6 us, 0.75.
+// rate; the same with one axis in fp16 117 us, 0.96; into an e4m3 cache 149 (63 MB
+// less to write; the conversion's instructions), three axes 168; 16 single tokens
+// into an e4m3 cache and back: 4.6 us for both kernels; 64 sequences of 64 drafted
+// tokens stored and up to 12 of them kept: 19.5 us, 0.80; keeping alone, 8 heads: up to
+// 12 of 64 3.4 us, 32 4.9, 60 (31 MB) 7.2, in an e4m3 cache 3.5, 4.0, 4.9.
 //
 // Rotation: for pair i of a row, with (c, s) the table's cosine and sine at the
 // token's position,  y_a = x_a c - x_b s,  y_b = x_b c + x_a s.  Products and sums
@@ -208,11 +211,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 // keep
 // ---------------------------------------------------------------------------
 
-// A block takes the rows of one (sequence, head), K or V (a thread with 16 bytes of every row:
-// 23 us for the 64 sequences above): a wave of them is in registers before any is stored.  As the path rises, a wave's rows come from its first place on or behind it, where
-// no earlier wave has written: so only a wave's own loads and stores are held apart.
+// A block takes the rows of one (sequence, head), K or V, each thread 16 bytes of a row: a wave of
+// rows is in registers before any is stored.  (Waves of 1, 2, 4 and 8 rows to a thread, the 64
+// sequences above with up to 12, 32 and 60 kept: 3.4, 3.4, 4.0, 5.5 us, 5.1, 4.9, 5.4, 7.2 and 7.8,
+// 7.2, 7.9, 10.3; e4m3 with 60 5.3, 4.9, 5.7, 7.5.)  As the path rises, a wave's rows come from its first place on or behind it, where no earlier wave has
+// written: so only a wave's own loads and stores are held apart.
 __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const KeepParams p) {
-  constexpr int kDeep = 4;
+  constexpr int kDeep = 2;
   const int each = kThreads / p.chunks;  // rows at a time, 16 bytes to a thread
   const int row0 = threadIdx.x / p.chunks, chunk = threadIdx.x - row0 * p.chunks;
   const bool is_v = blockIdx.x & 1;
