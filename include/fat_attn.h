@@ -389,7 +389,10 @@ int fat_kv_read(const fat_kv_cache* cache, const fat_page_table* table, void* k,
  * own rounding.  With scales as fat_kv_write sets them that is far below an
  * output's rounding, unless a column is (nearly) zero in the rows that dominate.
  * An infinite value of an fp16 cache gives NaN where its weight is below 2^-34
- * of the largest.
+ * of the largest.  Over a bf16 cache weighted values are summed with weights of up
+ * to 2^8 before the sum of the weights divides them: none overflows as long as the
+ * largest magnitude among the values seen, times their positions, is below 2^120;
+ * beyond that a result may be infinite or NaN.
  */
 #define FAT_DECODE_DIRECT 512
 int fat_attn_decode_paged(const fat_kv_cache* cache, const fat_page_table* table, const void* q,
@@ -538,7 +541,8 @@ int fat_kv_append(const fat_kv_cache* cache, const fat_rotation* rotation, const
  * them, with weights of up to 2^8 over a bf16 cache and 2^15 over the others: none
  * overflows as long as the largest magnitude among a row's values, times the positions that it
  * sees, is below 2^120 over a bf16 cache and 2^113 over an e4m3 cache; beyond that it may
- * be infinite or NaN.  (An fp16 cache holds none so large.)
+ * be infinite or NaN.  (An fp16 cache holds none so large; an infinite value of it gives
+ * NaN where its weight is below 2^-36 of the row's largest.)
  * Tokens of a page, and heads and tokens of q, lie apart (a stride of 0 between several:
  * FAT_ERR_UNSUPPORTED); pages, cached heads and sequences may share memory.
  * 1 <= tokens <= FAT_TREE_TOKENS; tree_stride may be 0 (one tree for all).

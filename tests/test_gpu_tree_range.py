@@ -1,5 +1,6 @@
-"""Attention of drafted tokens over values near the largest that it takes: the largest magnitude
-times the positions that a row sees just below 2^120 over a bf16 cache, 2^113 over an e4m3 one."""
+"""Attention of drafted tokens, and of single ones, over values near the largest that it takes: the
+largest magnitude times the positions that a row sees just below 2^120 over a bf16 cache, 2^113 over
+an e4m3 one."""
 import math
 
 import numpy as np
@@ -9,7 +10,7 @@ import torch
 import drafted_reference
 import tensorized_online_softmax_gb300 as fat
 from drafted_helpers import as_tensor, check_tree
-from paged_helpers import Cache, make_table, pages_for
+from paged_helpers import Cache, check_attention, make_table, pages_for
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +62,14 @@ def test_values_up_to_the_headroom(cuda_device, kind, T, group, d, signs, more):
         return x if not scales else x * 2.0 ** (scales[name].cpu().double() - 127)[..., None]
     kk, vv = held(kc, "k_scale"), held(vc, "v_scale")
     assert 0.4 * 2.0 ** limit < n * vv[table[0, 5].long()].abs().max() < 2.0 ** limit
-    want = drafted_reference.tree(q.double(), kk, vv, table, [n], [T], masks, page_size,
-                                  float(np.float32(d ** -0.5)))
+    scale = float(np.float32(d ** -0.5))
+    want = drafted_reference.tree(q.double(), kk, vv, table, [n], [T], masks, page_size, scale)
     check_tree(o, lse, *want, what=f"{kind} {T} {group} {d}")
+    if kind == "bf16":  # single tokens: the same headroom
+        lens = torch.tensor([n], dtype=torch.int32).cuda()
+        for got, window in ((fat.attn_decode_paged(q[:, 0].cuda(), kc, vc, table.cuda(), lens), n),
+                            (fat.attn_decode_window(q[:, 0].cuda(), kc, vc, table.cuda(), lens,
+                                                    800, 20), 800)):
+            want = drafted_reference.window(q[:, 0].double(), kk, vv, table, [n], page_size, scale,
+                                            window, 20)
+            check_attention(*got, *want, what=f"window {window}")
