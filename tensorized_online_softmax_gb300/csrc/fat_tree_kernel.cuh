@@ -59,7 +59,7 @@
 // GB/s of a plain copy), d = 128 and 8 cached heads but for the last:
 //   16 sequences of 1000 to 8192, 64 rows a head, bf16          54 us   4.7 TB/s
 //   8 of 4096 to 16384, 256 rows, bf16                          88 us   4.0 TB/s
-//   32 of 4096 to 16384, 64 rows, e4m3                         210 us   3.6 TB/s
+//   32 of 4096 to 16384, 64 rows, e4m3                         208 us   3.6 TB/s
 //   1 of 208, 32 rows, bf16                                    8.7 us
 //   13 of 5 to 4097 under a window of 1024, 20 heads of 5 rows, d = 64, fp16   30 us  2.0 TB/s
 // 64 rows over a 16-bit cache stream at the copy rate (2.8 k clocks a tile) between a start
